@@ -67,8 +67,9 @@ typedef enum {
                               /* MSEL_MAX_SEQLEN, batch*dim up to 2^30)                     */
     MSEL_ERR_DTYPE = 3,       /* dtype is not MSEL_F32 / MSEL_BF16, or a 0/1 flag is not 0/1 */
     MSEL_ERR_ALIGN = 4,       /* an activation pointer is not 16-byte aligned              */
-    MSEL_ERR_UNSUPPORTED = 5, /* dstate outside 1..MSEL_MAX_DSTATE, or a convolution width  */
-                              /* outside 1..MSEL_MAX_CONV_WIDTH                             */
+    MSEL_ERR_UNSUPPORTED = 5, /* dstate outside 1..MSEL_MAX_DSTATE, a convolution width     */
+                              /* outside 1..MSEL_MAX_CONV_WIDTH, a normed or embedded width */
+                              /* above MSEL_MAX_NORM_DIM, or an unsupported layout pair     */
     MSEL_ERR_WORKSPACE = 6,   /* workspace NULL or smaller than msel_scan_bwd_workspace_bytes */
     MSEL_ERR_ALIAS = 7,       /* an output pointer equals an input pointer                 */
     MSEL_ERR_HIP = 8,         /* the HIP runtime reported an error at launch               */
@@ -260,7 +261,8 @@ int msel_checked_build(void);
 /* Waits for the current device to finish its work, then stores the number of out-of-range
  * indexes that the kernels met on that device since the last call in *count and, when the
  * count is nonzero, where the first one was: *file (1 scan_fwd.hip, 2 chunk_carry.hip,
- * 3 scan_bwd.hip, 4 conv1d.hip, 5 scan_cplx.hip, 6 scan_cplx_bwd.hip; the first file with a
+ * 3 scan_bwd.hip, 4 conv1d.hip, 5 scan_cplx.hip, 6 scan_cplx_bwd.hip, 7 row_norm.hip,
+ * 8 tile_norm.hip, 9 tile_norm_bwd.hip, 10 embed.hip, 11 grads.hip; the first file with a
  * nonzero count) and *line (its source line); 0 and 0 otherwise.  Clears the records.  The
  * release build always reports 0.  MSEL_ERR_NULL if a pointer is NULL, MSEL_ERR_HIP if the
  * runtime fails. */
@@ -454,6 +456,210 @@ msel_status msel_conv1d_fwd(const msel_conv_args *args, hipStream_t stream);
  * may differ in the last bits between runs; dx and dstate_in are deterministic. */
 msel_status msel_conv1d_bwd(const msel_conv_args *args, const msel_conv_grads *grads,
                             hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The norms around a block: before it, with the residual sum, and after the scan, with the
+ * gate.  A language model is a stack of blocks on a residual stream (page 3, "a deep sequence
+ * model backbone (with repeating Mamba blocks) + language model head"); each is entered
+ * through an RMS norm, and the scan's output can be normed together with its gate.
+ *
+ * Before a block (msel_norm_fwd), per row of `dim` values:
+ *
+ *   s   = residual + scale * x                 (s = scale * x when residual is NULL)
+ *   out = s * rstd * weight,   rstd = (mean(s^2) + eps)^(-1/2)
+ *   residual_out = s
+ *
+ * Layouts: x, out, dout, dx [rows, dim] in `dtype`; residual, residual_out, s, dresidual_out,
+ * dresidual [rows, dim] in `residual_dtype`; weight, dweight [dim] fp32.  residual_dtype is
+ * dtype or MSEL_F32 (a residual stream kept in fp32 under bf16 blocks).  Activation pointers
+ * are 16-byte aligned; dim need not be a multiple of anything.  Sums and rstd are fp32.
+ * ---------------------------------------------------------------------------------------- */
+#define MSEL_MAX_NORM_DIM 16384
+#define MSEL_MAX_NORM_GROUPS 1024
+
+typedef struct {
+    int32_t abi_version;    /* must be MSEL_ABI_VERSION                                    */
+    int32_t dim;            /* 1..MSEL_MAX_NORM_DIM                                        */
+    int64_t rows;           /* >= 1, rows * dim up to 2^40                                 */
+    int32_t dtype;          /* msel_dtype of x, out, dout, dx                              */
+    int32_t residual_dtype; /* msel_dtype of the residual stream                           */
+    float scale;            /* of x                                                        */
+    float eps;              /* >= 0                                                        */
+    const void *x;          /* fwd: required; ignored by the backward                      */
+    const void *residual;   /* fwd: optional; ignored by the backward                      */
+    const float *weight;    /* optional; NULL means 1                                      */
+    void *out;              /* fwd: required output                                        */
+    void *residual_out;     /* fwd: optional output; may equal residual (updated in place)  */
+} msel_norm_args;
+
+/* Gradients of a scalar loss given dL/dout and dL/dresidual_out.  With g = dout * weight:
+ *   ds        = dresidual_out + rstd * (g - s * rstd^2 * mean(g * s))
+ *   dresidual = ds,   dx = scale * ds,   dweight = sum over rows of dout * s * rstd
+ * Every output is overwritten, not accumulated. */
+typedef struct {
+    const void *s;             /* required: the forward's residual_out                      */
+    const void *dout;          /* required                                                 */
+    const void *dresidual_out; /* optional; NULL means 0                                    */
+    void *dx;                  /* optional output                                          */
+    void *dresidual;           /* optional output; may equal dresidual_out                  */
+    float *dweight;            /* optional output [dim] (also when args->weight is NULL)     */
+} msel_norm_grads;
+
+/* Host-only argument checks of the entry points below (no HIP call, no device access). */
+msel_status msel_validate_norm_fwd(const msel_norm_args *args);
+msel_status msel_validate_norm_bwd(const msel_norm_args *args, const msel_norm_grads *grads,
+                                   const void *workspace, size_t workspace_bytes);
+
+/* One pass over the rows.  Deterministic. */
+msel_status msel_norm_fwd(const msel_norm_args *args, hipStream_t stream);
+
+/* Bytes of workspace msel_norm_bwd needs (partial sums of dweight; 0 for invalid sizes). */
+size_t msel_norm_bwd_workspace_bytes(const msel_norm_args *args);
+
+/* Its backward, recomputing rstd from s: one pass over the rows, and one over the partial sums
+ * of dweight when it is wanted (the workspace may be NULL otherwise).  Deterministic.  The
+ * workspace is 256-byte aligned. */
+msel_status msel_norm_bwd(const msel_norm_args *args, const msel_norm_grads *grads,
+                          void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* After the scan (msel_gated_norm_fwd), over the `dim / groups` channels of each group of a
+ * token, with the gate before the norm (gate_first = 1) or after it (0):
+ *
+ *   gate_first:  v = x * silu(z),  out = v * rstd(v) * weight
+ *   otherwise:   out = x * rstd(x) * weight * silu(z)
+ *
+ * layout says how x, z, dx and dz lie, out_layout how out and dout do: MSEL_BDL is the scan's
+ * [batch, dim, seqlen] (the normed axis is strided), MSEL_BLD [batch, seqlen, dim] (what an
+ * output projection reads).  BDL to BDL, BDL to BLD and BLD to BLD are supported. */
+typedef enum { MSEL_BDL = 0, MSEL_BLD = 1 } msel_layout;
+
+typedef struct {
+    int32_t abi_version;    /* must be MSEL_ABI_VERSION                                    */
+    int32_t batch;          /* >= 1, batch * dim up to 2^30                                 */
+    int32_t dim;            /* channels, >= 1                                              */
+    int32_t seqlen;         /* 1..MSEL_MAX_SEQLEN, batch * seqlen up to 2^30                */
+    int32_t groups;         /* 1..MSEL_MAX_NORM_GROUPS, divides dim; dim / groups up to
+                               MSEL_MAX_NORM_DIM                                           */
+    int32_t dtype;          /* msel_dtype of x, z, out, dout, dx, dz                        */
+    int32_t layout;         /* msel_layout of x, z, dx, dz                                 */
+    int32_t out_layout;     /* msel_layout of out, dout                                    */
+    int32_t gate_first;     /* 1: gate, then norm; 0: norm, then gate                       */
+    float eps;              /* >= 0                                                        */
+    const void *x;          /* required: the scan's ungated output                         */
+    const void *z;          /* required: the gate's input                                  */
+    const float *weight;    /* optional [dim]; NULL means 1                                */
+    void *out;              /* fwd: required output; ignored by the backward               */
+} msel_gated_norm_args;
+
+typedef struct {
+    const void *dout;       /* required                                                    */
+    void *dx;               /* required output                                             */
+    void *dz;               /* required output                                             */
+    float *dweight;         /* optional output [dim] (also when args->weight is NULL)        */
+} msel_gated_norm_grads;
+
+msel_status msel_validate_gated_norm_fwd(const msel_gated_norm_args *args);
+msel_status msel_validate_gated_norm_bwd(const msel_gated_norm_args *args,
+                                         const msel_gated_norm_grads *grads,
+                                         const void *workspace, size_t workspace_bytes);
+
+/* Deterministic. */
+msel_status msel_gated_norm_fwd(const msel_gated_norm_args *args, hipStream_t stream);
+
+/* Bytes of workspace msel_gated_norm_bwd needs (partial sums of dweight; 0 for invalid sizes). */
+size_t msel_gated_norm_bwd_workspace_bytes(const msel_gated_norm_args *args);
+
+/* Its backward, recomputing the gate and rstd from x and z.  Deterministic.  The workspace is
+ * 256-byte aligned and may be NULL when dweight is. */
+msel_status msel_gated_norm_bwd(const msel_gated_norm_args *args,
+                                const msel_gated_norm_grads *grads, void *workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Embedding lookup with a scale, and the table's gradient.
+ *
+ *   out[t]     = scale * weight[ids[t]]
+ *   dweight[v] = base[v] + scale * sum over t with ids[t] = v of dout[t]
+ *
+ * A token outside [0, vocab) reads a row of zeros and gives no gradient; a token equal to
+ * padding_idx gives no gradient.  The gradient sorts the tokens (stable, by id) and adds each
+ * id's rows in an order that the ids alone fix, in fp32: deterministic, no atomics on floats.
+ * Layouts: ids [tokens]; weight [vocab, dim]; out, dout [tokens, dim]; dweight, base
+ * [vocab, dim] fp32.  Table and activation pointers are 16-byte aligned.
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+    int32_t abi_version;    /* must be MSEL_ABI_VERSION                                    */
+    int32_t vocab;          /* >= 1, up to 2^30                                            */
+    int32_t dim;            /* 1..MSEL_MAX_NORM_DIM                                        */
+    int32_t ids_64bit;      /* 1: ids are int64; 0: int32                                   */
+    int64_t tokens;         /* >= 1, up to 2^30                                            */
+    int64_t padding_idx;    /* a token that gives no gradient; negative: none               */
+    int32_t dtype;          /* msel_dtype of out, dout                                     */
+    int32_t weight_dtype;   /* msel_dtype of weight (the forward's)                         */
+    float scale;
+    int32_t reserved;       /* must be 0                                                   */
+    const void *ids;        /* required                                                    */
+    const void *weight;     /* fwd: required; ignored by the backward                      */
+    void *out;              /* fwd: required output; ignored by the backward               */
+} msel_embed_args;
+
+typedef struct {
+    const void *dout;       /* required                                                    */
+    const float *base;      /* optional: the gradient so far; NULL means 0                  */
+    float *dweight;         /* required output; may equal base (added to in place)           */
+} msel_embed_grads;
+
+msel_status msel_validate_embed_fwd(const msel_embed_args *args);
+msel_status msel_validate_embed_bwd(const msel_embed_args *args, const msel_embed_grads *grads,
+                                    const void *workspace, size_t workspace_bytes);
+msel_status msel_embed_fwd(const msel_embed_args *args, hipStream_t stream);
+/* Bytes of workspace msel_embed_bwd needs (0 for invalid sizes). */
+size_t msel_embed_bwd_workspace_bytes(const msel_embed_args *args);
+msel_status msel_embed_bwd(const msel_embed_args *args, const msel_embed_grads *grads,
+                           void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The norm over all gradients of a model, and the gradients scaled to a bound on it.
+ *
+ *   norm   = sqrt(sum over tensors and elements of g^2)
+ *   out_i  = g_i * min(1, max_norm / (norm + eps))
+ *
+ * The sum is fp64: it neither overflows nor loses small tensors.  A norm that is infinite or
+ * not a number scales by 0 or by NaN (the step is spoilt visibly, and norm says so); nothing
+ * is read back, so the host decides from norm when it wants to.  Deterministic.  `tensors` and
+ * `outs` are HOST arrays of `count` entries, read during the call; an entry may have numel 0
+ * (its data is then ignored).  Data pointers are aligned to their element.
+ * ---------------------------------------------------------------------------------------- */
+#define MSEL_MAX_GRAD_TENSORS (1 << 20)
+
+typedef struct {
+    void *data;             /* device pointer                                              */
+    int64_t numel;          /* >= 0, up to 2^40                                            */
+    int32_t dtype;          /* msel_dtype                                                  */
+    int32_t reserved;       /* must be 0                                                   */
+} msel_tensor;
+
+typedef struct {
+    int32_t abi_version;    /* must be MSEL_ABI_VERSION                                    */
+    int32_t count;          /* 0..MSEL_MAX_GRAD_TENSORS                                    */
+    const msel_tensor *tensors; /* required when count > 0                                 */
+    const msel_tensor *outs;/* clip: where each scaled tensor goes, numel and dtype as in
+                               tensors; may equal tensors, or its data the same (in place) */
+    float max_norm;         /* clip: >= 0 (infinity: no bound)                              */
+    float eps;              /* clip: >= 0                                                  */
+    float *norm;            /* required output [1]                                         */
+} msel_grad_args;
+
+msel_status msel_validate_grad_norm(const msel_grad_args *args, const void *workspace,
+                                    size_t workspace_bytes);
+msel_status msel_validate_grad_clip(const msel_grad_args *args, const void *workspace,
+                                    size_t workspace_bytes);
+/* Bytes of workspace the two entry points need (partial sums; 0 for invalid arguments). */
+size_t msel_grad_workspace_bytes(const msel_grad_args *args);
+msel_status msel_grad_norm(const msel_grad_args *args, void *workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+msel_status msel_grad_clip(const msel_grad_args *args, void *workspace, size_t workspace_bytes,
+                           hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -58,6 +58,55 @@ class ConvGrads(ctypes.Structure):
     _fields_ = [("dout", _P), ("dx", _P), ("dweight", _P), ("dbias", _P), ("dstate_in", _P)]
 
 
+class NormArgs(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("x", _P), ("residual", _P), ("weight", _P),
+                ("out", _P), ("residual_out", _P)]
+
+
+class NormGrads(ctypes.Structure):
+    _fields_ = [("s", _P), ("dout", _P), ("dresidual_out", _P), ("dx", _P), ("dresidual", _P),
+                ("dweight", _P)]
+
+
+class GatedNormArgs(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("out_layout", ctypes.c_int32), ("gate_first", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x", _P), ("z", _P), ("weight", _P), ("out", _P)]
+
+
+class GatedNormGrads(ctypes.Structure):
+    _fields_ = [("dout", _P), ("dx", _P), ("dz", _P), ("dweight", _P)]
+
+
+class EmbedArgs(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("ids_64bit", ctypes.c_int32),
+                ("tokens", ctypes.c_int64), ("padding_idx", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("ids", _P),
+                ("weight", _P), ("out", _P)]
+
+
+class EmbedGrads(ctypes.Structure):
+    _fields_ = [("dout", _P), ("base", _P), ("dweight", _P)]
+
+
+class TensorEntry(ctypes.Structure):
+    _fields_ = [("data", _P), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class GradArgs(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("count", ctypes.c_int32),
+                ("tensors", ctypes.POINTER(TensorEntry)), ("outs", ctypes.POINTER(TensorEntry)),
+                ("max_norm", ctypes.c_float), ("eps", ctypes.c_float), ("norm", _P)]
+
+
 class MselError(RuntimeError):
     def __init__(self, fn: str, code: int, text: str):
         super().__init__(f"{fn} returned {STATUS.get(code, code)}: {text}")
@@ -77,7 +126,15 @@ EXPORTS = ["msel_abi_version", "msel_chunk_len", "msel_num_chunks", "msel_status
            "msel_set_ring_spin_limit", "msel_scan_bwd_noalloc", "msel_validate_trap_chunk_carry",
            "msel_scan_trap_chunk_carry", "msel_validate_complex_chunk_carry",
            "msel_scan_complex_chunk_carry", "msel_checked_build", "msel_bound_violations",
-           "msel_bounds_selftest", "msel_scan_bwd_fused", "msel_set_bwd_fused"]
+           "msel_bounds_selftest", "msel_scan_bwd_fused", "msel_set_bwd_fused",
+           "msel_validate_norm_fwd", "msel_validate_norm_bwd", "msel_norm_fwd",
+           "msel_norm_bwd_workspace_bytes", "msel_norm_bwd", "msel_validate_gated_norm_fwd",
+           "msel_validate_gated_norm_bwd", "msel_gated_norm_fwd",
+           "msel_gated_norm_bwd_workspace_bytes", "msel_gated_norm_bwd",
+           "msel_validate_embed_fwd", "msel_validate_embed_bwd", "msel_embed_fwd",
+           "msel_embed_bwd_workspace_bytes", "msel_embed_bwd", "msel_validate_grad_norm",
+           "msel_validate_grad_clip", "msel_grad_workspace_bytes", "msel_grad_norm",
+           "msel_grad_clip"]
 
 
 def default_path() -> str:
@@ -177,6 +234,27 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.msel_scan_bwd_fused.argtypes = [a]
     lib.msel_set_bwd_fused.restype = None
     lib.msel_set_bwd_fused.argtypes = [ctypes.c_int32]
+    for op, args, grads in (("norm", NormArgs, NormGrads),
+                            ("gated_norm", GatedNormArgs, GatedNormGrads),
+                            ("embed", EmbedArgs, EmbedGrads)):
+        pa, pg = ctypes.POINTER(args), ctypes.POINTER(grads)
+        for fn, res, argtypes in (
+                (f"msel_validate_{op}_fwd", ctypes.c_int, [pa]),
+                (f"msel_validate_{op}_bwd", ctypes.c_int, [pa, pg, _P, ctypes.c_size_t]),
+                (f"msel_{op}_fwd", ctypes.c_int, [pa, _P]),
+                (f"msel_{op}_bwd_workspace_bytes", ctypes.c_size_t, [pa]),
+                (f"msel_{op}_bwd", ctypes.c_int, [pa, pg, _P, ctypes.c_size_t, _P])):
+            getattr(lib, fn).restype = res
+            getattr(lib, fn).argtypes = argtypes
+    pn = ctypes.POINTER(GradArgs)
+    lib.msel_grad_workspace_bytes.restype = ctypes.c_size_t
+    lib.msel_grad_workspace_bytes.argtypes = [pn]
+    for fn in ("msel_validate_grad_norm", "msel_validate_grad_clip"):
+        getattr(lib, fn).restype = ctypes.c_int
+        getattr(lib, fn).argtypes = [pn, _P, ctypes.c_size_t]
+    for fn in ("msel_grad_norm", "msel_grad_clip"):
+        getattr(lib, fn).restype = ctypes.c_int
+        getattr(lib, fn).argtypes = [pn, _P, ctypes.c_size_t, _P]
     if lib.msel_abi_version() != ABI_VERSION:
         raise RuntimeError("libmsel.so ABI version mismatch")
     if path is None:

@@ -14,6 +14,16 @@
 #include "msel.h"  // include/ is on the include path
 #include "msel_kernels.hpp"
 
+namespace msel {
+// The operators around the scan are sources of their own (lm_kernels.hpp), which a build of the
+// scan alone leaves out: weak, so that their records are read where they are linked in.
+__attribute__((weak)) hipError_t take_bounds_row_norm(BoundsRecord* r);
+__attribute__((weak)) hipError_t take_bounds_tile_norm(BoundsRecord* r);
+__attribute__((weak)) hipError_t take_bounds_tile_norm_bwd(BoundsRecord* r);
+__attribute__((weak)) hipError_t take_bounds_embed(BoundsRecord* r);
+__attribute__((weak)) hipError_t take_bounds_grads(BoundsRecord* r);
+}  // namespace msel
+
 static_assert(MSEL_MAX_DSTATE == msel::kMaxN, "the kernels' state limit is the boundary's");
 
 namespace {
@@ -209,7 +219,8 @@ const char* msel_status_string(msel_status s) {
         case MSEL_ERR_SHAPE: return "MSEL_ERR_SHAPE: a size is out of range";
         case MSEL_ERR_DTYPE: return "MSEL_ERR_DTYPE: unknown dtype or softplus flag";
         case MSEL_ERR_ALIGN: return "MSEL_ERR_ALIGN: a pointer is not aligned";
-        case MSEL_ERR_UNSUPPORTED: return "MSEL_ERR_UNSUPPORTED: dstate above MSEL_MAX_DSTATE";
+        case MSEL_ERR_UNSUPPORTED:
+            return "MSEL_ERR_UNSUPPORTED: a width above its limit, or an unsupported layout pair";
         case MSEL_ERR_WORKSPACE: return "MSEL_ERR_WORKSPACE: workspace missing or too small";
         case MSEL_ERR_ALIAS: return "MSEL_ERR_ALIAS: an output aliases an input";
         case MSEL_ERR_HIP: return "MSEL_ERR_HIP: the HIP runtime reported an error";
@@ -610,12 +621,16 @@ msel_status msel_bound_violations(unsigned long long* count, uint32_t* file, uin
     if (hipDeviceSynchronize() != hipSuccess) return MSEL_ERR_HIP;
     using Taker = hipError_t (*)(msel::BoundsRecord*);
     // in the order of the file numbers of msel.h
-    const Taker takers[] = {msel::take_bounds_fwd,  msel::take_bounds_chunk_carry,
-                            msel::take_bounds_bwd,  msel::take_bounds_conv,
-                            msel::take_bounds_cplx, msel::take_bounds_cplx_bwd};
+    const Taker takers[] = {msel::take_bounds_fwd,       msel::take_bounds_chunk_carry,
+                            msel::take_bounds_bwd,       msel::take_bounds_conv,
+                            msel::take_bounds_cplx,      msel::take_bounds_cplx_bwd,
+                            msel::take_bounds_row_norm,  msel::take_bounds_tile_norm,
+                            msel::take_bounds_tile_norm_bwd, msel::take_bounds_embed,
+                            msel::take_bounds_grads};
     msel_status s = MSEL_OK;
     for (uint32_t i = 0; i < sizeof(takers) / sizeof(takers[0]); ++i) {
         msel::BoundsRecord r{};
+        if (takers[i] == nullptr) continue;  // built without that source
         if (takers[i](&r) != hipSuccess) {
             s = MSEL_ERR_HIP;  // the other records are still read and cleared
             continue;
