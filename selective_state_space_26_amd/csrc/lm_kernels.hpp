@@ -45,19 +45,20 @@ hipError_t launch_column_sums(const float* part, int rows, int64_t cols, float* 
 // The gated norm over the channels of [batch, D, L]; out_bld: out and dout are [batch, L, D].
 struct TileNormParams {
     int B, D, L, groups, n;  // n = D / groups
-    int tiles;               // token tiles per batch row, set by the launcher
+    int tiles;               // token tiles per batch row, set by the launchers
     float eps;
     int out_bld;
     const void* x;
     const void* z;
     const float* w;
     const void* dout;
-    void* out;  // forward: out; backward: dx
+    void* out;       // forward: out; backward: dx
     void* dz;
-    float* dw_part;
+    float* dw_part;  // backward: [tiles of all batch rows][D] partial sums, or null
     float* dw;
 };
-int tile_norm_partials(int B, int D, int L, int groups, bool bf16, bool gate_first);
+// Rows of partial dweight sums that a backward over these sizes may write.
+int64_t tile_norm_partials(int B, int L, bool bf16);
 hipError_t launch_tile_norm_fwd(const TileNormParams& p, bool gate_first, bool bf16,
                                 hipStream_t stream);
 hipError_t launch_tile_norm_bwd(const TileNormParams& p, bool gate_first, bool bf16,

@@ -2,7 +2,10 @@
 // [batch, dim, seqlen], to the same layout or turned to [batch, seqlen, dim]:
 //   gate first:  v = x silu(z),  out = v rstd(v) w;   gate last:  out = x rstd(x) w silu(z),
 //   rstd(v) = (sum over the group's n channels of v^2 / n + eps)^(-1/2).
-// HBM bounds it: x and z read, out written (the tiles are described in tile_norm.hpp).
+// HBM bounds it: x and z read, out written (the tiles are described in tile_norm.hpp).  The
+// gate's exp and reciprocal are computed once for a pass in registers: gate first keeps v, in the
+// registers of x and z (as many in bf16); gate last keeps x and z, and needs the gate for the
+// output alone.
 #include <hip/hip_runtime.h>
 
 #include "tile_norm.hpp"
@@ -11,128 +14,182 @@ namespace msel {
 
 namespace {
 
-// NIT: passes whose values stay in registers between the sum and the output; 0: any number of
-// passes, read again for the output.
-template <typename T, bool FIRST, bool OUT_BLD, int TT, int THREADS, int NIT>
-__global__ __launch_bounds__(THREADS) void tile_norm_fwd_kernel(TileNormParams p) {
-    using Sh = TileShape<T, TT, THREADS>;
-    constexpr int VE = Sh::VE, VL = Sh::VL, CPB = Sh::CPB;
-    __shared__ float red[Sh::WAVES * TT];
-    __shared__ TurnTile<T, TT, THREADS> turn[OUT_BLD ? 2 : 1];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int vl = tid % VL, ch = tid / VL;
-    const int tile = static_cast<int>(xcd_order(blockIdx.x, gridDim.x));
-    const int b = tile / p.tiles;
-    const int t0 = (tile - b * p.tiles) * TT;
-    const int t = t0 + vl * VE;
-    const int valid = p.L - t;  // of this lane's tokens, may be <= 0
-    const int c0 = blockIdx.y * p.n;
-    [[maybe_unused]] const int64_t elems = static_cast<int64_t>(p.B) * p.D * p.L;
-    const T* x = static_cast<const T*>(p.x);
-    const T* z = static_cast<const T*>(p.z);
-    const bool whole = t0 + TT <= p.L;  // block-uniform
-
-    const auto at = [&](int c) {
-        return (static_cast<int64_t>(b) * p.D + c0 + c) * p.L + t;
-    };
-    const auto load = [&](const T* q, int c) {
-        RawVec<T, VE> r;
-        r.w = 0;
-        if (whole) {
-            if (c < p.n) r = ld_raw<T, VE>(q + MSEL_SPAN(at(c), VE, elems));
-        } else if (c < p.n && valid > 0) {
-            r = ld_part<T, VE>(q + MSEL_SPAN(at(c), valid < VE ? valid : VE, elems), valid);
-        }
-        return r;
-    };
-
-    constexpr int R = NIT > 0 ? NIT : 1;
-    RawVec<T, VE> rx[R], rz[R];
-    float acc[VE] = {};
-    const auto add = [&](const RawVec<T, VE>& ax, const RawVec<T, VE>& az) {
-        float xv[VE], zv[VE];
-        to_f32<T, VE>(ax, xv);
-        to_f32<T, VE>(az, zv);
-#pragma unroll
-        for (int k = 0; k < VE; ++k) {
-            const float v = FIRST ? xv[k] * silu_f(zv[k]) : xv[k];
-            acc[k] = fmaf(v, v, acc[k]);
-        }
-    };
-    const int passes = (p.n + CPB - 1) / CPB;
-    if constexpr (NIT > 0) {
-#pragma unroll
-        for (int i = 0; i < NIT; ++i) {
-            rx[i] = load(x, i * CPB + ch);
-            rz[i] = load(z, i * CPB + ch);
-        }
-#pragma unroll
-        for (int i = 0; i < NIT; ++i) add(rx[i], rz[i]);
+// fp32 values in the words of two vectors as loaded: neighbours k, k + 1 of bf16 vectors in the
+// words that held their inputs.
+template <typename T, int VE>
+__device__ __forceinline__ void put_pair(RawVec<T, VE>& a, RawVec<T, VE>& b, int k, float lo,
+                                         float hi) {
+    if constexpr (sizeof(T) == 4) {
+        a.w[k] = __float_as_uint(lo);
+        a.w[k + 1] = __float_as_uint(hi);
     } else {
-        for (int i = 0; i < passes; ++i) add(load(x, i * CPB + ch), load(z, i * CPB + ch));
+        a.w[k / 2] = __float_as_uint(lo);
+        b.w[k / 2] = __float_as_uint(hi);
     }
-    tile_sum<VE, VL, Sh::WAVES, TT>(acc, red, lane, wave);
-    float rstd[VE];
-    const float inv_n = 1.0f / static_cast<float>(p.n);
-#pragma unroll
-    for (int k = 0; k < VE; ++k) rstd[k] = rstd_of(acc[k], inv_n, p.eps);
+}
+template <typename T, int VE>
+__device__ __forceinline__ float kept_elem(const RawVec<T, VE>& a, const RawVec<T, VE>& b, int k) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(a.w[k]);
+    else return __uint_as_float(k & 1 ? b.w[k / 2] : a.w[k / 2]);
+}
 
-    T* out = static_cast<T*>(p.out);
-    const auto emit = [&](int i, const RawVec<T, VE>& ax, const RawVec<T, VE>& az) {
-        const int c = i * CPB + ch;
-        const float w =
-            c < p.n && p.w != nullptr ? p.w[MSEL_IDX(c0 + c, p.D)] : 1.0f;
-        float xv[VE], zv[VE], o[VE];
-        to_f32<T, VE>(ax, xv);
-        to_f32<T, VE>(az, zv);
+// NIT: passes kept in registers, NL: passes after them kept in LDS (a thread's own words; no
+// barrier), STREAM: there may be more, which are read twice.
+template <typename T, bool FIRST, bool OUT_BLD, int SB, int THREADS, int NIT, int NL,
+          bool STREAM, bool WHOLE>
+__global__ __launch_bounds__(THREADS) void tile_norm_fwd_kernel(TileNormParams p) {
+    using Sh = TileShape<T, SB, THREADS>;
+    using Rows = RowLane<T, SB, THREADS, WHOLE>;
+    constexpr int VE = Sh::VE, TT = Sh::TT, CPB = Sh::CPB;
+    __shared__ float red[Sh::WAVES * TT], rstds[TT];
+    __shared__ std::conditional_t<OUT_BLD, TurnTile<T, SB, THREADS>, NoTile> turn[2];
+    using Vec = RawVec<T, VE>;
+    constexpr int HELD = NIT + NL;
+    __shared__ decltype(Vec::w) held[NL > 0 ? NL : 1][2][NL > 0 ? THREADS : 1];
+    const int tid = threadIdx.x;
+    const TileLane<T, SB, THREADS, WHOLE> me(p, tid);
+    const TilePlace<TT> at(p, static_cast<int>(xcd_order(blockIdx.x, gridDim.x)));
+    const int c0 = blockIdx.y * p.n;
+
+    Vec x[NIT > 0 ? NIT : 1], z[NIT > 0 ? NIT : 1];
 #pragma unroll
-        for (int k = 0; k < VE; ++k) o[k] = xv[k] * silu_f(zv[k]) * rstd[k] * w;
-        if constexpr (OUT_BLD) {
-            auto& tl = turn[i & 1];
-            tl.put_tokens(vl, ch, o);
-            // one barrier per pass: the buffer of pass i is written again in pass i + 2, whose
-            // writes come after the barrier of pass i + 1, hence after every read of pass i
-            __syncthreads();
-            const int row = tid / Sh::RV, cv = (tid % Sh::RV) * VE;
-            const int left = p.n - (i * CPB + cv);
-            if (t0 + row < p.L && left > 0) {
-                const int64_t o0 =
-                    (static_cast<int64_t>(b) * p.L + t0 + row) * p.D + c0 + i * CPB + cv;
-                st_part<T, VE>(out + MSEL_SPAN(o0, left < VE ? left : VE, elems),
-                               tl.get_channels(row, cv), left);
+    for (int i = 0; i < NIT; ++i) {
+        x[i].w = 0;
+        z[i].w = 0;
+        if (i * CPB < p.n) {  // block-uniform, here and below
+            x[i] = me.load(p, p.x, at, c0, i * CPB);
+            z[i] = me.load(p, p.z, at, c0, i * CPB);
+        }
+    }
+    float acc[1][VE] = {};
+    const auto add = [&](Vec& ax, Vec& az) {  // gate first: v takes the place of x and z
+#pragma unroll
+        for (int k = 0; k < VE; k += 2) {
+            float v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                v[e] = elem_of(ax, k + e);
+                if constexpr (FIRST) v[e] *= silu_f(elem_of(az, k + e));
+                acc[0][k + e] = fmaf(v[e], v[e], acc[0][k + e]);
             }
-        } else if (c < p.n && valid > 0) {
-            st_part<T, VE>(out + MSEL_SPAN(at(c), valid < VE ? valid : VE, elems),
-                           from_f32<T, VE>(o), valid);
+            if constexpr (FIRST) put_pair(ax, az, k, v[0], v[1]);
+            one_at_a_time();
         }
     };
-    if constexpr (NIT > 0) {
 #pragma unroll
-        for (int i = 0; i < NIT; ++i)
-            if (i < passes) emit(i, rx[i], rz[i]);
-    } else {
-        for (int i = 0; i < passes; ++i) emit(i, load(x, i * CPB + ch), load(z, i * CPB + ch));
+    for (int i = 0; i < NIT; ++i)
+        if (i * CPB < p.n) add(x[i], z[i]);
+    if constexpr (STREAM) {
+        // gate last needs z for the output alone
+        const auto want_z = [](int i) { return FIRST || i < HELD; };
+        Vec sx = me.load(p, p.x, at, c0, NIT * CPB), sz;
+        sz.w = 0;
+        if (want_z(NIT)) sz = me.load(p, p.z, at, c0, NIT * CPB);
+        for (int i = NIT; i * CPB < p.n; ++i) {  // one pass ahead
+            Vec nx = me.load(p, p.x, at, c0, (i + 1) * CPB), nz;
+            nz.w = 0;
+            if (want_z(i + 1)) nz = me.load(p, p.z, at, c0, (i + 1) * CPB);
+            add(sx, sz);
+            if (NL > 0 && i < HELD) {
+                held[i - NIT][0][tid] = sx.w;
+                held[i - NIT][1][tid] = sz.w;
+            }
+            sx = nx;
+            sz = nz;
+        }
+    }
+    const float s = tile_sum<1, VE, Sh::VL, Sh::WAVES, TT>(acc, red, tid);
+    if (tid < TT) rstds[tid] = rstd_of(s, 1.0f / static_cast<float>(p.n), p.eps);
+    __syncthreads();
+    float rstd[VE];
+#pragma unroll
+    for (int k = 0; k < VE; ++k) rstd[k] = rstds[me.vl * VE + k];
+
+    // pass i; kept: x and z as add left them
+    const auto emit = [&](auto kept, int i, const Vec& ax, const Vec& az) {
+        const int c = i * CPB, ch = c + me.ch;
+        const float w = ch < p.n && p.w != nullptr ? p.w[MSEL_IDX(c0 + ch, p.D)] : 1.0f;
+        Vec o;
+#pragma unroll
+        for (int k = 0; k < VE; k += 2) {
+            float v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                constexpr bool have = FIRST && kept.value;
+                v[e] = have ? kept_elem(ax, az, k + e) : elem_of(ax, k + e);
+                if constexpr (!have) v[e] *= silu_f(elem_of(az, k + e));
+                v[e] *= rstd[k + e] * w;
+            }
+            set_pair(o, k, v[0], v[1]);
+            one_at_a_time();
+        }
+        if constexpr (OUT_BLD) {
+            turn[i & 1].put_tokens(me.vl, me.ch, o);
+            // one barrier per pass: a buffer is written again two passes later, after the barrier
+            // of the pass between, hence after every read of it
+            __syncthreads();
+            Rows::store(p, p.out, at, c0, c, tid, turn[i & 1].get_group(tid));
+        } else {
+            me.store(p, p.out, at, c0, c, o);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NIT; ++i)
+        if (i * CPB < p.n) emit(std::true_type{}, i, x[i], z[i]);
+    if constexpr (NL > 0)
+        for (int i = NIT; i < HELD && i * CPB < p.n; ++i) {
+            Vec ax, az;
+            ax.w = held[i - NIT][0][tid];
+            az.w = held[i - NIT][1][tid];
+            emit(std::true_type{}, i, ax, az);
+        }
+    if constexpr (STREAM) {
+        Vec sx = me.load(p, p.x, at, c0, HELD * CPB), sz = me.load(p, p.z, at, c0, HELD * CPB);
+        for (int i = HELD; i * CPB < p.n; ++i) {
+            const Vec nx = me.load(p, p.x, at, c0, (i + 1) * CPB);
+            const Vec nz = me.load(p, p.z, at, c0, (i + 1) * CPB);
+            emit(std::false_type{}, i, sx, sz);
+            sx = nx;
+            sz = nz;
+        }
     }
 }
 
-template <typename T, bool FIRST, bool OUT_BLD>
+template <typename T, bool FIRST, bool OUT_BLD, int SB, int THREADS, int NIT, int NL,
+          bool STREAM, bool WHOLE = true>
 hipError_t tile_fwd_go(TileNormParams p, hipStream_t stream) {
-    constexpr int TT = 32, THREADS = 512;
-    p.tiles = (p.L + TT - 1) / TT;
-    const dim3 grid(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles),
-                    static_cast<unsigned>(p.groups));
-    hipLaunchKernelGGL((tile_norm_fwd_kernel<T, FIRST, OUT_BLD, TT, THREADS, 0>), grid,
-                       dim3(THREADS), 0, stream, p);
+    using Sh = TileShape<T, SB, THREADS>;
+    p.tiles = (p.L + Sh::TT - 1) / Sh::TT;
+    hipLaunchKernelGGL(
+        (tile_norm_fwd_kernel<T, FIRST, OUT_BLD, SB, THREADS, NIT, NL, STREAM, WHOLE>),
+        dim3(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles),
+             static_cast<unsigned>(p.groups)),
+        dim3(THREADS), 0, stream, p);
     return hipGetLastError();
+}
+
+template <typename T, bool FIRST, bool OUT_BLD>
+hipError_t tile_fwd_width(const TileNormParams& p, hipStream_t stream) {
+    // Wide tiles where the group stays on the CU (n <= 1536 there) and enough of them fill the
+    // chip: 8 x 1536 x 2048 bf16 33-36 us against 43 in tiles of 64 bytes.  Beyond that narrow
+    // tiles hold twice the channels: 5120 x 65536 538 us against 597.  Narrow groups take smaller
+    // blocks, several on a CU: 8 groups of 640 x 65536 399 us against 427.
+    constexpr int kBytes = static_cast<int>(sizeof(T));
+    if (p.L < 64 / kBytes) return tile_fwd_go<T, FIRST, OUT_BLD, 64, 256, 0, 0, true, false>(p, stream);
+    const bool wide = p.L >= 128 / kBytes && tile_blocks<T, 128>(p) >= kWideBlocks;
+    if (wide && p.n <= 64) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 128, 4, 0, false>(p, stream);
+    if (wide && p.n <= 640) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 512, 10, 0, false>(p, stream);
+    if (wide && p.n <= 1536) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 1024, 9, 3, true>(p, stream);
+    return tile_fwd_go<T, FIRST, OUT_BLD, 64, 1024, 9, 3, true>(p, stream);
 }
 
 template <typename T>
 hipError_t tile_fwd(const TileNormParams& p, bool gate_first, hipStream_t stream) {
     if (gate_first)
-        return p.out_bld ? tile_fwd_go<T, true, true>(p, stream)
-                         : tile_fwd_go<T, true, false>(p, stream);
-    return p.out_bld ? tile_fwd_go<T, false, true>(p, stream)
-                     : tile_fwd_go<T, false, false>(p, stream);
+        return p.out_bld ? tile_fwd_width<T, true, true>(p, stream)
+                         : tile_fwd_width<T, true, false>(p, stream);
+    return p.out_bld ? tile_fwd_width<T, false, true>(p, stream)
+                     : tile_fwd_width<T, false, false>(p, stream);
 }
 
 }  // namespace

@@ -2,28 +2,44 @@
 // [batch, dim, seqlen] share (tile_norm.hip, tile_norm_bwd.hip).
 //
 // The normed axis is strided: token t of channel c lies seqlen elements from channel c + 1's.
-// A block takes a tile of TT consecutive tokens of one batch row and one group of n channels.
-// A lane loads one 16-byte vector, VE consecutive tokens of one channel; VL = TT / VE lanes
-// side by side cover the tile's tokens, and a pass of the block CPB = THREADS / VL channels.
-// Sums over channels: each lane over its passes, then over the lanes of a wavefront that hold
-// the same tokens, then over the wavefronts through LDS, in a fixed order.
-// Rows in [batch, seqlen, dim] are turned through LDS one pass of CPB channels at a time.
+// A block takes a tile of TT consecutive tokens of one batch row, SB bytes of the row of each of
+// the n channels of a group: a lane loads one 16-byte vector, VE consecutive tokens of one
+// channel; VL = TT / VE lanes side by side cover the tile's tokens and a pass of the block takes
+// CPB channels.  Sums over channels: each lane over its passes, then over the lanes of a
+// wavefront that hold the same tokens, then over the wavefronts through LDS, in a fixed order.
+// Rows in [batch, seqlen, dim] are turned through LDS, a pass at a time.
+//
+// A tile's first passes stay in registers and LDS from the sums to the outputs; passes beyond
+// them are read twice.  Reading is faster in wide tiles (two 671 MB tensors of 5120 rows in 221 us at SB = 256, 264 at 128, 306 at
+// 64, 400 at 32), but a wide tile holds fewer channels, and two blocks on a CU, one loading while
+// the other computes, are faster than one of twice the size.  The launchers choose by n.
+// Measured and not kept: blocks that walk tiles and load a pass of the next tile as they write
+// one of the current (neighbouring tiles then run apart and no longer share cache lines: 790 us
+// against 650 for the forward of 5120 x 65536 at SB = 32), and two kernels, sums and then outputs
+// with all inputs read twice at SB = 256 (663 against 621 us there; 52 against 43 for
+// 8 x 1536 x 2048).
+//
+// A last tile that is not full starts early, at seqlen - TT, and does the tokens it shares with
+// the tile before it again (the same values in the same order, so the same bits; the backward
+// leaves them out of dweight).  Only sequences shorter than 64 bytes take partial vectors.
 #pragma once
+
+#include <algorithm>
+#include <type_traits>
 
 #include "lm_device.hpp"
 #include "lm_kernels.hpp"
 
 namespace msel {
 
-template <typename T, int TT, int THREADS>
+template <typename T, int SB, int THREADS>
 struct TileShape {
     static constexpr int VE = 16 / static_cast<int>(sizeof(T));
-    static constexpr int VL = TT / VE;
-    static constexpr int CPB = THREADS / VL;
+    static constexpr int TT = SB / static_cast<int>(sizeof(T));
+    static constexpr int VL = SB / 16;
+    static constexpr int CPB = THREADS / VL;        // channels per pass
     static constexpr int WAVES = THREADS / 64;
-    static constexpr int RV = CPB / VE;          // vectors of a turned row of one pass
-    static constexpr int S = CPB + 16 / static_cast<int>(sizeof(T));  // its padded length
-    static_assert(TT % VE == 0 && 64 % VL == 0 && TT * RV == THREADS, "one vector per thread");
+    static_assert(64 % VL == 0, "whole vectors of tokens");
 };
 
 // Consecutive tiles on one XCD: blocks go to the 8 XCDs in turn, and neighbouring tiles share
@@ -33,55 +49,234 @@ __device__ __forceinline__ unsigned xcd_order(unsigned bid, unsigned n) {
     return x * q + (x < r ? x : r) + (bid >> 3);
 }
 
-// Sums acc over the lanes of the block that hold the same tokens; red: [WAVES][TT] floats.
-// One barrier; the caller puts another between two calls on the same red.
-template <int VE, int VL, int WAVES, int TT>
-__device__ __forceinline__ void tile_sum(float (&acc)[VE], float* red, int lane, int wave) {
-#pragma unroll
-    for (int m = VL; m < 64; m *= 2)
-#pragma unroll
-        for (int k = 0; k < VE; ++k) acc[k] += __shfl_xor(acc[k], m);
-    if (lane < VL) {
-#pragma unroll
-        for (int k = 0; k < VE; ++k) red[wave * TT + lane * VE + k] = acc[k];
+// Blocks of a launch in tiles of SB bytes, and how many make wide tiles worth it: 2048 x 2047
+// x 4 bf16 forward, 128 blocks, took 34 us wide and 22 narrow.
+template <typename T, int SB>
+inline int64_t tile_blocks(const TileNormParams& p) {
+    constexpr int TT = SB / static_cast<int>(sizeof(T));
+    return static_cast<int64_t>(p.B) * p.groups * ((p.L + TT - 1) / TT);
+}
+constexpr int kWideBlocks = 224;
+
+// Element k of a vector as loaded, and the other way round for two neighbours: unlike to_f32 and
+// from_f32 these keep few fp32 values alive.
+template <typename T, int VE>
+__device__ __forceinline__ float elem_of(const RawVec<T, VE>& r, int k) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r.w[k]);
+    else return k & 1 ? bf16hi(r.w[k / 2]) : bf16lo(r.w[k / 2]);
+}
+template <typename T, int VE>
+__device__ __forceinline__ void set_pair(RawVec<T, VE>& r, int k, float lo, float hi) {
+    if constexpr (sizeof(T) == 4) {
+        r.w[k] = __float_as_uint(lo);
+        r.w[k + 1] = __float_as_uint(hi);
+    } else {
+        r.w[k / 2] = pack_bf16(lo, hi);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < VE; ++k) acc[k] = 0.0f;
-    const int vl = lane % VL;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w)
-#pragma unroll
-        for (int k = 0; k < VE; ++k) acc[k] += red[w * TT + vl * VE + k];
 }
 
-// A pass's turned tile in LDS: TT rows of CPB channels, padded to S.
-template <typename T, int TT, int THREADS>
-struct TurnTile {
-    using Sh = TileShape<T, TT, THREADS>;
-    T v[TT * Sh::S];
+// Keeps the scheduler from working on many elements at once, which costs registers that hold
+// passes (the wavefronts hide the latencies).
+__device__ __forceinline__ void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }
 
-    // this thread's VE tokens of one channel
-    __device__ __forceinline__ void put_tokens(int vl, int ch, const float (&o)[Sh::VE]) {
+// One level of a sum over lanes: lanes l and l ^ M share their N values out, so that each is
+// left with N / 2 sums (the upper half of the values where the lane's bit M is set); N = 1 adds.
+template <int M, int N>
+__device__ __forceinline__ void share_sums(float* v, int lane) {
+    if constexpr (N > 1) {
+        const bool up = (lane & M) != 0;
 #pragma unroll
-        for (int k = 0; k < Sh::VE; ++k)
-            Elem<T>::store1(v + MSEL_IDX((vl * Sh::VE + k) * Sh::S + ch, TT * Sh::S), o[k]);
+        for (int k = 0; k < N / 2; ++k) {
+            const float give = up ? v[k] : v[k + N / 2];
+            const float keep = up ? v[k + N / 2] : v[k];
+            v[k] = keep + __shfl_xor(give, M);
+        }
+    } else {
+        v[0] += __shfl_xor(v[0], M);
     }
-    __device__ __forceinline__ void get_tokens(int vl, int ch, float (&o)[Sh::VE]) const {
+}
+template <int M, int N, int VL>
+__device__ __forceinline__ void share_levels(float* v, int lane) {
+    if constexpr (M >= VL) {
+        share_sums<M, N>(v, lane);
+        share_levels<M / 2, (N > 1 ? N / 2 : 1), VL>(v, lane);
+    }
+}
+
+// Sums NS values per token (VE tokens per lane) over the lanes of the block that hold the same
+// tokens; red: [NS][WAVES][TT] floats of LDS.  Returns sum tid / TT of token tid % TT in threads
+// below NS * TT.  A wavefront's lanes share the values out between them, so a level moves half
+// as many as the one before.  One barrier.
+template <int NS, int VE, int VL, int WAVES, int TT>
+__device__ __forceinline__ float tile_sum(float (&acc)[NS][VE], float* red, int tid) {
+    const int lane = tid & 63, wave = tid >> 6;
+    constexpr int LEVELS = VL == 32 ? 1 : VL == 16 ? 2 : VL == 8 ? 3 : VL == 4 ? 4 : 5;  // log2(64 / VL)
+    constexpr int BITS = VE == 8 ? 3 : 2;                                  // log2(VE)
+    constexpr int SHARED = LEVELS < BITS ? LEVELS : BITS;  // levels that halve the values
+    constexpr int LEFT = VE >> SHARED;
+    static_assert(VL >= 2 && NS * TT <= WAVES * 64, "a thread per sum");
+    // the lane's values start where its bits 5, 4, .. say; of the lanes that only added, the
+    // first writes
+    const int first = ((lane >> (6 - SHARED)) & ((1 << SHARED) - 1)) * LEFT;
+    const int rest = lane & ((1 << (6 - SHARED)) - 1);  // lane within its values' holders
 #pragma unroll
-        for (int k = 0; k < Sh::VE; ++k)
-            o[k] = Elem<T>::load1(v + MSEL_IDX((vl * Sh::VE + k) * Sh::S + ch, TT * Sh::S));
+    for (int s = 0; s < NS; ++s) {
+        share_levels<32, VE, VL>(acc[s], lane);
+        if (rest < VL) {
+#pragma unroll
+            for (int k = 0; k < LEFT; ++k)
+                red[(s * WAVES + wave) * TT + (lane % VL) * VE + first + k] = acc[s][k];
+        }
     }
-    // VE channels of one token (16-byte aligned)
-    __device__ __forceinline__ void put_channels(int row, int cv, const RawVec<T, Sh::VE>& r) {
-        *reinterpret_cast<decltype(r.w)*>(v + MSEL_SPAN(row * Sh::S + cv, Sh::VE, TT * Sh::S)) =
-            r.w;
+    __syncthreads();
+    float v = 0.0f;
+    if (tid < NS * TT) {
+        const int s = tid / TT, t = tid % TT;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) v += red[(s * WAVES + w) * TT + t];
     }
-    __device__ __forceinline__ RawVec<T, Sh::VE> get_channels(int row, int cv) const {
-        RawVec<T, Sh::VE> r;
-        r.w = *reinterpret_cast<const decltype(r.w)*>(
-            v + MSEL_SPAN(row * Sh::S + cv, Sh::VE, TT * Sh::S));
+    return v;
+}
+
+// A tile's first token, and how many of its tokens the tile before has done (block-uniform).
+template <int TT>
+struct TilePlace {
+    int b, t0, skip;
+
+    __device__ __forceinline__ TilePlace(const TileNormParams& p, int tile) {
+        b = tile / p.tiles;
+        const int t = (tile - b * p.tiles) * TT;
+        t0 = max(0, min(t, p.L - TT));
+        skip = t - t0;
+    }
+};
+
+// A thread's part of a tile.  Addresses are a block-uniform element plus the thread's offset.
+// WHOLE: seqlen >= TT, every tile is full.
+template <typename T, int SB, int THREADS, bool WHOLE>
+struct TileLane {
+    using Sh = TileShape<T, SB, THREADS>;
+    static constexpr int VE = Sh::VE;
+    int vl, ch;   // vector of the tile's tokens, channel within a pass
+    int64_t off;  // ch * L + vl * VE
+
+    __device__ __forceinline__ TileLane(const TileNormParams& p, int tid) {
+        vl = tid % Sh::VL;
+        ch = tid / Sh::VL;
+        off = static_cast<int64_t>(ch) * p.L + vl * VE;
+    }
+    // of this lane's VE tokens
+    __device__ __forceinline__ int valid(const TileNormParams& p) const {
+        return WHOLE ? VE : p.L - vl * VE;
+    }
+    // element of this lane's tokens of channel c + ch of the group that starts at channel c0
+    __device__ __forceinline__ int64_t at(const TileNormParams& p, const TilePlace<Sh::TT>& pl,
+                                          int c0, int c) const {
+        const int64_t first = (static_cast<int64_t>(pl.b) * p.D + c0 + c) * p.L + pl.t0;
+        return MSEL_SPAN(first + off, min(valid(p), VE), static_cast<int64_t>(p.B) * p.D * p.L);
+    }
+    __device__ __forceinline__ RawVec<T, VE> load(const TileNormParams& p, const void* q,
+                                                  const TilePlace<Sh::TT>& pl, int c0,
+                                                  int c) const {
+        RawVec<T, VE> r;
+        r.w = 0;
+        if (c + ch < p.n && (WHOLE || valid(p) > 0)) {
+            const T* from = static_cast<const T*>(q) + at(p, pl, c0, c);
+            if constexpr (WHOLE) r = ld_raw<T, VE>(from);
+            else r = ld_part<T, VE>(from, valid(p));
+        }
         return r;
+    }
+    __device__ __forceinline__ void store(const TileNormParams& p, void* q,
+                                          const TilePlace<Sh::TT>& pl, int c0, int c,
+                                          const RawVec<T, VE>& r) const {
+        if (c + ch < p.n && (WHOLE || valid(p) > 0)) {
+            T* to = static_cast<T*>(q) + at(p, pl, c0, c);
+            if constexpr (WHOLE) st_raw<T, VE>(to, r);
+            else st_part<T, VE>(to, r, valid(p));
+        }
+    }
+};
+
+// A pass in LDS, TT rows of its CPB channels, between [batch, dim, seqlen] and
+// [batch, seqlen, dim].  16-byte groups of a row are swapped by the row's vector of tokens, which
+// spreads the accesses of a pass over the banks.
+template <typename T, int SB, int THREADS>
+struct TurnTile {
+    using Sh = TileShape<T, SB, THREADS>;
+    static constexpr int VE = Sh::VE, TT = Sh::TT, CH = Sh::CPB;
+    static constexpr int G = CH / VE;  // groups per row: a group per thread
+    static constexpr int kElems = TT * CH;
+    static_assert(TT * G == THREADS && (G & (G - 1)) == 0, "a group per thread");
+    T v[kElems] __attribute__((aligned(16)));
+
+    __device__ __forceinline__ static int place(int row, int g) {
+        return row * CH + (g ^ (row / VE & (G - 1))) * VE;
+    }
+    // VE tokens of channel c
+    __device__ __forceinline__ void put_tokens(int vl, int c, const RawVec<T, VE>& o) {
+        T* col = v + MSEL_SPAN(place(vl * VE, c / VE) + c % VE, (VE - 1) * CH + 1, kElems);
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+            T& to = col[k * CH];
+            if constexpr (sizeof(T) == 4) to = __uint_as_float(o.w[k]);
+            else to.bits = static_cast<uint16_t>(k & 1 ? o.w[k / 2] >> 16 : o.w[k / 2]);
+        }
+    }
+    __device__ __forceinline__ RawVec<T, VE> get_tokens(int vl, int c) const {
+        const T* col = v + MSEL_SPAN(place(vl * VE, c / VE) + c % VE, (VE - 1) * CH + 1, kElems);
+        RawVec<T, VE> o;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+            const T& at = col[k * CH];
+            if constexpr (sizeof(T) == 4) o.w[k] = __float_as_uint(at);
+            else if (k & 1) o.w[k / 2] |= static_cast<uint32_t>(at.bits) << 16;
+            else o.w[k / 2] = at.bits;
+        }
+        return o;
+    }
+    __device__ __forceinline__ void put_group(int tid, const RawVec<T, VE>& r) {
+        *reinterpret_cast<decltype(RawVec<T, VE>::w)*>(
+            v + MSEL_SPAN(place(tid / G, tid % G), VE, kElems)) = r.w;
+    }
+    __device__ __forceinline__ RawVec<T, VE> get_group(int tid) const {
+        RawVec<T, VE> r;
+        r.w = *reinterpret_cast<const decltype(r.w)*>(
+            v + MSEL_SPAN(place(tid / G, tid % G), VE, kElems));
+        return r;
+    }
+};
+struct NoTile {};  // of a kernel that turns nothing
+
+// The thread's group of a pass in [batch, L, D]: VE channels, from c on, of the group at c0.
+template <typename T, int SB, int THREADS, bool WHOLE>
+struct RowLane {
+    using Sh = TileShape<T, SB, THREADS>;
+    static constexpr int VE = Sh::VE, G = Sh::CPB / VE;
+
+    __device__ __forceinline__ static int64_t at(const TileNormParams& p,
+                                                 const TilePlace<Sh::TT>& pl, int c0, int c,
+                                                 int tid) {
+        const int64_t i = (static_cast<int64_t>(pl.b) * p.L + pl.t0 + tid / G) * p.D + c0 + c +
+                          tid % G * VE;
+        return MSEL_SPAN(i, min(p.n - c - tid % G * VE, VE), static_cast<int64_t>(p.B) * p.D * p.L);
+    }
+    __device__ __forceinline__ static RawVec<T, VE> load(const TileNormParams& p, const void* q,
+                                                         const TilePlace<Sh::TT>& pl, int c0,
+                                                         int c, int tid) {
+        const int left = p.n - c - tid % G * VE;
+        RawVec<T, VE> r;
+        r.w = 0;
+        if (left > 0 && (WHOLE || tid / G < p.L))
+            r = ld_part<T, VE>(static_cast<const T*>(q) + at(p, pl, c0, c, tid), left);
+        return r;
+    }
+    __device__ __forceinline__ static void store(const TileNormParams& p, void* q,
+                                                 const TilePlace<Sh::TT>& pl, int c0, int c,
+                                                 int tid, const RawVec<T, VE>& r) {
+        const int left = p.n - c - tid % G * VE;
+        if (left > 0 && (WHOLE || tid / G < p.L))
+            st_part<T, VE>(static_cast<T*>(q) + at(p, pl, c0, c, tid), r, left);
     }
 };
 

@@ -5,12 +5,10 @@
 //   gate first: dx = dv silu(z), dz = dv x silu'(z);
 //   gate last:  dx = dv,         dz = dout w x rstd silu'(z).
 // The gate and rstd are recomputed.  HBM bounds it: x, z and dout read, dx and dz written (the
-// tiles are described in tile_norm.hpp).  Blocks walk tiles with the grid's stride and keep
-// their channels' dweight sums in LDS (one lane adds to each, no atomics); a second kernel adds
-// the blocks' sums in block order.
+// tiles are described in tile_norm.hpp).  A tile also writes its tokens' share of dweight, a row
+// of partial sums, and a second kernel adds the rows in a fixed order (no atomics:
+// deterministic).
 #include <hip/hip_runtime.h>
-
-#include <algorithm>
 
 #include "tile_norm.hpp"
 
@@ -18,190 +16,211 @@ namespace msel {
 
 namespace {
 
-// Blocks of a launch over all groups: each writes a row of partial dweight sums.
-constexpr int kBwdBlocks = 512;
-
-template <typename T, bool FIRST, bool DOUT_BLD, int TT, int THREADS, int NIT>
+// NIT: passes kept in registers, NL: passes after them kept in LDS (a thread's own words; no
+// barrier), STREAM: there may be more, which are read twice.
+template <typename T, bool FIRST, bool DOUT_BLD, int SB, int THREADS, int NIT, int NL,
+          bool STREAM, bool WHOLE>
 __global__ __launch_bounds__(THREADS) void tile_norm_bwd_kernel(TileNormParams p) {
-    using Sh = TileShape<T, TT, THREADS>;
-    constexpr int VE = Sh::VE, VL = Sh::VL, CPB = Sh::CPB;
-    __shared__ float red[2][Sh::WAVES * TT];
-    __shared__ TurnTile<T, TT, THREADS> turn[DOUT_BLD ? 2 : 1];
-    extern __shared__ float dwl[];  // [passes * CPB]
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int vl = tid % VL, ch = tid / VL;
+    using Sh = TileShape<T, SB, THREADS>;
+    using Rows = RowLane<T, SB, THREADS, WHOLE>;
+    using Vec = RawVec<T, Sh::VE>;
+    constexpr int VE = Sh::VE, TT = Sh::TT, CPB = Sh::CPB;
+    __shared__ float red[2 * Sh::WAVES * TT];
+    __shared__ float tok[2 * TT];  // rstd and c of the tile's tokens
+    __shared__ std::conditional_t<DOUT_BLD, TurnTile<T, SB, THREADS>, NoTile> turn[2];
+    constexpr int HELD = NIT + NL;
+    __shared__ decltype(Vec::w) held[NL > 0 ? NL : 1][3][NL > 0 ? THREADS : 1];
+    const int tid = threadIdx.x;
+    const TileLane<T, SB, THREADS, WHOLE> me(p, tid);
+    const int tile = static_cast<int>(xcd_order(blockIdx.x, gridDim.x));
+    const TilePlace<TT> at(p, tile);
     const int c0 = blockIdx.y * p.n;
-    [[maybe_unused]] const int64_t elems = static_cast<int64_t>(p.B) * p.D * p.L;
-    const T* x = static_cast<const T*>(p.x);
-    const T* z = static_cast<const T*>(p.z);
-    const T* dout = static_cast<const T*>(p.dout);
-    T* dx = static_cast<T*>(p.out);
-    T* dz = static_cast<T*>(p.dz);
-    const float inv_n = 1.0f / static_cast<float>(p.n);
-    const int passes = (p.n + CPB - 1) / CPB;
-    const int ntiles = p.B * p.tiles;  // < 2^31: checked on the host
-    if (vl == 0)
-        for (int i = 0; i < passes; ++i) dwl[i * CPB + ch] = 0.0f;  // this lane's alone
 
-    for (int tile = static_cast<int>(xcd_order(blockIdx.x, gridDim.x)); tile < ntiles;
-         tile += static_cast<int>(gridDim.x)) {
-        const int b = tile / p.tiles;
-        const int t0 = (tile - b * p.tiles) * TT;
-        const int t = t0 + vl * VE;
-        const int valid = p.L - t;
-        const bool whole = t0 + TT <= p.L;
-        const auto at = [&](int c) {
-            return (static_cast<int64_t>(b) * p.D + c0 + c) * p.L + t;
-        };
-        const auto load = [&](const T* q, int c) {
-            RawVec<T, VE> r;
-            r.w = 0;
-            if (whole) {
-                if (c < p.n) r = ld_raw<T, VE>(q + MSEL_SPAN(at(c), VE, elems));
-            } else if (c < p.n && valid > 0) {
-                r = ld_part<T, VE>(q + MSEL_SPAN(at(c), valid < VE ? valid : VE, elems), valid);
-            }
-            return r;
-        };
-        // dout of pass i: this lane's tokens of its channel
-        const auto load_dout = [&](int i) {
-            if constexpr (!DOUT_BLD) {
-                return load(dout, i * CPB + ch);
-            } else {
-                const int row = tid / Sh::RV, cv = (tid % Sh::RV) * VE;
-                const int left = p.n - (i * CPB + cv);
-                RawVec<T, VE> r;
-                r.w = 0;
-                if (t0 + row < p.L && left > 0) {
-                    const int64_t o0 =
-                        (static_cast<int64_t>(b) * p.L + t0 + row) * p.D + c0 + i * CPB + cv;
-                    r = ld_part<T, VE>(dout + MSEL_SPAN(o0, left < VE ? left : VE, elems), left);
-                }
-                return r;
-            }
-        };
-        // turned to tokens through LDS when it came as rows; one barrier per pass (a buffer is
-        // written again two passes later)
-        const auto turn_dout = [&](int i, const RawVec<T, VE>& r, float (&dy)[VE]) {
-            if constexpr (!DOUT_BLD) {
-                to_f32<T, VE>(r, dy);
-            } else {
-                auto& tl = turn[i & 1];
-                tl.put_channels(tid / Sh::RV, (tid % Sh::RV) * VE, r);
-                __syncthreads();
-                tl.get_tokens(vl, ch, dy);
-            }
-        };
-        const auto weight = [&](int c) {
-            return c < p.n && p.w != nullptr ? p.w[MSEL_IDX(c0 + c, p.D)] : 1.0f;
-        };
-
-        float sv[VE] = {}, sg[VE] = {};
-        for (int i = 0; i < passes; ++i) {
-            const int c = i * CPB + ch;
-            float xv[VE], zv[VE], dy[VE];
-            to_f32<T, VE>(load(x, c), xv);
-            to_f32<T, VE>(load(z, c), zv);
-            turn_dout(i, load_dout(i), dy);
-            const float w = weight(c);
-#pragma unroll
-            for (int k = 0; k < VE; ++k) {
-                const float gate = silu_f(zv[k]);
-                const float v = FIRST ? xv[k] * gate : xv[k];
-                const float g = FIRST ? dy[k] * w : dy[k] * w * gate;
-                sv[k] = fmaf(v, v, sv[k]);
-                sg[k] = fmaf(g, v, sg[k]);
-            }
+    const auto load_dout = [&](int c) {
+        if constexpr (DOUT_BLD) return Rows::load(p, p.dout, at, c0, c, tid);
+        else return me.load(p, p.dout, at, c0, c);
+    };
+    // dout that came as rows, turned through LDS; one barrier per pass (a buffer is written again
+    // two passes later, after the barrier of the pass between)
+    const auto turned = [&](const Vec& d, int buf) {
+        if constexpr (DOUT_BLD) {
+            turn[buf].put_group(tid, d);
+            __syncthreads();
+            return turn[buf].get_tokens(me.vl, me.ch);
+        } else {
+            return d;
         }
-        if constexpr (DOUT_BLD) __syncthreads();
-        tile_sum<VE, VL, Sh::WAVES, TT>(sv, red[0], lane, wave);
-        tile_sum<VE, VL, Sh::WAVES, TT>(sg, red[1], lane, wave);
-        float rstd[VE], cf[VE];
+    };
+    const auto weight = [&](int c) {
+        const int ch = c + me.ch;
+        return ch < p.n && p.w != nullptr ? p.w[MSEL_IDX(c0 + ch, p.D)] : 1.0f;
+    };
+
+    Vec x[NIT > 0 ? NIT : 1], z[NIT > 0 ? NIT : 1], d[NIT > 0 ? NIT : 1];
+#pragma unroll
+    for (int i = 0; i < NIT; ++i) {
+        x[i].w = 0;
+        z[i].w = 0;
+        d[i].w = 0;
+        if (i * CPB < p.n) {  // block-uniform, here and below
+            x[i] = me.load(p, p.x, at, c0, i * CPB);
+            z[i] = me.load(p, p.z, at, c0, i * CPB);
+            d[i] = load_dout(i * CPB);
+        }
+    }
+    float acc[2][VE] = {};  // sums of v^2 and of g v
+    const auto add = [&](int c, const Vec& ax, const Vec& az, const Vec& ad) {
+        const float w = weight(c);
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
-            rstd[k] = rstd_of(sv[k], inv_n, p.eps);
-            cf[k] = rstd[k] * rstd[k] * (sg[k] * inv_n);
+            // g v is dout w x silu(z) in either order
+            const float xk = elem_of(ax, k), xg = xk * silu_f(elem_of(az, k));
+            const float v = FIRST ? xg : xk;
+            acc[0][k] = fmaf(v, v, acc[0][k]);
+            acc[1][k] = fmaf(elem_of(ad, k) * w, xg, acc[1][k]);
+            if (k & 1) one_at_a_time();
         }
-        for (int i = 0; i < passes; ++i) {
-            const int c = i * CPB + ch;
-            float xv[VE], zv[VE], dy[VE], gx[VE], gz[VE];
-            to_f32<T, VE>(load(x, c), xv);
-            to_f32<T, VE>(load(z, c), zv);
-            turn_dout(i, load_dout(i), dy);
-            const float w = weight(c);
-            float dw = 0.0f;
+    };
 #pragma unroll
-            for (int k = 0; k < VE; ++k) {
-                float gate, slope;
-                silu_grad_f(zv[k], gate, slope);
+    for (int i = 0; i < NIT; ++i)
+        if (i * CPB < p.n) {
+            d[i] = turned(d[i], i & 1);
+            add(i * CPB, x[i], z[i], d[i]);
+            // the loaded words alone stay, not their fp32 values beside them
+            asm volatile("" : "+v"(x[i].w), "+v"(z[i].w), "+v"(d[i].w));
+        }
+    const auto stream = [&](int first, auto&& f) {
+        Vec sx = me.load(p, p.x, at, c0, first * CPB), sz = me.load(p, p.z, at, c0, first * CPB);
+        Vec sd = load_dout(first * CPB);
+        for (int i = first; i * CPB < p.n; ++i) {  // one pass ahead
+            const Vec nx = me.load(p, p.x, at, c0, (i + 1) * CPB);
+            const Vec nz = me.load(p, p.z, at, c0, (i + 1) * CPB);
+            const Vec nd = load_dout((i + 1) * CPB);
+            f(i, sx, sz, turned(sd, i & 1));
+            sx = nx;
+            sz = nz;
+            sd = nd;
+        }
+    };
+    if constexpr (STREAM)
+        stream(NIT, [&](int i, const Vec& ax, const Vec& az, const Vec& ad) {
+            add(i * CPB, ax, az, ad);
+            if (NL > 0 && i < HELD) {
+                held[i - NIT][0][tid] = ax.w;
+                held[i - NIT][1][tid] = az.w;
+                held[i - NIT][2][tid] = ad.w;
+            }
+        });
+    const float s = tile_sum<2, VE, Sh::VL, Sh::WAVES, TT>(acc, red, tid);
+    const float inv_n = 1.0f / static_cast<float>(p.n);
+    if (tid < TT) tok[tid] = rstd_of(s, inv_n, p.eps);
+    __syncthreads();
+    if (tid >= TT && tid < 2 * TT) tok[tid] = tok[tid - TT] * tok[tid - TT] * (s * inv_n);
+    __syncthreads();
+
+    float* part = p.dw_part == nullptr ? nullptr : p.dw_part + static_cast<int64_t>(tile) * p.D + c0;
+    const auto emit = [&](int c, const Vec& ax, const Vec& az, const Vec& ad) {
+        const float w = weight(c);
+        float dw = 0.0f;
+        Vec ox, oz;
+#pragma unroll
+        for (int k = 0; k < VE; k += 2) {
+            float gx[2], gz[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = me.vl * VE + k + e;
+                const float xk = elem_of(ax, k + e), dy = elem_of(ad, k + e);
+                const float r = tok[t], cf = tok[TT + t];
+                float gate, slope, part_t;
+                silu_grad_f(elem_of(az, k + e), gate, slope);
                 if constexpr (FIRST) {
-                    const float v = xv[k] * gate;
-                    const float dv = rstd[k] * fmaf(-v, cf[k], dy[k] * w);
-                    gx[k] = dv * gate;
-                    gz[k] = dv * xv[k] * slope;
-                    dw = fmaf(dy[k], v * rstd[k], dw);
+                    const float v = xk * gate;
+                    const float dv = r * fmaf(-v, cf, dy * w);
+                    gx[e] = dv * gate;
+                    gz[e] = dv * xk * slope;
+                    part_t = dy * (v * r);
                 } else {
-                    const float xh = xv[k] * rstd[k];
-                    gx[k] = rstd[k] * fmaf(-xv[k], cf[k], dy[k] * w * gate);
-                    gz[k] = dy[k] * w * xh * slope;
-                    dw = fmaf(dy[k] * gate, xh, dw);
+                    const float xh = xk * r;
+                    gx[e] = r * fmaf(-xk, cf, dy * w * gate);
+                    gz[e] = dy * w * xh * slope;
+                    part_t = dy * gate * xh;
                 }
+                dw += t >= at.skip ? part_t : 0.0f;
             }
-            if (c < p.n && valid > 0) {
-                const int64_t o0 = MSEL_SPAN(at(c), valid < VE ? valid : VE, elems);
-                st_part<T, VE>(dx + o0, from_f32<T, VE>(gx), valid);
-                st_part<T, VE>(dz + o0, from_f32<T, VE>(gz), valid);
-            }
-#pragma unroll
-            for (int m = 1; m < VL; m *= 2) dw += __shfl_xor(dw, m);
-            if (vl == 0) dwl[MSEL_IDX(c, passes * CPB)] += dw;
+            set_pair(ox, k, gx[0], gx[1]);
+            set_pair(oz, k, gz[0], gz[1]);
+            one_at_a_time();
         }
-        __syncthreads();  // red and turn are free again
-    }
-    if (p.dw_part == nullptr) return;
-    float* out = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.D + c0;
-    if (vl == 0)
-        for (int i = 0; i < passes; ++i)
-            if (i * CPB + ch < p.n) out[MSEL_IDX(i * CPB + ch, p.n)] = dwl[i * CPB + ch];
+        me.store(p, p.out, at, c0, c, ox);
+        me.store(p, p.dz, at, c0, c, oz);
+        if (part != nullptr) {
+#pragma unroll
+            for (int m = 1; m < Sh::VL; m *= 2) dw += __shfl_xor(dw, m);
+            if (me.vl == 0 && c + me.ch < p.n) part[MSEL_IDX(c + me.ch, p.n)] = dw;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NIT; ++i)
+        if (i * CPB < p.n) emit(i * CPB, x[i], z[i], d[i]);
+    if constexpr (NL > 0)
+        for (int i = NIT; i < HELD && i * CPB < p.n; ++i) {
+            Vec ax, az, ad;
+            ax.w = held[i - NIT][0][tid];
+            az.w = held[i - NIT][1][tid];
+            ad.w = held[i - NIT][2][tid];
+            emit(i * CPB, ax, az, ad);
+        }
+    if constexpr (STREAM)
+        stream(HELD, [&](int i, const Vec& ax, const Vec& az, const Vec& ad) {
+            emit(i * CPB, ax, az, ad);
+        });
 }
 
-int bwd_blocks(int B, int tiles, int groups) {
-    return static_cast<int>(std::min<int64_t>(static_cast<int64_t>(B) * tiles,
-                                              std::max(1, kBwdBlocks / groups)));
+template <typename T, bool FIRST, bool DOUT_BLD, int SB, int THREADS, int NIT, int NL,
+          bool STREAM, bool WHOLE = true>
+hipError_t tile_bwd_go(TileNormParams p, hipStream_t stream) {
+    using Sh = TileShape<T, SB, THREADS>;
+    p.tiles = (p.L + Sh::TT - 1) / Sh::TT;
+    const unsigned tiles = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles);
+    hipLaunchKernelGGL(
+        (tile_norm_bwd_kernel<T, FIRST, DOUT_BLD, SB, THREADS, NIT, NL, STREAM, WHOLE>),
+        dim3(tiles, static_cast<unsigned>(p.groups)), dim3(THREADS), 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.dw_part == nullptr) return e;
+    return launch_column_sums(p.dw_part, static_cast<int>(tiles), p.D, p.dw, stream);
 }
-
-constexpr int kTT = 32, kThreads = 512;
 
 template <typename T, bool FIRST, bool DOUT_BLD>
-hipError_t tile_bwd_go(TileNormParams p, hipStream_t stream) {
-    using Sh = TileShape<T, kTT, kThreads>;
-    p.tiles = (p.L + kTT - 1) / kTT;
-    const dim3 grid(static_cast<unsigned>(bwd_blocks(p.B, p.tiles, p.groups)),
-                    static_cast<unsigned>(p.groups));
-    const int lds = (p.n + Sh::CPB - 1) / Sh::CPB * Sh::CPB * static_cast<int>(sizeof(float));
-    constexpr auto kern = tile_norm_bwd_kernel<T, FIRST, DOUT_BLD, kTT, kThreads, 0>;
-    hipError_t e = allow_dynamic_lds<kern>(kMaxNormDim * static_cast<int>(sizeof(float)));
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, grid, dim3(kThreads), static_cast<size_t>(lds), stream, p);
-    e = hipGetLastError();
-    if (e != hipSuccess || p.dw_part == nullptr) return e;
-    return launch_column_sums(p.dw_part, static_cast<int>(grid.x), p.D, p.dw, stream);
+hipError_t tile_bwd_width(const TileNormParams& p, hipStream_t stream) {
+    // Wide tiles where the group stays on the CU (n <= 768 there) or does not in narrow ones
+    // either (5120 x 16384 bf16: 273 us against 337); between the two narrow tiles hold it
+    // (8 x 1536 x 2048 from [batch, seqlen, dim]: 72 us against 78).  Narrow groups take smaller
+    // blocks, several on a CU (64 x 128 x 4096 fp32: 186 us against 208).
+    constexpr int kBytes = static_cast<int>(sizeof(T));
+    if (p.L < 64 / kBytes) return tile_bwd_go<T, FIRST, DOUT_BLD, 64, 256, 0, 0, true, false>(p, stream);
+    const bool wide = p.L >= 128 / kBytes && tile_blocks<T, 128>(p) >= kWideBlocks;
+    if (wide && p.n <= 64) return tile_bwd_go<T, FIRST, DOUT_BLD, 128, 128, 4, 0, false>(p, stream);
+    if (wide && p.n <= 256) return tile_bwd_go<T, FIRST, DOUT_BLD, 128, 512, 4, 0, false>(p, stream);
+    if (wide && (p.n <= 768 || p.n > 1536))
+        return tile_bwd_go<T, FIRST, DOUT_BLD, 128, 1024, 4, 2, true>(p, stream);
+    return tile_bwd_go<T, FIRST, DOUT_BLD, 64, 1024, 4, 2, true>(p, stream);
 }
 
 template <typename T>
 hipError_t tile_bwd(const TileNormParams& p, bool gate_first, hipStream_t stream) {
     if (gate_first)
-        return p.out_bld ? tile_bwd_go<T, true, true>(p, stream)
-                         : tile_bwd_go<T, true, false>(p, stream);
-    return p.out_bld ? tile_bwd_go<T, false, true>(p, stream)
-                     : tile_bwd_go<T, false, false>(p, stream);
+        return p.out_bld ? tile_bwd_width<T, true, true>(p, stream)
+                         : tile_bwd_width<T, true, false>(p, stream);
+    return p.out_bld ? tile_bwd_width<T, false, true>(p, stream)
+                     : tile_bwd_width<T, false, false>(p, stream);
 }
 
 }  // namespace
 
-int tile_norm_partials(int B, int D, int L, int groups, bool, bool) {
-    (void)D;
-    return bwd_blocks(B, (L + kTT - 1) / kTT, groups);
+int64_t tile_norm_partials(int B, int L, bool bf16) {
+    // the narrowest tiles
+    const int tt = bf16 ? TileShape<bf16_t, 64, 256>::TT : TileShape<float, 64, 256>::TT;
+    return static_cast<int64_t>(B) * ((L + tt - 1) / tt);
 }
 
 hipError_t launch_tile_norm_bwd(const TileNormParams& p, bool gate_first, bool bf16,

@@ -70,6 +70,9 @@ CASES = {
     "gated_odd": lambda: _gated(2, 1537, 77, 1, "bf16", True, "bdl", "bld"),
     "gated_groups": lambda: _gated(1, 1000, 133, 4, "f32", False, "bdl", "bdl"),
     "gated_wide": lambda: _gated(1, 5121, 65, 1, "bf16", True, "bdl", "bld"),
+    "gated_narrow_wide_tiles": lambda: _gated(3, 40, 5000, 1, "bf16", True, "bdl", "bld"),
+    "gated_wide_tiles": lambda: _gated(1, 1601, 14500, 1, "bf16", True, "bdl", "bld"),
+    "gated_wide_tiles_groups": lambda: _gated(2, 2400, 1000, 8, "f32", False, "bdl", "bdl"),
     "gated_widest": lambda: _gated(1, 16384, 40, 1, "f32", True, "bdl", "bdl"),
     "embed_small": lambda: _embed(5, 3, 2, "f32"),
     "embed_odd": lambda: _embed(3001, 777, 33, "bf16"),

@@ -145,6 +145,32 @@ def test_gated_norm(shape, layout, out_layout, dtype, first):
     assert_sum("dweight", g["dweight"], ref["dweight"], ref["dweight_terms"])
 
 
+# channels of a group (8 groups, 240 or more wide tiles): every block size, groups held on the CU
+# whole and in part
+@pytest.mark.parametrize("n", [40, 203, 300, 700, 1001, 1601])
+@pytest.mark.parametrize("dtype,first,out_layout", [("bf16", True, "bld"), ("f32", False, "bdl")])
+def test_gated_norm_wide_tiles(n, dtype, first, out_layout):
+    bsz, groups, L = 1, 8, 1873 if dtype == "bf16" else 937
+    dim = groups * n
+    log(f"gated norm wide tiles {n} {dtype}")
+    x, z = normal((bsz, dim, L), dtype, 1), normal((bsz, dim, L), dtype, 2)
+    w = normal((dim,), "f32", 3, 0.1, 1.0)
+    dout = normal((bsz, dim, L) if out_layout == "bdl" else (bsz, L, dim), dtype, 4)
+    args = (1e-5, groups, first, "bdl", out_layout)
+    out = msel.msel_gated_norm_fwd(x, z, w, *args)
+    g = msel.msel_gated_norm_bwd(x, z, w, dout, *args)
+    opt = dict(eps=1e-5, groups=groups, gate_first=first)
+    rx, rz, rd = _to_rows(x, "bdl"), _to_rows(z, "bdl"), _to_rows(dout, out_layout)
+
+    def rows(t, lay):
+        return (t.transpose(1, 2) if lay == "bdl" else t).reshape(-1, dim)
+    assert_elementwise("out", rows(out, out_layout), lm.gated_fwd(rx, rz, host(w), **opt))
+    ref = lm.gated_bwd(rx, rz, host(w), rd, **opt)
+    assert_elementwise("dx", rows(g["dx"], "bdl"), ref["dx"], ref["dx_terms"])
+    assert_elementwise("dz", rows(g["dz"], "bdl"), ref["dz"], ref["dz_terms"])
+    assert_sum("dweight", g["dweight"], ref["dweight"], ref["dweight_terms"])
+
+
 @pytest.mark.parametrize("layout,out_layout", LAYOUTS)
 def test_gated_norm_many_tiles_without_weight(layout, out_layout):
     """More tiles and rows than the backward's grid has blocks; no weight, no dweight."""
