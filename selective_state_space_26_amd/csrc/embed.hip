@@ -8,14 +8,16 @@
 // Three steps:
 //  1. a stable radix sort of (id, position), ids outside [0, vocab) and the padding id last.
 //     Digits of up to 9 bits; a block counts and places a run of consecutive tokens, ranks within
-//     a wavefront by ballots, so that the order is the tokens' own: deterministic.  The sort
-//     needs few blocks and waits on latency, so the same launches fill dw (with base or 0) on
-//     the remaining CUs;
-//  2. segment sums: the sorted positions in chunks of kSeg entries; a team of lanes adds its
+//     a wavefront by ballots, so that the order is the tokens' own: deterministic.  Up to
+//     kOneBlock tokens are sorted by one block in one launch.  The sort needs few blocks and
+//     waits on latency, so the same launches fill dw (with base or 0) on the remaining CUs;
+//  2. segment sums: the sorted positions in chunks of `seg` entries; a team of lanes adds its
 //     chunk's rows in fp32.  An id's run inside a chunk is written to dw directly; a run that
 //     crosses chunks leaves one partial sum per chunk;
 //  3. the partial sums of each crossing run are added in chunk order.
-// No floating-point atomics, and a frequent id costs no more than a rare one.
+// No floating-point atomics, and a frequent id costs no more than a rare one.  (Counting a pass's
+// digits with global atomics in the pass before saved a launch and cost 22 us: the most frequent
+// ids' counters are one address each.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -32,18 +34,27 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kDigitBits = 9;
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kMaxSortBlocks = 128;
+constexpr int kOneBlock = 2048;  // tokens that one block sorts alone
 constexpr int kFillBlocks = 512;
-constexpr int kSeg = 32;         // sorted entries per segment-sum chunk
-constexpr int kSegBatch = 8;     // of them in flight at a time
+constexpr int kSegBatch = 8;     // rows of a chunk in flight at a time
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 1024;  // blocks per slab of columns that look for runs to join
 
 struct EmbedPlan {
     int passes, dbits, nblocks;
     int chunk;       // tokens per sort block
-    int nseg;        // segment chunks
+    int seg, nseg;   // sorted entries per segment-sum chunk, chunks
+    int launches;    // of the sort, each with a share of the fill
     size_t key[2], pos[2], table, partial, bytes;  // offsets into the workspace
 };
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+int team_of(int nvec, int most) {
+    int s = 8;
+    while (s < nvec && s < most) s *= 2;
+    return s;
+}
 
 EmbedPlan embed_plan(int64_t tokens, int vocab, int dim) {
     EmbedPlan pl{};
@@ -52,10 +63,17 @@ EmbedPlan embed_plan(int64_t tokens, int vocab, int dim) {
     pl.passes = (bits + kDigitBits - 1) / kDigitBits;
     pl.dbits = (bits + pl.passes - 1) / pl.passes;
     const int64_t tiles = (tokens + kSortThreads - 1) / kSortThreads;
-    const int64_t blocks = std::min<int64_t>(kMaxSortBlocks, tiles);
+    const int64_t blocks = tokens <= kOneBlock ? 1 : std::min<int64_t>(kMaxSortBlocks, tiles);
     pl.chunk = static_cast<int>((tiles + blocks - 1) / blocks * kSortThreads);
     pl.nblocks = static_cast<int>((tokens + pl.chunk - 1) / pl.chunk);
-    pl.nseg = static_cast<int>((tokens + kSeg - 1) / kSeg);
+    pl.launches = pl.nblocks == 1 ? 1 : 2 * pl.passes;
+    // short chunks while the teams would not fill the chip (a chunk is a team's work), long ones
+    // for many rows, which leave fewer partial sums: 2048 x 1024 of 32000 ids took 32 us with 8
+    // entries and 40 with 32, 262144 x 64 of 16 ids 48 and 36, 16384 x 768 of 50257 ids 53 with 16
+    const int64_t lanes = tokens * std::min(256, (dim + 7) / 8);
+    pl.seg = 8;
+    while (pl.seg < 32 && lanes / pl.seg > 98304) pl.seg *= 2;
+    pl.nseg = static_cast<int>((tokens + pl.seg - 1) / pl.seg);
     size_t at = 0;
     const auto take = [&](size_t n) {
         const size_t o = at;
@@ -66,7 +84,7 @@ EmbedPlan embed_plan(int64_t tokens, int vocab, int dim) {
         pl.key[i] = take(static_cast<size_t>(tokens) * 4);
         pl.pos[i] = take(static_cast<size_t>(tokens) * 4);
     }
-    pl.table = take(static_cast<size_t>(pl.passes) * kBins * pl.nblocks * 4);
+    pl.table = take(static_cast<size_t>(kBins) * pl.nblocks * 4);
     pl.partial = take(static_cast<size_t>(pl.nseg) * 2 * dim * 4);
     pl.bytes = at;
     return pl;
@@ -122,238 +140,302 @@ __device__ __forceinline__ uint32_t key_of(const EmbedParams& p, int64_t t) {
                                                           : static_cast<uint32_t>(p.vocab);
 }
 
-// Pass 0's digit counts per block, table[digit][block], and zeros for the later passes' tables.
-__global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedParams p, EmbedPlan pl) {
+__device__ __forceinline__ uint32_t* part_of(const EmbedParams& p, size_t offset) {
+    return reinterpret_cast<uint32_t*>(static_cast<char*>(p.ws) + offset);
+}
+
+// (key, position) of entry t before pass `pass`.
+__device__ __forceinline__ uint32_t key_at(const EmbedParams& p, const EmbedPlan& pl, int pass,
+                                           int64_t t) {
+    return pass == 0 ? key_of(p, t) : part_of(p, pl.key[(pass + 1) & 1])[MSEL_IDX(t, p.tokens)];
+}
+
+// Counts the digits of pass `pass` in this block's tokens into cnt[1 << dbits] (LDS).
+__device__ __forceinline__ void count_digits(const EmbedParams& p, const EmbedPlan& pl, int pass,
+                                             uint32_t* cnt) {
+    const int nb = 1 << pl.dbits;
+    for (int i = threadIdx.x; i < nb; i += kSortThreads) cnt[i] = 0;
+    __syncthreads();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * pl.chunk;
+    const int64_t t1 = min(t0 + pl.chunk, p.tokens);
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += kSortThreads)
+        atomicAdd(&cnt[(key_at(p, pl, pass, t) >> (pass * pl.dbits)) & (nb - 1)], 1u);
+    __syncthreads();
+}
+
+// Digit counts per block of one pass: table[block][digit].
+__global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedParams p, EmbedPlan pl,
+                                                                   int pass) {
     __shared__ uint32_t cnt[kBins];
     if (static_cast<int>(blockIdx.x) >= pl.nblocks) {
-        fill_share(p, 0, pl.passes + 1, blockIdx.x - pl.nblocks, gridDim.x - pl.nblocks);
+        fill_share(p, 2 * pass, pl.launches, blockIdx.x - pl.nblocks, gridDim.x - pl.nblocks);
         return;
     }
-    uint32_t* table = reinterpret_cast<uint32_t*>(static_cast<char*>(p.ws) + pl.table);
-    const int words = kBins * pl.nblocks;
-    for (int i = threadIdx.x; i < kBins; i += kSortThreads) cnt[i] = 0;
-    __syncthreads();
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * pl.chunk;
-    const int64_t t1 = min(t0 + pl.chunk, p.tokens);
-    const uint32_t mask = (1u << pl.dbits) - 1u;
-    for (int64_t t = t0 + threadIdx.x; t < t1; t += kSortThreads)
-        atomicAdd(&cnt[MSEL_IDX(key_of(p, t) & mask, kBins)], 1u);
-    __syncthreads();
-    for (int d = threadIdx.x; d < kBins; d += kSortThreads) {
-        const int at = d * pl.nblocks + static_cast<int>(blockIdx.x);
-        table[MSEL_IDX(at, words)] = cnt[d];
-        for (int q = 1; q < pl.passes; ++q) table[q * words + MSEL_IDX(at, words)] = 0;
-    }
+    count_digits(p, pl, pass, cnt);
+    const int nb = 1 << pl.dbits;
+    uint32_t* table = part_of(p, pl.table);
+    for (int d = threadIdx.x; d < nb; d += kSortThreads)
+        table[MSEL_IDX(static_cast<int>(blockIdx.x) * nb + d, kBins * pl.nblocks)] = cnt[d];
 }
 
-// Places the tokens of pass `pass` in digit order (stable), and counts the next pass's digits
-// by destination block.
+// Places the tokens of pass `pass` in digit order (stable); a block alone counts them itself and
+// makes all passes.
 __global__ __launch_bounds__(kSortThreads) void embed_place_kernel(EmbedParams p, EmbedPlan pl,
                                                                    int pass) {
-    __shared__ uint32_t run[kBins];               // next free place of each digit
+    __shared__ uint32_t run[kBins];  // next free place of each digit
     __shared__ uint32_t cnt[kSortWaves][kBins];
+    __shared__ uint32_t wsum[kSortWaves];
+    const bool alone = pl.nblocks == 1;
     if (static_cast<int>(blockIdx.x) >= pl.nblocks) {
-        fill_share(p, pass + 1, pl.passes + 1, blockIdx.x - pl.nblocks, gridDim.x - pl.nblocks);
+        fill_share(p, alone ? 0 : 2 * pass + 1, pl.launches, blockIdx.x - pl.nblocks,
+                   gridDim.x - pl.nblocks);
         return;
     }
-    char* ws = static_cast<char*>(p.ws);
-    const int words = kBins * pl.nblocks;
-    const uint32_t* table = reinterpret_cast<const uint32_t*>(ws + pl.table) + pass * words;
-    uint32_t* next = reinterpret_cast<uint32_t*>(ws + pl.table) + (pass + 1) * words;
-    const uint32_t* key_in = reinterpret_cast<const uint32_t*>(ws + pl.key[(pass + 1) & 1]);
-    const uint32_t* pos_in = reinterpret_cast<const uint32_t*>(ws + pl.pos[(pass + 1) & 1]);
-    uint32_t* key_out = reinterpret_cast<uint32_t*>(ws + pl.key[pass & 1]);
-    uint32_t* pos_out = reinterpret_cast<uint32_t*>(ws + pl.pos[pass & 1]);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int shift = pass * pl.dbits;
-    const uint32_t mask = (1u << pl.dbits) - 1u;
-
-    // where this block's tokens of each digit go: all smaller digits, then this digit in the
-    // blocks before
-    uint32_t total = 0, before = 0;
-    if (tid < kBins) {
-        for (int j = 0; j < pl.nblocks; ++j) {
-            const uint32_t c = table[MSEL_IDX(tid * pl.nblocks + j, words)];
-            total += c;
-            before += j < static_cast<int>(blockIdx.x) ? c : 0u;
-        }
-        run[tid] = total;
-    }
-    __syncthreads();
-    for (int s = 1; s < kBins; s *= 2) {
-        const uint32_t v = tid < kBins && tid >= s ? run[tid - s] : 0u;
-        __syncthreads();
-        if (tid < kBins) run[tid] += v;
-        __syncthreads();
-    }
-    if (tid < kBins) run[tid] += before - total;
-
+    const int nb = 1 << pl.dbits;
+    const uint32_t mask = static_cast<uint32_t>(nb) - 1u;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * pl.chunk;
     const int64_t t1 = min(t0 + pl.chunk, p.tokens);
-    for (int64_t tb = t0; tb < t1; tb += kSortThreads) {  // block-uniform
-        for (int i = tid; i < kSortWaves * kBins; i += kSortThreads) (&cnt[0][0])[i] = 0;
-        __syncthreads();
-        const int64_t t = tb + tid;
-        const bool in = t < t1;
-        uint32_t key = 0, pos = 0;
-        if (in) {
-            key = pass == 0 ? key_of(p, t) : key_in[MSEL_IDX(t, p.tokens)];
-            pos = pass == 0 ? static_cast<uint32_t>(t) : pos_in[MSEL_IDX(t, p.tokens)];
-        }
-        const uint32_t digit = (key >> shift) & mask;
-        uint64_t same = __ballot(in);
-        for (int bit = 0; bit < pl.dbits; ++bit) {
-            const uint64_t b = __ballot((digit >> bit) & 1u);
-            same &= (digit >> bit) & 1u ? b : ~b;
-        }
-        const int rank = __popcll(same & ((uint64_t(1) << lane) - 1u));
-        if (in && rank == 0) cnt[wave][digit] = static_cast<uint32_t>(__popcll(same));
-        __syncthreads();
-        if (tid < kBins) {
-            uint32_t s = run[tid];
-            for (int w = 0; w < kSortWaves; ++w) {
-                const uint32_t c = cnt[w][tid];
-                cnt[w][tid] = s;
-                s += c;
+    do {
+        // where this block's tokens of each digit go: all smaller digits, then this digit in the
+        // blocks before
+        uint32_t total = 0, before = 0;
+        if (alone) {
+            count_digits(p, pl, pass, &cnt[0][0]);
+            if (tid < nb) total = cnt[0][tid];
+            __syncthreads();
+        } else {
+            const uint32_t* table = part_of(p, pl.table);
+            const int d = tid & (nb - 1), grp = tid >> pl.dbits, grps = kSortThreads >> pl.dbits;
+            const int me = static_cast<int>(blockIdx.x);
+#pragma unroll 8
+            for (int j = grp; j < pl.nblocks; j += grps) {
+                const uint32_t c = table[MSEL_IDX(j * nb + d, kBins * pl.nblocks)];
+                total += c;
+                before += j < me ? c : 0u;
             }
-            run[tid] = s;
+            // the groups' sums, [2][grps][nb] in cnt
+            uint32_t* sums = &cnt[0][0];
+            sums[tid] = total;
+            sums[kSortThreads + tid] = before;
+            __syncthreads();
+            total = before = 0;
+            if (tid < nb)
+                for (int g = 0; g < grps; ++g) {
+                    total += sums[g * nb + tid];
+                    before += sums[kSortThreads + g * nb + tid];
+                }
+            __syncthreads();
         }
+        // exclusive sums of the totals over the digits (0 in threads past them)
+        uint32_t incl = total;
+#pragma unroll
+        for (int s = 1; s < 64; s *= 2) {
+            const uint32_t v = __shfl_up(incl, s);
+            incl += lane >= s ? v : 0u;
+        }
+        if (lane == 63) wsum[wave] = incl;
         __syncthreads();
-        if (in) {
-            const int64_t to = MSEL_IDX(static_cast<int64_t>(cnt[wave][digit] + rank), p.tokens);
-            key_out[to] = key;
-            pos_out[to] = pos;
-            if (pass + 1 < pl.passes) {
-                const uint32_t d2 = (key >> (shift + pl.dbits)) & mask;
-                const int at = static_cast<int>(d2) * pl.nblocks + static_cast<int>(to / pl.chunk);
-                atomicAdd(&next[MSEL_IDX(at, words)], 1u);
+        uint32_t base = 0;
+        for (int w = 0; w < wave; ++w) base += wsum[w];
+        if (tid < nb) run[tid] = base + incl - total + before;
+
+        uint32_t* key_out = part_of(p, pl.key[pass & 1]);
+        uint32_t* pos_out = part_of(p, pl.pos[pass & 1]);
+        const int shift = pass * pl.dbits;
+        for (int64_t tb = t0; tb < t1; tb += kSortThreads) {  // block-uniform
+            for (int i = tid; i < kSortWaves * nb; i += kSortThreads)
+                cnt[i >> pl.dbits][i & (nb - 1)] = 0;
+            __syncthreads();
+            const int64_t t = tb + tid;
+            const bool in = t < t1;
+            uint32_t key = 0, pos = 0;
+            if (in) {
+                key = key_at(p, pl, pass, t);
+                pos = pass == 0 ? static_cast<uint32_t>(t)
+                                : part_of(p, pl.pos[(pass + 1) & 1])[MSEL_IDX(t, p.tokens)];
             }
+            const uint32_t digit = (key >> shift) & mask;
+            uint64_t same = __ballot(in);
+            for (int bit = 0; bit < pl.dbits; ++bit) {
+                const uint64_t b = __ballot((digit >> bit) & 1u);
+                same &= (digit >> bit) & 1u ? b : ~b;
+            }
+            const int rank = __popcll(same & ((uint64_t(1) << lane) - 1u));
+            if (in && rank == 0) cnt[wave][digit] = static_cast<uint32_t>(__popcll(same));
+            __syncthreads();
+            if (tid < nb) {
+                uint32_t s = run[tid];
+#pragma unroll
+                for (int w = 0; w < kSortWaves; ++w) {
+                    const uint32_t c = cnt[w][tid];
+                    cnt[w][tid] = s;
+                    s += c;
+                }
+                run[tid] = s;
+            }
+            __syncthreads();
+            if (in) {
+                const int64_t to = MSEL_IDX(static_cast<int64_t>(cnt[wave][digit] + rank), p.tokens);
+                key_out[to] = key;
+                pos_out[to] = pos;
+            }
+            __syncthreads();
         }
-        __syncthreads();
-    }
+        // a block alone goes on: its own writes are visible to it after the barrier
+    } while (alone && ++pass < pl.passes);
 }
 
+template <int VE>
 __device__ __forceinline__ void write_row(const EmbedParams& p, uint32_t v, int e0, int left,
-                                          const float* acc, int ve) {
+                                          const float (&acc)[VE]) {
     const int64_t at = static_cast<int64_t>(MSEL_IDX(v, p.vocab)) * p.dim + e0;
-    for (int k = 0; k < ve; ++k)
-        if (k < left) {
-            const float b = p.base != nullptr ? p.base[at + k] : 0.0f;
-            p.dw[at + k] = fmaf(p.scale, acc[k], b);
-        }
+    float o[VE] = {};
+    if (p.base != nullptr) to_f32<float, VE>(ld_part<float, VE>(p.base + at, left), o);
+#pragma unroll
+    for (int k = 0; k < VE; ++k) o[k] = fmaf(p.scale, acc[k], o[k]);
+    st_part<float, VE>(p.dw + at, from_f32<float, VE>(o), left);
 }
 
-// Segment sums: a team of S lanes (S columns vectors of VE) per chunk of kSeg sorted entries.
+// Segment sums: a team of S lanes (S vectors of a row) per chunk of pl.seg sorted entries.  The
+// chunk's ids and positions are loaded by the team's lanes, R = min(S, 64) at a time, and handed
+// round the wavefront.
 template <typename T, int VE>
 __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedParams p, EmbedPlan pl, int S,
                                                         int nvec) {
-    const char* ws = static_cast<const char*>(p.ws);
-    const uint32_t* key = reinterpret_cast<const uint32_t*>(ws + pl.key[(pl.passes - 1) & 1]);
-    const uint32_t* pos = reinterpret_cast<const uint32_t*>(ws + pl.pos[(pl.passes - 1) & 1]);
-    float* part = reinterpret_cast<float*>(static_cast<char*>(p.ws) + pl.partial);
+    const uint32_t* key = part_of(p, pl.key[(pl.passes - 1) & 1]);
+    const uint32_t* pos = part_of(p, pl.pos[(pl.passes - 1) & 1]);
     const int team = threadIdx.x / S, lane = threadIdx.x % S;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * (256 / S) + team;
+    const bool on = c < pl.nseg;  // team-uniform; idle teams keep their lanes for the handing round
     const int cv = blockIdx.y * S + lane;
-    if (c >= pl.nseg || cv >= nvec) return;
-    const int e0 = cv * VE, left = p.dim - e0;
-    const int64_t i0 = c * kSeg;
-    const int64_t i1 = min(i0 + kSeg, p.tokens);
+    const int e0 = cv * VE, left = on && cv < nvec ? p.dim - e0 : 0;
+    const int64_t i0 = on ? c * pl.seg : 0;
+    const int n = on ? static_cast<int>(min(static_cast<int64_t>(pl.seg), p.tokens - i0)) : 0;
     const uint32_t none = static_cast<uint32_t>(p.vocab);
-    const T* dout = static_cast<const T*>(p.dout);
-    float* mine = part + (c * 2) * p.dim + e0;
+    const T* dout = static_cast<const T*>(p.dout) + e0;
+    float* mine = reinterpret_cast<float*>(part_of(p, pl.partial)) + (c * 2) * p.dim + e0;
+    const int R = min(S, 64), rl = lane & (R - 1), first = lane_id() - rl;
 
-    uint32_t cur = key[MSEL_IDX(i0, p.tokens)];
-    bool head = i0 > 0 && key[i0 - 1] == cur;  // the run began in an earlier chunk
+    // the ids before and after the chunk: a run may begin before it, or go on after it
+    const uint32_t before = i0 > 0 ? key[i0 - 1] : none;
+    const uint32_t after = i0 + n < p.tokens ? key[i0 + n] : none;
+    uint32_t mk = rl < n ? key[i0 + rl] : none;
+    uint32_t mp = rl < n ? pos[i0 + rl] : 0u;
+    uint32_t cur = __shfl(mk, first);
+    bool head = i0 > 0 && before == cur;
     float acc[VE] = {};
-    const auto store_part = [&](float* q) {
-#pragma unroll
-        for (int k = 0; k < VE; ++k)
-            if (k < left) q[k] = acc[k];
-    };
-    for (int64_t i = i0; i < i1; i += kSegBatch) {
-        uint32_t kk[kSegBatch];
-        RawVec<T, VE> r[kSegBatch];
-#pragma unroll
-        for (int j = 0; j < kSegBatch; ++j) {
-            const int64_t e = min(i + j, i1 - 1);
-            kk[j] = i + j < i1 ? key[MSEL_IDX(e, p.tokens)] : none;
-            const int64_t t = MSEL_IDX(static_cast<int64_t>(pos[e]), p.tokens);
-            r[j] = ld_part<T, VE>(dout + t * p.dim + e0, left);
+    for (int r = 0; r < pl.seg; r += R) {  // block-uniform
+        const uint32_t ks = mk, ps = mp;
+        if (r + R < pl.seg) {  // the next ids while these rows are added
+            const int j = r + R + rl;
+            mk = j < n ? key[i0 + j] : none;
+            mp = j < n ? pos[i0 + j] : 0u;
         }
+        const int rows = min(R, pl.seg - r);
+        for (int j0 = 0; j0 < rows; j0 += kSegBatch) {
+            uint32_t kk[kSegBatch];
+            RawVec<T, VE> v[kSegBatch];
 #pragma unroll
-        for (int j = 0; j < kSegBatch; ++j) {
-            if (i + j >= i1) break;
-            if (kk[j] != cur) {  // team-uniform
-                if (cur != none) {
-                    if (head) store_part(mine);
-                    else write_row(p, cur, e0, left, acc, VE);
-                }
-                head = false;
-                cur = kk[j];
-#pragma unroll
-                for (int k = 0; k < VE; ++k) acc[k] = 0.0f;
+            for (int j = 0; j < kSegBatch; ++j) {
+                kk[j] = __shfl(ks, first + j0 + j);
+                const int64_t t = MSEL_IDX(static_cast<int64_t>(__shfl(ps, first + j0 + j)), p.tokens);
+                v[j].w = 0;
+                if (left > 0 && kk[j] != none) v[j] = ld_part<T, VE>(dout + t * p.dim, left);
             }
-            float v[VE];
-            to_f32<T, VE>(r[j], v);
 #pragma unroll
-            for (int k = 0; k < VE; ++k) acc[k] += v[k];
+            for (int j = 0; j < kSegBatch; ++j) {
+                if (r + j0 + j >= n) break;  // team-uniform
+                if (kk[j] != cur) {
+                    if (cur != none && left > 0) {
+                        if (head) st_part<float, VE>(mine, from_f32<float, VE>(acc), left);
+                        else write_row<VE>(p, cur, e0, left, acc);
+                    }
+                    head = false;
+                    cur = kk[j];
+#pragma unroll
+                    for (int k = 0; k < VE; ++k) acc[k] = 0.0f;
+                }
+                float f[VE];
+                to_f32<T, VE>(v[j], f);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) acc[k] += f[k];
+            }
         }
     }
-    if (cur == none) return;
-    const bool goes_on = i1 < p.tokens && key[i1] == cur;
-    if (head) store_part(mine);
-    else if (goes_on) store_part(mine + p.dim);
-    else write_row(p, cur, e0, left, acc, VE);
+    if (cur == none || left <= 0) return;
+    if (head) st_part<float, VE>(mine, from_f32<float, VE>(acc), left);
+    else if (after == cur) st_part<float, VE>(mine + p.dim, from_f32<float, VE>(acc), left);
+    else write_row<VE>(p, cur, e0, left, acc);
 }
 
-// The runs that cross chunks: the chunk a run starts in adds the run's partial sums, row lanes
-// of the block every RL-th each, then the row lanes in order.
-__global__ __launch_bounds__(256) void embed_join_kernel(EmbedParams p, EmbedPlan pl, int S,
-                                                         int nvec) {
-    __shared__ float red[256][4];
-    const char* ws = static_cast<const char*>(p.ws);
-    const uint32_t* key = reinterpret_cast<const uint32_t*>(ws + pl.key[(pl.passes - 1) & 1]);
-    const float* part = reinterpret_cast<const float*>(ws + pl.partial);
-    const int64_t c = blockIdx.x;  // c + 1 < nseg
-    const uint32_t k = key[(c + 1) * kSeg - 1];
-    if (k == static_cast<uint32_t>(p.vocab) || key[(c + 1) * kSeg] != k) return;
-    if (key[c * kSeg] == k && c > 0 && key[c * kSeg - 1] == k) return;  // began before
-    int64_t lo = c + 1, hi = pl.nseg - 1;  // the last chunk whose first entry is in the run
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) / 2;
-        if (key[MSEL_IDX(mid * kSeg, p.tokens)] == k) lo = mid;
-        else hi = mid - 1;
-    }
-    const int rl = threadIdx.x / S, lane = threadIdx.x % S, RL = 256 / S;
+// The runs that cross chunks: for each of the block's `look` (up to 64 at a time) chunks that such
+// a run starts in, the block adds the run's partial sums, its row lanes every RL-th row each, then
+// the row lanes in order.
+__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedParams p, EmbedPlan pl,
+                                                                  int S, int nvec, int look) {
+    __shared__ float red[kJoinThreads][4];
+    const uint32_t* key = part_of(p, pl.key[(pl.passes - 1) & 1]);
+    const float* part = reinterpret_cast<const float*>(part_of(p, pl.partial));
+    const int64_t seg = pl.seg;
+    const uint32_t none = static_cast<uint32_t>(p.vocab);
+    const int rl = threadIdx.x / S, lane = threadIdx.x % S, RL = kJoinThreads / S;
     const int cv = blockIdx.y * S + lane;
     const int e0 = cv * 4, left = cv < nvec ? p.dim - e0 : 0;
-    float acc[4] = {};
-    const int64_t n = lo - c + 1;
-#pragma unroll 4
-    for (int64_t j = rl; j < n; j += RL) {
-        // row 0 is the run's part in its first chunk, the others the heads of the next ones
-        const int64_t row = j == 0 ? c * 2 + 1 : (c + j) * 2;
-        float v[4];
-        to_f32<float, 4>(ld_part<float, 4>(
-                             part + MSEL_IDX(row, static_cast<int64_t>(pl.nseg) * 2) * p.dim + e0,
-                             left), v);
+    for (int l0 = 0; l0 < look; l0 += 64) {
+        const int64_t cb = static_cast<int64_t>(blockIdx.x) * look + l0;
+        bool starts = false;
+        if (lane_id() < look - l0 && cb + lane_id() + 1 < pl.nseg) {
+            const int64_t c = cb + lane_id();
+            const uint32_t k = key[(c + 1) * seg - 1], next = key[(c + 1) * seg], first = key[c * seg];
+            const uint32_t prev = c > 0 ? key[c * seg - 1] : none;
+            starts = k != none && next == k && !(first == k && prev == k);
+        }
+        uint64_t todo = __ballot(starts);  // the same in every wavefront
+        for (; todo != 0; todo &= todo - 1) {  // block-uniform
+            const int64_t c = cb + __builtin_ctzll(todo);
+            const uint32_t k = key[(c + 1) * seg];
+            // n: the chunks from c on whose first entries are in the run (but c's own), 64 at a
+            // time: in strides of 1, 64, .. until one stride reaches past the run, then back
+            const auto matches = [&](int64_t from, int64_t stride) {
+                const int64_t j = from + lane_id() * stride;
+                const bool in = j < pl.nseg && key[MSEL_IDX(j * seg, p.tokens)] == k;
+                return __popcll(__ballot(in));  // ids are sorted: a prefix of the lanes
+            };
+            int64_t at = c + 1, stride = 1;
+            int m = matches(at, 1);
+            while (m == 64 && stride < pl.nseg) m = matches(at, stride *= 64);
+            for (; stride > 1; m = matches(at, stride)) {
+                at += (m - 1) * stride;
+                stride /= 64;
+            }
+            const int64_t n = at + m - c;
+            float acc[4] = {};
+#pragma unroll 8
+            for (int64_t j = rl; j < n; j += RL) {
+                // row 0 is the run's part in its first chunk, the others the heads of the next ones
+                const int64_t row = j == 0 ? c * 2 + 1 : (c + j) * 2;
+                float v[4];
+                to_f32<float, 4>(
+                    ld_part<float, 4>(
+                        part + MSEL_IDX(row, static_cast<int64_t>(pl.nseg) * 2) * p.dim + e0, left),
+                    v);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] += v[q];
+                for (int q = 0; q < 4; ++q) acc[q] += v[q];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) red[threadIdx.x][q] = acc[q];
+            __syncthreads();
+            if (rl == 0 && left > 0) {
+                const int rows = static_cast<int>(min(static_cast<int64_t>(RL), n));
+                for (int r = 1; r < rows; ++r)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[q] += red[r * S + lane][q];
+                write_row<4>(p, k, e0, left, acc);
+            }
+            __syncthreads();  // red is free again
+        }
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) red[threadIdx.x][q] = acc[q];
-    __syncthreads();
-    if (rl != 0 || left <= 0) return;
-    for (int r = 1; r < RL; ++r)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] += red[r * S + lane][q];
-    write_row(p, k, e0, left, acc, 4);
-}
-
-int team_of(int nvec, int most) {
-    int s = 8;
-    while (s < nvec && s < most) s *= 2;
-    return s;
 }
 
 template <typename T, typename TW, int VE>
@@ -385,14 +467,19 @@ hipError_t launch_embed_bwd(const EmbedParams& p, bool bf16, hipStream_t stream)
     const EmbedPlan pl = embed_plan(p.tokens, p.vocab, p.dim);
     int fill = 0;
     if (p.base != p.dw) {
-        const int64_t nv = static_cast<int64_t>(p.vocab) * p.dim / 4 / (pl.passes + 1);
+        const int64_t nv = static_cast<int64_t>(p.vocab) * p.dim / 4 / pl.launches;
         fill = static_cast<int>(std::clamp<int64_t>((nv + kSortThreads - 1) / kSortThreads, 1,
                                                     kFillBlocks));
     }
     const dim3 grid(static_cast<unsigned>(pl.nblocks + fill));
-    hipLaunchKernelGGL(embed_count_kernel, grid, dim3(kSortThreads), 0, stream, p, pl);
-    for (int pass = 0; pass < pl.passes; ++pass)
-        hipLaunchKernelGGL(embed_place_kernel, grid, dim3(kSortThreads), 0, stream, p, pl, pass);
+    if (pl.nblocks == 1) {
+        hipLaunchKernelGGL(embed_place_kernel, grid, dim3(kSortThreads), 0, stream, p, pl, 0);
+    } else {
+        for (int pass = 0; pass < pl.passes; ++pass) {
+            hipLaunchKernelGGL(embed_count_kernel, grid, dim3(kSortThreads), 0, stream, p, pl, pass);
+            hipLaunchKernelGGL(embed_place_kernel, grid, dim3(kSortThreads), 0, stream, p, pl, pass);
+        }
+    }
     {
         const int ve = bf16 ? 8 : 4;
         const int nvec = (p.dim + ve - 1) / ve;
@@ -409,8 +496,11 @@ hipError_t launch_embed_bwd(const EmbedParams& p, bool bf16, hipStream_t stream)
     if (pl.nseg > 1) {
         const int nvec = (p.dim + 3) / 4;
         const int S = team_of(nvec, 64);
-        const dim3 g(static_cast<unsigned>(pl.nseg - 1), static_cast<unsigned>((nvec + S - 1) / S));
-        hipLaunchKernelGGL(embed_join_kernel, g, dim3(256), 0, stream, p, pl, S, nvec);
+        const int look = std::max(4, (pl.nseg - 1 + kJoinBlocks - 1) / kJoinBlocks);
+        const dim3 g(static_cast<unsigned>((pl.nseg - 1 + look - 1) / look),
+                     static_cast<unsigned>((nvec + S - 1) / S));
+        hipLaunchKernelGGL(embed_join_kernel, g, dim3(kJoinThreads), 0, stream, p, pl, S, nvec,
+                           look);
     }
     return hipGetLastError();
 }
