@@ -359,9 +359,11 @@ hipError_t fwd_go(const RowNormParams& p, hipStream_t stream) {
 }
 
 template <typename T, typename TA, typename TB, NormMode MODE>
-hipError_t bwd_go(const RowNormParams& p, hipStream_t stream) {
+hipError_t bwd_go(RowNormParams p, hipStream_t stream) {
     const int W = waves_for(p.n, row_ve<TA, T>(1));
     const dim3 grid(grid_of(p.rows, p.groups, W, true), static_cast<unsigned>(p.groups));
+    const bool one = grid.x == 1 && p.dw_part != nullptr;
+    if (one) p.dw_part = p.dw;  // one row of partial sums is the sum
     const dim3 block(static_cast<unsigned>(block_threads(W)));
     switch (W) {
         case 1:
@@ -377,7 +379,7 @@ hipError_t bwd_go(const RowNormParams& p, hipStream_t stream) {
                                p);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.dw_part == nullptr) return e;
+    if (e != hipSuccess || p.dw_part == nullptr || one) return e;
     return launch_column_sums(p.dw_part, static_cast<int>(grid.x),
                               static_cast<int64_t>(p.groups) * p.n, p.dw, stream);
 }

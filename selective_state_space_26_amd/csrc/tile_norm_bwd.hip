@@ -182,11 +182,13 @@ hipError_t tile_bwd_go(TileNormParams p, hipStream_t stream) {
     using Sh = TileShape<T, SB, THREADS>;
     p.tiles = (p.L + Sh::TT - 1) / Sh::TT;
     const unsigned tiles = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles);
+    const bool one = tiles == 1 && p.dw_part != nullptr;
+    if (one) p.dw_part = p.dw;  // one row of partial sums is the sum
     hipLaunchKernelGGL(
         (tile_norm_bwd_kernel<T, FIRST, DOUT_BLD, SB, THREADS, NIT, NL, STREAM, WHOLE>),
         dim3(tiles, static_cast<unsigned>(p.groups)), dim3(THREADS), 0, stream, p);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.dw_part == nullptr) return e;
+    if (e != hipSuccess || p.dw_part == nullptr || one) return e;
     return launch_column_sums(p.dw_part, static_cast<int>(tiles), p.D, p.dw, stream);
 }
 

@@ -14,8 +14,8 @@ import ctypes
 import torch
 
 from . import _lib
-from .norm import _at, _workspace
-from .scan import _dtype_code, _need, _ptr, _stream
+from .norm import _at, _handle, _workspace
+from .scan import _dtype_code, _need
 
 
 def _embed_args(ids, vocab, dim, scale, padding_idx, code, wcode):
@@ -46,7 +46,7 @@ def msel_embed_fwd(ids, weight, scale=1.0, dtype=None, out=None):
     out = (torch.empty(shape, device=dev, dtype=dt) if out is None
            else _need(out, "out", shape, dt, dev))
     a.weight, a.out = weight.data_ptr(), out.data_ptr()
-    _lib.check("msel_embed_fwd", _lib.load().msel_embed_fwd(ctypes.byref(a), _stream(dev)))
+    _lib.check("msel_embed_fwd", _lib.load().msel_embed_fwd(ctypes.byref(a), _handle(dev)))
     return out
 
 
@@ -70,5 +70,5 @@ def msel_embed_bwd(ids, dout, vocab, scale=1.0, base=None, padding_idx=None, dwe
     workspace, size = _workspace(workspace, lib.msel_embed_bwd_workspace_bytes(ctypes.byref(a)),
                                  dev)
     _lib.check("msel_embed_bwd", lib.msel_embed_bwd(ctypes.byref(a), ctypes.byref(g),
-                                                    _ptr(workspace), size, _stream(dev)))
+                                                    _at(workspace), size, _handle(dev)))
     return dweight

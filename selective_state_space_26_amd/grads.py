@@ -7,8 +7,8 @@ import ctypes
 import torch
 
 from . import _lib
-from .norm import _workspace
-from .scan import _dtype_code, _ptr, _stream
+from .norm import _at, _handle, _workspace
+from .scan import _dtype_code
 
 
 class GradList:
@@ -55,7 +55,7 @@ def _call(fn, grads, outs, max_norm, eps, norm, workspace):
     a = _lib.GradArgs(_lib.ABI_VERSION, len(grads.tensors), grads.entries,
                       None if outs is None else outs.entries, max_norm, eps, norm.data_ptr())
     workspace, size = _workspace(workspace, grads.workspace_bytes, dev)
-    _lib.check(fn, getattr(_lib.load(), fn)(ctypes.byref(a), _ptr(workspace), size, _stream(dev)))
+    _lib.check(fn, getattr(_lib.load(), fn)(ctypes.byref(a), _at(workspace), size, _handle(dev)))
     return norm
 
 
