@@ -262,8 +262,8 @@ int msel_checked_build(void);
  * indexes that the kernels met on that device since the last call in *count and, when the
  * count is nonzero, where the first one was: *file (1 scan_fwd.hip, 2 chunk_carry.hip,
  * 3 scan_bwd.hip, 4 conv1d.hip, 5 scan_cplx.hip, 6 scan_cplx_bwd.hip, 7 row_norm.hip,
- * 8 tile_norm.hip, 9 tile_norm_bwd.hip, 10 embed.hip, 11 grads.hip; the first file with a
- * nonzero count) and *line (its source line); 0 and 0 otherwise.  Clears the records.  The
+ * 8 tile_norm.hip, 9 tile_norm_bwd.hip, 10 tile_short.hip, 11 embed.hip, 12 grads.hip; the
+ * first file with a nonzero count) and *line (its source line); 0 and 0 otherwise.  Clears the records.  The
  * release build always reports 0.  MSEL_ERR_NULL if a pointer is NULL, MSEL_ERR_HIP if the
  * runtime fails. */
 msel_status msel_bound_violations(unsigned long long *count, uint32_t *file, uint32_t *line);

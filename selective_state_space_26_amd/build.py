@@ -24,7 +24,7 @@ ARCH = "gfx950"
 
 SOURCES = ["msel_api.cpp", "scan_fwd.hip", "chunk_carry.hip", "scan_bwd.hip", "conv1d.hip",
            "scan_cplx.hip", "scan_cplx_bwd.hip", "lm_api.cpp", "row_norm.hip", "tile_norm.hip",
-           "tile_norm_bwd.hip", "embed.hip", "grads.hip"]
+           "tile_norm_bwd.hip", "tile_short.hip", "embed.hip", "grads.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -150,7 +150,7 @@ size_t gated_ws(const msel_gated_norm_args* a) {
         gated_by_rows(a)
             ? msel::row_norm_partials(static_cast<int64_t>(a->batch) * a->seqlen, a->groups,
                                       a->dim / a->groups, gated_mode(a), bf16, bf16)
-            : msel::tile_norm_partials(a->batch, a->seqlen, bf16);
+            : msel::tile_norm_partials(a->batch, a->groups, a->seqlen, bf16);
     return static_cast<size_t>(parts) * static_cast<size_t>(a->dim) * sizeof(float);
 }
 

@@ -106,6 +106,13 @@ __device__ __forceinline__ void st_part(T* p, const RawVec<T, VE>& r, int valid)
         if (k < valid) Elem<T>::store1(p + k, v[k]);
 }
 
+// Consecutive tiles on one XCD: blocks go to the 8 XCDs in turn, and neighbouring tiles share
+// cache lines wherever a tile's rows do not start and end on one.
+__device__ __forceinline__ unsigned xcd_order(unsigned bid, unsigned n) {
+    const unsigned x = bid & 7u, q = n >> 3, r = n & 7u;
+    return x * q + (x < r ? x : r) + (bid >> 3);
+}
+
 // silu(z) = z sigmoid(z) and its derivative sigmoid(z) (1 + z (1 - sigmoid(z))).
 __device__ __forceinline__ float silu_f(float z) { return z * sigmoid_f(z); }
 __device__ __forceinline__ void silu_grad_f(float z, float& gate, float& slope) {

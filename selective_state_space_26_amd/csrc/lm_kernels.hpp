@@ -58,7 +58,12 @@ struct TileNormParams {
     float* dw;
 };
 // Rows of partial dweight sums that a backward over these sizes may write.
-int64_t tile_norm_partials(int B, int L, bool bf16);
+int64_t tile_norm_partials(int B, int groups, int L, bool bf16);
+// Whether the launch goes to the kernels for few or short tiles (tile_short.hip).
+bool tile_is_short(int B, int groups, int L, bool bf16);
+int64_t tile_short_partials(int B, int groups, int L);
+hipError_t launch_tile_short(const TileNormParams& p, bool gate_first, bool bf16, bool bwd,
+                             hipStream_t stream);
 hipError_t launch_tile_norm_fwd(const TileNormParams& p, bool gate_first, bool bf16,
                                 hipStream_t stream);
 hipError_t launch_tile_norm_bwd(const TileNormParams& p, bool gate_first, bool bf16,
@@ -107,6 +112,7 @@ hipError_t launch_grad_norm(const GradNormParams& p, bool clip, hipStream_t stre
 hipError_t take_bounds_row_norm(BoundsRecord* r);
 hipError_t take_bounds_tile_norm(BoundsRecord* r);
 hipError_t take_bounds_tile_norm_bwd(BoundsRecord* r);
+hipError_t take_bounds_tile_short(BoundsRecord* r);
 hipError_t take_bounds_embed(BoundsRecord* r);
 hipError_t take_bounds_grads(BoundsRecord* r);
 

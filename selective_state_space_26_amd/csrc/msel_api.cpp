@@ -20,6 +20,7 @@ namespace msel {
 __attribute__((weak)) hipError_t take_bounds_row_norm(BoundsRecord* r);
 __attribute__((weak)) hipError_t take_bounds_tile_norm(BoundsRecord* r);
 __attribute__((weak)) hipError_t take_bounds_tile_norm_bwd(BoundsRecord* r);
+__attribute__((weak)) hipError_t take_bounds_tile_short(BoundsRecord* r);
 __attribute__((weak)) hipError_t take_bounds_embed(BoundsRecord* r);
 __attribute__((weak)) hipError_t take_bounds_grads(BoundsRecord* r);
 }  // namespace msel
@@ -625,7 +626,8 @@ msel_status msel_bound_violations(unsigned long long* count, uint32_t* file, uin
                             msel::take_bounds_bwd,       msel::take_bounds_conv,
                             msel::take_bounds_cplx,      msel::take_bounds_cplx_bwd,
                             msel::take_bounds_row_norm,  msel::take_bounds_tile_norm,
-                            msel::take_bounds_tile_norm_bwd, msel::take_bounds_embed,
+                            msel::take_bounds_tile_norm_bwd, msel::take_bounds_tile_short,
+                            msel::take_bounds_embed,
                             msel::take_bounds_grads};
     msel_status s = MSEL_OK;
     for (uint32_t i = 0; i < sizeof(takers) / sizeof(takers[0]); ++i) {

@@ -36,10 +36,10 @@ __device__ __forceinline__ float kept_elem(const RawVec<T, VE>& a, const RawVec<
 // NIT: passes kept in registers, NL: passes after them kept in LDS (a thread's own words; no
 // barrier), STREAM: there may be more, which are read twice.
 template <typename T, bool FIRST, bool OUT_BLD, int SB, int THREADS, int NIT, int NL,
-          bool STREAM, bool WHOLE>
+          bool STREAM>
 __global__ __launch_bounds__(THREADS) void tile_norm_fwd_kernel(TileNormParams p) {
     using Sh = TileShape<T, SB, THREADS>;
-    using Rows = RowLane<T, SB, THREADS, WHOLE>;
+    using Rows = RowLane<T, SB, THREADS>;
     constexpr int VE = Sh::VE, TT = Sh::TT, CPB = Sh::CPB;
     __shared__ float red[Sh::WAVES * TT], rstds[TT];
     __shared__ std::conditional_t<OUT_BLD, TurnTile<T, SB, THREADS>, NoTile> turn[2];
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(THREADS) void tile_norm_fwd_kernel(TileNormParams p
     constexpr int HELD = NIT + NL;
     __shared__ decltype(Vec::w) held[NL > 0 ? NL : 1][2][NL > 0 ? THREADS : 1];
     const int tid = threadIdx.x;
-    const TileLane<T, SB, THREADS, WHOLE> me(p, tid);
+    const TileLane<T, SB, THREADS> me(p, tid);
     const TilePlace<TT> at(p, static_cast<int>(xcd_order(blockIdx.x, gridDim.x)));
     const int c0 = blockIdx.y * p.n;
 
@@ -156,12 +156,12 @@ __global__ __launch_bounds__(THREADS) void tile_norm_fwd_kernel(TileNormParams p
 }
 
 template <typename T, bool FIRST, bool OUT_BLD, int SB, int THREADS, int NIT, int NL,
-          bool STREAM, bool WHOLE = true>
+          bool STREAM>
 hipError_t tile_fwd_go(TileNormParams p, hipStream_t stream) {
     using Sh = TileShape<T, SB, THREADS>;
     p.tiles = (p.L + Sh::TT - 1) / Sh::TT;
     hipLaunchKernelGGL(
-        (tile_norm_fwd_kernel<T, FIRST, OUT_BLD, SB, THREADS, NIT, NL, STREAM, WHOLE>),
+        (tile_norm_fwd_kernel<T, FIRST, OUT_BLD, SB, THREADS, NIT, NL, STREAM>),
         dim3(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles),
              static_cast<unsigned>(p.groups)),
         dim3(THREADS), 0, stream, p);
@@ -175,7 +175,6 @@ hipError_t tile_fwd_width(const TileNormParams& p, hipStream_t stream) {
     // tiles hold twice the channels: 5120 x 65536 538 us against 597.  Narrow groups take smaller
     // blocks, several on a CU: 8 groups of 640 x 65536 399 us against 427.
     constexpr int kBytes = static_cast<int>(sizeof(T));
-    if (p.L < 64 / kBytes) return tile_fwd_go<T, FIRST, OUT_BLD, 64, 256, 0, 0, true, false>(p, stream);
     const bool wide = p.L >= 128 / kBytes && tile_blocks<T, 128>(p) >= kWideBlocks;
     if (wide && p.n <= 64) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 128, 4, 0, false>(p, stream);
     if (wide && p.n <= 640) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 512, 10, 0, false>(p, stream);
@@ -194,8 +193,15 @@ hipError_t tile_fwd(const TileNormParams& p, bool gate_first, hipStream_t stream
 
 }  // namespace
 
+bool tile_is_short(int B, int groups, int L, bool bf16) {
+    const int tt = 64 / (bf16 ? 2 : 4);
+    return L < tt / 4 || static_cast<int64_t>(B) * groups * ((L + tt - 1) / tt) < kFewTiles;
+}
+
 hipError_t launch_tile_norm_fwd(const TileNormParams& p, bool gate_first, bool bf16,
                                 hipStream_t stream) {
+    if (tile_is_short(p.B, p.groups, p.L, bf16))
+        return launch_tile_short(p, gate_first, bf16, false, stream);
     return bf16 ? tile_fwd<bf16_t>(p, gate_first, stream) : tile_fwd<float>(p, gate_first, stream);
 }
 

@@ -21,7 +21,9 @@
 //
 // A last tile that is not full starts early, at seqlen - TT, and does the tokens it shares with
 // the tile before it again (the same values in the same order, so the same bits; the backward
-// leaves them out of dweight).  Only sequences shorter than 64 bytes take partial vectors.
+// leaves them out of dweight).  Within a tile, the last vectors of a sequence shorter than the
+// tile start early in the same way.  Sequences shorter than a vector, and calls with few tiles, go
+// to the kernels of tile_short.hip.
 #pragma once
 
 #include <algorithm>
@@ -42,13 +44,6 @@ struct TileShape {
     static_assert(64 % VL == 0, "whole vectors of tokens");
 };
 
-// Consecutive tiles on one XCD: blocks go to the 8 XCDs in turn, and neighbouring tiles share
-// cache lines wherever a tile's rows do not start and end on one.
-__device__ __forceinline__ unsigned xcd_order(unsigned bid, unsigned n) {
-    const unsigned x = bid & 7u, q = n >> 3, r = n & 7u;
-    return x * q + (x < r ? x : r) + (bid >> 3);
-}
-
 // Blocks of a launch in tiles of SB bytes, and how many make wide tiles worth it: 2048 x 2047
 // x 4 bf16 forward, 128 blocks, took 34 us wide and 22 narrow.
 template <typename T, int SB>
@@ -57,6 +52,8 @@ inline int64_t tile_blocks(const TileNormParams& p) {
     return static_cast<int64_t>(p.B) * p.groups * ((p.L + TT - 1) / TT);
 }
 constexpr int kWideBlocks = 224;
+// Fewer tiles of 64 bytes than this leave most of the chip idle (tile_short.hip).
+constexpr int kFewTiles = 33;
 
 // Element k of a vector as loaded, and the other way round for two neighbours: unlike to_f32 and
 // from_f32 these keep few fp32 values alive.
@@ -152,49 +149,38 @@ struct TilePlace {
 };
 
 // A thread's part of a tile.  Addresses are a block-uniform element plus the thread's offset.
-// WHOLE: seqlen >= TT, every tile is full.
-template <typename T, int SB, int THREADS, bool WHOLE>
+template <typename T, int SB, int THREADS>
 struct TileLane {
     using Sh = TileShape<T, SB, THREADS>;
     static constexpr int VE = Sh::VE;
     int vl, ch;   // vector of the tile's tokens, channel within a pass
-    int64_t off;  // ch * L + vl * VE
+    int early;    // tokens by which the vector starts early (they are the vector before's)
+    int64_t off;  // ch * L + the vector's first token
 
     __device__ __forceinline__ TileLane(const TileNormParams& p, int tid) {
         vl = tid % Sh::VL;
         ch = tid / Sh::VL;
-        off = static_cast<int64_t>(ch) * p.L + vl * VE;
-    }
-    // of this lane's VE tokens
-    __device__ __forceinline__ int valid(const TileNormParams& p) const {
-        return WHOLE ? VE : p.L - vl * VE;
+        early = max(0, (vl + 1) * VE - p.L);
+        off = static_cast<int64_t>(ch) * p.L + vl * VE - early;
     }
     // element of this lane's tokens of channel c + ch of the group that starts at channel c0
     __device__ __forceinline__ int64_t at(const TileNormParams& p, const TilePlace<Sh::TT>& pl,
                                           int c0, int c) const {
         const int64_t first = (static_cast<int64_t>(pl.b) * p.D + c0 + c) * p.L + pl.t0;
-        return MSEL_SPAN(first + off, min(valid(p), VE), static_cast<int64_t>(p.B) * p.D * p.L);
+        return MSEL_SPAN(first + off, VE, static_cast<int64_t>(p.B) * p.D * p.L);
     }
     __device__ __forceinline__ RawVec<T, VE> load(const TileNormParams& p, const void* q,
                                                   const TilePlace<Sh::TT>& pl, int c0,
                                                   int c) const {
         RawVec<T, VE> r;
         r.w = 0;
-        if (c + ch < p.n && (WHOLE || valid(p) > 0)) {
-            const T* from = static_cast<const T*>(q) + at(p, pl, c0, c);
-            if constexpr (WHOLE) r = ld_raw<T, VE>(from);
-            else r = ld_part<T, VE>(from, valid(p));
-        }
+        if (c + ch < p.n) r = ld_raw<T, VE>(static_cast<const T*>(q) + at(p, pl, c0, c));
         return r;
     }
     __device__ __forceinline__ void store(const TileNormParams& p, void* q,
                                           const TilePlace<Sh::TT>& pl, int c0, int c,
                                           const RawVec<T, VE>& r) const {
-        if (c + ch < p.n && (WHOLE || valid(p) > 0)) {
-            T* to = static_cast<T*>(q) + at(p, pl, c0, c);
-            if constexpr (WHOLE) st_raw<T, VE>(to, r);
-            else st_part<T, VE>(to, r, valid(p));
-        }
+        if (c + ch < p.n) st_raw<T, VE>(static_cast<T*>(q) + at(p, pl, c0, c), r);
     }
 };
 
@@ -249,7 +235,7 @@ struct TurnTile {
 struct NoTile {};  // of a kernel that turns nothing
 
 // The thread's group of a pass in [batch, L, D]: VE channels, from c on, of the group at c0.
-template <typename T, int SB, int THREADS, bool WHOLE>
+template <typename T, int SB, int THREADS>
 struct RowLane {
     using Sh = TileShape<T, SB, THREADS>;
     static constexpr int VE = Sh::VE, G = Sh::CPB / VE;
@@ -257,8 +243,9 @@ struct RowLane {
     __device__ __forceinline__ static int64_t at(const TileNormParams& p,
                                                  const TilePlace<Sh::TT>& pl, int c0, int c,
                                                  int tid) {
-        const int64_t i = (static_cast<int64_t>(pl.b) * p.L + pl.t0 + tid / G) * p.D + c0 + c +
-                          tid % G * VE;
+        const int row = tid / G, token = row - max(0, row / VE * VE + VE - p.L);
+        const int64_t i =
+            (static_cast<int64_t>(pl.b) * p.L + pl.t0 + token) * p.D + c0 + c + tid % G * VE;
         return MSEL_SPAN(i, min(p.n - c - tid % G * VE, VE), static_cast<int64_t>(p.B) * p.D * p.L);
     }
     __device__ __forceinline__ static RawVec<T, VE> load(const TileNormParams& p, const void* q,
@@ -267,7 +254,7 @@ struct RowLane {
         const int left = p.n - c - tid % G * VE;
         RawVec<T, VE> r;
         r.w = 0;
-        if (left > 0 && (WHOLE || tid / G < p.L))
+        if (left > 0)
             r = ld_part<T, VE>(static_cast<const T*>(q) + at(p, pl, c0, c, tid), left);
         return r;
     }
@@ -275,7 +262,7 @@ struct RowLane {
                                                  const TilePlace<Sh::TT>& pl, int c0, int c,
                                                  int tid, const RawVec<T, VE>& r) {
         const int left = p.n - c - tid % G * VE;
-        if (left > 0 && (WHOLE || tid / G < p.L))
+        if (left > 0)
             st_part<T, VE>(static_cast<T*>(q) + at(p, pl, c0, c, tid), r, left);
     }
 };

@@ -19,10 +19,10 @@ namespace {
 // NIT: passes kept in registers, NL: passes after them kept in LDS (a thread's own words; no
 // barrier), STREAM: there may be more, which are read twice.
 template <typename T, bool FIRST, bool DOUT_BLD, int SB, int THREADS, int NIT, int NL,
-          bool STREAM, bool WHOLE>
+          bool STREAM>
 __global__ __launch_bounds__(THREADS) void tile_norm_bwd_kernel(TileNormParams p) {
     using Sh = TileShape<T, SB, THREADS>;
-    using Rows = RowLane<T, SB, THREADS, WHOLE>;
+    using Rows = RowLane<T, SB, THREADS>;
     using Vec = RawVec<T, Sh::VE>;
     constexpr int VE = Sh::VE, TT = Sh::TT, CPB = Sh::CPB;
     __shared__ float red[2 * Sh::WAVES * TT];
@@ -31,7 +31,7 @@ __global__ __launch_bounds__(THREADS) void tile_norm_bwd_kernel(TileNormParams p
     constexpr int HELD = NIT + NL;
     __shared__ decltype(Vec::w) held[NL > 0 ? NL : 1][3][NL > 0 ? THREADS : 1];
     const int tid = threadIdx.x;
-    const TileLane<T, SB, THREADS, WHOLE> me(p, tid);
+    const TileLane<T, SB, THREADS> me(p, tid);
     const int tile = static_cast<int>(xcd_order(blockIdx.x, gridDim.x));
     const TilePlace<TT> at(p, tile);
     const int c0 = blockIdx.y * p.n;
@@ -118,6 +118,8 @@ __global__ __launch_bounds__(THREADS) void tile_norm_bwd_kernel(TileNormParams p
     if (tid >= TT && tid < 2 * TT) tok[tid] = tok[tid - TT] * tok[tid - TT] * (s * inv_n);
     __syncthreads();
 
+    // tokens that another tile or vector counts in dweight: those below this place in the tile
+    const int skip = max(at.skip, me.early > 0 ? me.vl * VE + me.early : 0);
     float* part = p.dw_part == nullptr ? nullptr : p.dw_part + static_cast<int64_t>(tile) * p.D + c0;
     const auto emit = [&](int c, const Vec& ax, const Vec& az, const Vec& ad) {
         const float w = weight(c);
@@ -145,7 +147,7 @@ __global__ __launch_bounds__(THREADS) void tile_norm_bwd_kernel(TileNormParams p
                     gz[e] = dy * w * xh * slope;
                     part_t = dy * gate * xh;
                 }
-                dw += t >= at.skip ? part_t : 0.0f;
+                dw += t >= skip ? part_t : 0.0f;
             }
             set_pair(ox, k, gx[0], gx[1]);
             set_pair(oz, k, gz[0], gz[1]);
@@ -177,7 +179,7 @@ __global__ __launch_bounds__(THREADS) void tile_norm_bwd_kernel(TileNormParams p
 }
 
 template <typename T, bool FIRST, bool DOUT_BLD, int SB, int THREADS, int NIT, int NL,
-          bool STREAM, bool WHOLE = true>
+          bool STREAM>
 hipError_t tile_bwd_go(TileNormParams p, hipStream_t stream) {
     using Sh = TileShape<T, SB, THREADS>;
     p.tiles = (p.L + Sh::TT - 1) / Sh::TT;
@@ -185,7 +187,7 @@ hipError_t tile_bwd_go(TileNormParams p, hipStream_t stream) {
     const bool one = tiles == 1 && p.dw_part != nullptr;
     if (one) p.dw_part = p.dw;  // one row of partial sums is the sum
     hipLaunchKernelGGL(
-        (tile_norm_bwd_kernel<T, FIRST, DOUT_BLD, SB, THREADS, NIT, NL, STREAM, WHOLE>),
+        (tile_norm_bwd_kernel<T, FIRST, DOUT_BLD, SB, THREADS, NIT, NL, STREAM>),
         dim3(tiles, static_cast<unsigned>(p.groups)), dim3(THREADS), 0, stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.dw_part == nullptr || one) return e;
@@ -199,7 +201,6 @@ hipError_t tile_bwd_width(const TileNormParams& p, hipStream_t stream) {
     // (8 x 1536 x 2048 from [batch, seqlen, dim]: 72 us against 78).  Narrow groups take smaller
     // blocks, several on a CU (64 x 128 x 4096 fp32: 186 us against 208).
     constexpr int kBytes = static_cast<int>(sizeof(T));
-    if (p.L < 64 / kBytes) return tile_bwd_go<T, FIRST, DOUT_BLD, 64, 256, 0, 0, true, false>(p, stream);
     const bool wide = p.L >= 128 / kBytes && tile_blocks<T, 128>(p) >= kWideBlocks;
     if (wide && p.n <= 64) return tile_bwd_go<T, FIRST, DOUT_BLD, 128, 128, 4, 0, false>(p, stream);
     if (wide && p.n <= 256) return tile_bwd_go<T, FIRST, DOUT_BLD, 128, 512, 4, 0, false>(p, stream);
@@ -219,14 +220,16 @@ hipError_t tile_bwd(const TileNormParams& p, bool gate_first, hipStream_t stream
 
 }  // namespace
 
-int64_t tile_norm_partials(int B, int L, bool bf16) {
-    // the narrowest tiles
-    const int tt = bf16 ? TileShape<bf16_t, 64, 256>::TT : TileShape<float, 64, 256>::TT;
+int64_t tile_norm_partials(int B, int groups, int L, bool bf16) {
+    if (tile_is_short(B, groups, L, bf16)) return tile_short_partials(B, groups, L);
+    const int tt = 64 / (bf16 ? 2 : 4);  // the narrowest tiles
     return static_cast<int64_t>(B) * ((L + tt - 1) / tt);
 }
 
 hipError_t launch_tile_norm_bwd(const TileNormParams& p, bool gate_first, bool bf16,
                                 hipStream_t stream) {
+    if (tile_is_short(p.B, p.groups, p.L, bf16))
+        return launch_tile_short(p, gate_first, bf16, true, stream);
     return bf16 ? tile_bwd<bf16_t>(p, gate_first, stream) : tile_bwd<float>(p, gate_first, stream);
 }
 

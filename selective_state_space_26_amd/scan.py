@@ -473,7 +473,8 @@ def set_ring_spin_limit(polls: int) -> None:
 
 BOUNDS_FILES = {1: "scan_fwd.hip", 2: "chunk_carry.hip", 3: "scan_bwd.hip", 4: "conv1d.hip",
                 5: "scan_cplx.hip", 6: "scan_cplx_bwd.hip", 7: "row_norm.hip",
-                8: "tile_norm.hip", 9: "tile_norm_bwd.hip", 10: "embed.hip", 11: "grads.hip"}
+                8: "tile_norm.hip", 9: "tile_norm_bwd.hip", 10: "tile_short.hip",
+                11: "embed.hip", 12: "grads.hip"}
 
 
 def checked_build() -> bool:
