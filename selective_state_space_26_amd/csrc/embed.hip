@@ -93,7 +93,9 @@ EmbedPlan embed_plan(int64_t tokens, int vocab, int dim) {
 template <typename T, typename TW, int VE>
 __global__ __launch_bounds__(256) void embed_fwd_kernel(EmbedParams p, int nvec, FastDiv by_nvec,
                                                         int block_tokens) {
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * block_tokens;
+    const int64_t t0 =
+        (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * block_tokens;
+    if (t0 >= p.tokens) return;
     const int nt = static_cast<int>(min(static_cast<int64_t>(block_tokens), p.tokens - t0));
     const uint32_t total = static_cast<uint32_t>(nt) * static_cast<uint32_t>(nvec);
     const T* const out0 = static_cast<const T*>(p.out);
@@ -443,9 +445,11 @@ hipError_t embed_fwd_go(const EmbedParams& p, hipStream_t stream) {
     const int nvec = (p.dim + VE - 1) / VE;
     const int block_tokens = std::max(1, 1024 / nvec);
     const int64_t blocks = (p.tokens + block_tokens - 1) / block_tokens;
-    hipLaunchKernelGGL((embed_fwd_kernel<T, TW, VE>), dim3(static_cast<unsigned>(blocks)),
-                       dim3(256), 0, stream, p, nvec, make_fastdiv(static_cast<uint32_t>(nvec)),
-                       block_tokens);
+    const int64_t most = 1 << 23;  // a grid's dimension has fewer than 2^32 threads
+    const dim3 grid(static_cast<unsigned>(std::min(blocks, most)),
+                    static_cast<unsigned>((blocks + most - 1) / most));
+    hipLaunchKernelGGL((embed_fwd_kernel<T, TW, VE>), grid, dim3(256), 0, stream, p, nvec,
+                       make_fastdiv(static_cast<uint32_t>(nvec)), block_tokens);
     return hipGetLastError();
 }
 

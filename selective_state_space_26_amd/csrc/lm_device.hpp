@@ -113,6 +113,16 @@ __device__ __forceinline__ unsigned xcd_order(unsigned bid, unsigned n) {
     return x * q + (x < r ? x : r) + (bid >> 3);
 }
 
+// Tiles over a grid: a grid's dimension has fewer than 2^32 threads, so that tiles beyond kGridX
+// go on along z (the last slice may have blocks without a tile).
+constexpr unsigned kGridX = 1u << 21;
+inline dim3 tile_grid(unsigned tiles, unsigned groups) {
+    return tiles <= kGridX ? dim3(tiles, groups) : dim3(kGridX, groups, (tiles + kGridX - 1) / kGridX);
+}
+__device__ __forceinline__ int tile_of_block() {
+    return static_cast<int>(blockIdx.z * gridDim.x + xcd_order(blockIdx.x, gridDim.x));
+}
+
 // silu(z) = z sigmoid(z) and its derivative sigmoid(z) (1 + z (1 - sigmoid(z))).
 __device__ __forceinline__ float silu_f(float z) { return z * sigmoid_f(z); }
 __device__ __forceinline__ void silu_grad_f(float z, float& gate, float& slope) {

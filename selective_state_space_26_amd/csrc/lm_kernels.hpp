@@ -39,7 +39,7 @@ hipError_t launch_row_norm_bwd(const RowNormParams& p, NormMode mode, bool bf16,
                                hipStream_t stream);
 
 // dw[c] = sum over r of part[r][c], r in order: part is [rows][cols].
-hipError_t launch_column_sums(const float* part, int rows, int64_t cols, float* dw,
+hipError_t launch_column_sums(float* part, int64_t rows, int64_t cols, float* dw,
                               hipStream_t stream);
 
 // The gated norm over the channels of [batch, D, L]; out_bld: out and dout are [batch, L, D].

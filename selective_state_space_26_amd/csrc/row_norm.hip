@@ -9,12 +9,13 @@
 // come from the same registers in one pass.
 //
 // Each value is read once and written once, with a few operations in between, so HBM bounds
-// both kernels.  A row stays in registers between its sum and its output: a team of W
-// wavefronts holds it as kVecs vectors of VE elements per lane, W = 1, 4 or 16 by the row's
-// width (one wavefront needs no barrier, wider rows need the lanes).  Teams walk rows with the
-// grid's stride, so that the weights, and the backward's dweight sums, stay in registers too;
-// a block adds its dweight sums over its teams in LDS and writes one row of partial sums, and a
-// second kernel adds those in a fixed order (no atomics: deterministic).
+// both kernels.  A row stays in registers between its sum and its output: a team of 16, 64, 256 or
+// 1024 lanes holds it as NV vectors of VE elements per lane, by the row's width (up to a wavefront
+// needs no barrier, wider rows need the lanes; narrow rows in small teams leave no lane to work on
+// nothing).  Teams walk rows with the grid's stride, so that the weights, and the backward's
+// dweight sums, stay in registers too; a block adds its dweight sums over its teams in LDS and
+// writes one row of partial sums, and a second kernel adds those in a fixed order (no atomics:
+// deterministic).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -26,51 +27,74 @@ namespace msel {
 
 namespace {
 
-constexpr int kVecs = 4;  // vectors per lane
 // elements per vector: 16 bytes of the wider type; 16 wavefronts (128 VGPRs each) hold 4
 template <typename TA, typename TB>
-constexpr int row_ve(int W) { return sizeof(TA) == 2 && sizeof(TB) == 2 && W < 16 ? 8 : 4; }
+constexpr int row_ve(int team) { return sizeof(TA) == 2 && sizeof(TB) == 2 && team < 1024 ? 8 : 4; }
 
-constexpr int team_threads(int W) { return 64 * W; }
-constexpr int block_threads(int W) { return W == 1 ? 256 : 64 * W; }
-constexpr int block_teams(int W) { return block_threads(W) / team_threads(W); }
+constexpr int block_threads(int team) { return team < 256 ? 256 : team; }
+constexpr int block_teams(int team) { return block_threads(team) / team; }
+
+// Partial rows that one block per 64 columns adds; more are first added in spans (1024 x 768: 5.0
+// us in one launch, 8.6 in two; 4096 x 128: 38 and 9.5).
+constexpr int64_t kSumRows = 2048, kSumSpan = 64;
 
 // Blocks a launch aims for, over all groups: the threads that fit on 256 CUs at once.
-constexpr int grid_target(int W) { return W == 1 ? 2048 : W == 4 ? 2048 : 512; }
-// The backward writes a row of partial sums per block, so it takes fewer.
-constexpr int bwd_grid_target(int W) { return W == 1 ? 1024 : W == 4 ? 1024 : 512; }
+constexpr int grid_target(int team) { return team <= 256 ? 2048 : 512; }
+// The backward writes a row of partial sums per block, so it takes fewer of wide rows.
+constexpr int bwd_grid_target(int team, int vecs) {
+    return vecs == 1 ? 2048 : team <= 256 ? 1024 : 512;
+}
 
-// Sum over a team; red: [2][16] floats of LDS per block (W > 1), alternating between calls so
-// that one barrier per call suffices.
-template <int W>
+// Sum over a team of 16, 64, 256 or 1024 lanes; red: [2][16] floats of LDS per block (several
+// wavefronts), alternating between calls so that one barrier per call suffices.
+template <int TEAM>
 __device__ __forceinline__ float team_sum(float v, float (*red)[16], int& phase) {
+    if constexpr (TEAM == 16) {  // one row of lanes, rotated by 8, 4, 2 and 1
+        const auto rot = [](float x, auto ctrl) {
+            return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x),
+                                                              decltype(ctrl)::value, 0xf, 0xf, true));
+        };
+        v += rot(v, std::integral_constant<int, 0x128>{});
+        v += rot(v, std::integral_constant<int, 0x124>{});
+        v += rot(v, std::integral_constant<int, 0x122>{});
+        v += rot(v, std::integral_constant<int, 0x121>{});
+        return v;
+    }
     v = wave_sum_fused(v);
-    if constexpr (W > 1) {
+    if constexpr (TEAM > 64) {
         const int wave = threadIdx.x >> 6;
         if (lane_id() == 0) red[phase][wave] = v;
         __syncthreads();
         float t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < W; ++i) t += red[phase][i];
+        for (int i = 0; i < TEAM / 64; ++i) t += red[phase][i];
         v = t;
         phase ^= 1;
     }
     return v;
 }
 
-// A team's row: vectors i = lane + k * team for k < kVecs that lie wholly in the row, and the
+// The team of this thread in its block; uniform over a wavefront where a team has one or more.
+template <int TEAM>
+__device__ __forceinline__ int team_index() {
+    if constexpr (block_teams(TEAM) == 1) return 0;
+    const int t = static_cast<int>(threadIdx.x) / TEAM;
+    return TEAM < 64 ? t : __builtin_amdgcn_readfirstlane(t);
+}
+
+// A team's row: vectors i = lane + k * team for k < NV that lie wholly in the row, and the
 // last n % VE elements, one per lane.
-template <typename T, int VE>
+template <typename T, int VE, int NV>
 struct RowRegs {
-    RawVec<T, VE> v[kVecs];
+    RawVec<T, VE> v[NV];
     float tail;
 };
 
-template <typename T, int VE, int TEAM>
-__device__ __forceinline__ void load_row(const T* row, int n, int lane, RowRegs<T, VE>& r) {
+template <int TEAM, typename T, int VE, int NV>
+__device__ __forceinline__ void load_row(const T* row, int n, int lane, RowRegs<T, VE, NV>& r) {
     const int full = n / VE;
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
+    for (int k = 0; k < NV; ++k) {
         const int i = lane + k * TEAM;
         r.v[k].w = 0;
         if (i < full) r.v[k] = ld_raw<T, VE>(row + MSEL_SPAN(i * VE, VE, n));
@@ -78,13 +102,12 @@ __device__ __forceinline__ void load_row(const T* row, int n, int lane, RowRegs<
     r.tail = lane < n - full * VE ? Elem<T>::load1(row + MSEL_IDX(full * VE + lane, n)) : 0.0f;
 }
 
-#define MSEL_FOR_ROW(k) _Pragma("unroll") for (int k = 0; k < kVecs; ++k)
+#define MSEL_FOR_ROW(k) _Pragma("unroll") for (int k = 0; k < NV; ++k)
 
-template <typename TA, typename TB, NormMode MODE, int W>
-__global__ __launch_bounds__(block_threads(W)) void row_norm_fwd_kernel(RowNormParams p) {
-    constexpr int VE = row_ve<TA, TB>(W);
-    constexpr int TEAM = team_threads(W);
-    constexpr int TEAMS = block_teams(W);
+template <typename TA, typename TB, NormMode MODE, int TEAM, int NV>
+__global__ __launch_bounds__(block_threads(TEAM)) void row_norm_fwd_kernel(RowNormParams p) {
+    constexpr int VE = row_ve<TA, TB>(TEAM);
+    constexpr int TEAMS = block_teams(TEAM);
     using TO = std::conditional_t<MODE == NormMode::kResidual, TB, TA>;
     __shared__ float red[2][16];
     int phase = 0;
@@ -94,9 +117,9 @@ __global__ __launch_bounds__(block_threads(W)) void row_norm_fwd_kernel(RowNormP
     const int g = blockIdx.y;
     const float inv_n = 1.0f / static_cast<float>(n);
 
-    RowRegs<float, VE> w;
+    RowRegs<float, VE, NV> w;
     if (p.w != nullptr) {
-        load_row<float, VE, TEAM>(p.w + static_cast<int64_t>(g) * n, n, lane, w);
+        load_row<TEAM>(p.w + static_cast<int64_t>(g) * n, n, lane, w);
     } else {
         MSEL_FOR_ROW(k)
 #pragma unroll
@@ -104,18 +127,18 @@ __global__ __launch_bounds__(block_threads(W)) void row_norm_fwd_kernel(RowNormP
         w.tail = 1.0f;
     }
 
-    // the team index is wave-uniform; W > 1 has one team, so its barriers are block-uniform
-    const int team = TEAMS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM);
+    // a team of several wavefronts is alone in its block, so its barriers are block-uniform
+    const int team = team_index<TEAM>();
     for (int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS + team; r < p.rows;
          r += static_cast<int64_t>(gridDim.x) * TEAMS) {
         const int64_t base = MSEL_SPAN((r * p.groups + g) * n, n, p.rows * p.groups * n);
-        RowRegs<TA, VE> a;
-        RowRegs<TB, VE> b;
-        load_row<TA, VE, TEAM>(static_cast<const TA*>(p.a) + base, n, lane, a);
-        if (p.b != nullptr) load_row<TB, VE, TEAM>(static_cast<const TB*>(p.b) + base, n, lane, b);
+        RowRegs<TA, VE, NV> a;
+        RowRegs<TB, VE, NV> b;
+        load_row<TEAM>(static_cast<const TA*>(p.a) + base, n, lane, a);
+        if (p.b != nullptr) load_row<TEAM>(static_cast<const TB*>(p.b) + base, n, lane, b);
 
-        float v[kVecs][VE], tail;
-        float gate[MODE == NormMode::kGateLast ? kVecs : 1][VE], tgate = 0.0f;
+        float v[NV][VE], tail;
+        float gate[MODE == NormMode::kGateLast ? NV : 1][VE], tgate = 0.0f;
         float sum = 0.0f;
         MSEL_FOR_ROW(k) {
             float av[VE], bv[VE];
@@ -153,7 +176,7 @@ __global__ __launch_bounds__(block_threads(W)) void row_norm_fwd_kernel(RowNormP
             if (lane < n - full * VE) Elem<TO>::store1(so + MSEL_IDX(full * VE + lane, n), tail);
         }
 
-        const float rstd = rstd_of(team_sum<W>(sum, red, phase), inv_n, p.eps);
+        const float rstd = rstd_of(team_sum<TEAM>(sum, red, phase), inv_n, p.eps);
         TA* out = static_cast<TA*>(p.out) + base;
         MSEL_FOR_ROW(k) {
             const int i = lane + k * TEAM;
@@ -214,14 +237,13 @@ __device__ __forceinline__ void bwd_sums(float a, float b, float dy, float w, fl
 }
 
 // TA: a, TB: b; T: dout and dx
-template <typename T, typename TA, typename TB, NormMode MODE, int W>
-__global__ __launch_bounds__(block_threads(W)) void row_norm_bwd_kernel(RowNormParams p) {
-    constexpr int VE = row_ve<TA, T>(W);
-    constexpr int TEAM = team_threads(W);
-    constexpr int TEAMS = block_teams(W);
-    constexpr int ROW = kVecs * VE * TEAM;  // floats of a team's dweight vectors
+template <typename T, typename TA, typename TB, NormMode MODE, int TEAM, int NV>
+__global__ __launch_bounds__(block_threads(TEAM)) void row_norm_bwd_kernel(RowNormParams p) {
+    constexpr int VE = row_ve<TA, T>(TEAM);
+    constexpr int TEAMS = block_teams(TEAM);
+    constexpr int ROW = NV * VE * TEAM;  // floats of a team's dweight vectors
     __shared__ float red[2][16];
-    __shared__ float comb[TEAMS > 1 ? (TEAMS - 1) * (ROW + 64) : 1];
+    __shared__ float comb[TEAMS > 1 ? (TEAMS - 1) * (ROW + TEAM) : 1];
     int phase = 0;
     const int n = p.n;
     const int full = n / VE;
@@ -230,29 +252,29 @@ __global__ __launch_bounds__(block_threads(W)) void row_norm_bwd_kernel(RowNormP
     const int g = blockIdx.y;
     const float inv_n = 1.0f / static_cast<float>(n);
 
-    RowRegs<float, VE> w;
+    RowRegs<float, VE, NV> w;
     if (p.w != nullptr) {
-        load_row<float, VE, TEAM>(p.w + static_cast<int64_t>(g) * n, n, lane, w);
+        load_row<TEAM>(p.w + static_cast<int64_t>(g) * n, n, lane, w);
     } else {
         MSEL_FOR_ROW(k)
 #pragma unroll
         for (int e = 0; e < VE; ++e) w.v[k].w[e] = __float_as_uint(1.0f);
         w.tail = 1.0f;
     }
-    float dw[kVecs][VE] = {}, dwt = 0.0f;
+    float dw[NV][VE] = {}, dwt = 0.0f;
 
-    const int team = TEAMS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM);
+    const int team = team_index<TEAM>();
     for (int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS + team; r < p.rows;
          r += static_cast<int64_t>(gridDim.x) * TEAMS) {
         const int64_t base = MSEL_SPAN((r * p.groups + g) * n, n, p.rows * p.groups * n);
-        RowRegs<TA, VE> a;
-        RowRegs<TB, VE> b;
-        RowRegs<T, VE> dy;
-        load_row<TA, VE, TEAM>(static_cast<const TA*>(p.a) + base, n, lane, a);
-        load_row<T, VE, TEAM>(static_cast<const T*>(p.dout) + base, n, lane, dy);
+        RowRegs<TA, VE, NV> a;
+        RowRegs<TB, VE, NV> b;
+        RowRegs<T, VE, NV> dy;
+        load_row<TEAM>(static_cast<const TA*>(p.a) + base, n, lane, a);
+        load_row<TEAM>(static_cast<const T*>(p.dout) + base, n, lane, dy);
         MSEL_FOR_ROW(k) b.v[k].w = 0;
         b.tail = 0.0f;
-        if (p.b != nullptr) load_row<TB, VE, TEAM>(static_cast<const TB*>(p.b) + base, n, lane, b);
+        if (p.b != nullptr) load_row<TEAM>(static_cast<const TB*>(p.b) + base, n, lane, b);
 
         float sv = 0.0f, sg = 0.0f;
         MSEL_FOR_ROW(k) {
@@ -265,8 +287,8 @@ __global__ __launch_bounds__(block_threads(W)) void row_norm_bwd_kernel(RowNormP
             for (int e = 0; e < VE; ++e) bwd_sums<MODE>(av[e], bv[e], dv[e], wv[e], sv, sg);
         }
         bwd_sums<MODE>(a.tail, b.tail, dy.tail, w.tail, sv, sg);
-        sv = team_sum<W>(sv, red, phase);
-        sg = team_sum<W>(sg, red, phase);
+        sv = team_sum<TEAM>(sv, red, phase);
+        sg = team_sum<TEAM>(sg, red, phase);
         const float rstd = rstd_of(sv, inv_n, p.eps);
         const float c = rstd * rstd * (sg * inv_n);
 
@@ -302,7 +324,7 @@ __global__ __launch_bounds__(block_threads(W)) void row_norm_bwd_kernel(RowNormP
     // the teams' sums, added in team order by team 0
     if constexpr (TEAMS > 1) {
         if (team > 0) {
-            float* mine = comb + (team - 1) * (ROW + 64);
+            float* mine = comb + (team - 1) * (ROW + TEAM);
             MSEL_FOR_ROW(k)
 #pragma unroll
             for (int e = 0; e < VE; ++e)
@@ -313,7 +335,7 @@ __global__ __launch_bounds__(block_threads(W)) void row_norm_bwd_kernel(RowNormP
         if (team > 0) return;
 #pragma unroll
         for (int t = 0; t < TEAMS - 1; ++t) {
-            const float* other = comb + t * (ROW + 64);
+            const float* other = comb + t * (ROW + TEAM);
             MSEL_FOR_ROW(k)
 #pragma unroll
             for (int e = 0; e < VE; ++e) dw[k][e] += other[(k * VE + e) * TEAM + lane];
@@ -328,96 +350,114 @@ __global__ __launch_bounds__(block_threads(W)) void row_norm_bwd_kernel(RowNormP
     if (lane < ntail) out[MSEL_IDX(full * VE + lane, n)] = dwt;
 }
 
-// Wavefronts per row: the fewest that hold it in kVecs vectors per lane.
-int waves_for(int n, int ve) {
-    if (n <= kVecs * ve * 64) return 1;
-    return n <= kVecs * ve * 256 ? 4 : 16;  // 16 hold kMaxNormDim values at any ve
+// Lanes per row and vectors per lane: the fewest that hold it, so that no lane works on vectors
+// beyond it.
+struct RowTeam {
+    int team, vecs;
+};
+RowTeam team_for(int n, int ve) {
+    if (n <= 16 * ve) return {16, 1};
+    if (n <= 64 * ve) return {64, 1};
+    if (n <= 4 * 64 * ve) return {64, 4};
+    return {n <= 4 * 256 * ve ? 256 : 1024, 4};  // 1024 hold kMaxNormDim values at any ve
 }
 
-unsigned grid_of(int64_t rows, int groups, int W, bool bwd) {
-    const int64_t want = (rows + block_teams(W) - 1) / block_teams(W);
-    const int64_t target = std::max(1, (bwd ? bwd_grid_target(W) : grid_target(W)) / groups);
-    return static_cast<unsigned>(std::min(want, target));
+unsigned grid_of(int64_t rows, int groups, RowTeam t, bool bwd) {
+    const int64_t want = (rows + block_teams(t.team) - 1) / block_teams(t.team);
+    const int all = bwd ? bwd_grid_target(t.team, t.vecs) : grid_target(t.team);
+    return static_cast<unsigned>(std::min<int64_t>(want, std::max(1, all / groups)));
+}
+
+// Calls go with the team's lanes and vectors as constants.
+template <typename F>
+void with_team(RowTeam t, F&& go) {
+    using std::integral_constant;
+    if (t.team == 16) return go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+    if (t.team == 64 && t.vecs == 1)
+        return go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    if (t.team == 64) return go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    if (t.team == 256) return go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+    return go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
 template <typename TA, typename TB, NormMode MODE>
 hipError_t fwd_go(const RowNormParams& p, hipStream_t stream) {
-    const int W = waves_for(p.n, row_ve<TA, TB>(1));
-    const dim3 grid(grid_of(p.rows, p.groups, W, false), static_cast<unsigned>(p.groups));
-    const dim3 block(static_cast<unsigned>(block_threads(W)));
-    switch (W) {
-        case 1:
-            hipLaunchKernelGGL((row_norm_fwd_kernel<TA, TB, MODE, 1>), grid, block, 0, stream, p);
-            break;
-        case 4:
-            hipLaunchKernelGGL((row_norm_fwd_kernel<TA, TB, MODE, 4>), grid, block, 0, stream, p);
-            break;
-        default:
-            hipLaunchKernelGGL((row_norm_fwd_kernel<TA, TB, MODE, 16>), grid, block, 0, stream, p);
-    }
+    const RowTeam t = team_for(p.n, row_ve<TA, TB>(64));
+    const dim3 grid(grid_of(p.rows, p.groups, t, false), static_cast<unsigned>(p.groups));
+    with_team(t, [&](auto team, auto vecs) {
+        constexpr int TEAM = decltype(team)::value, NV = decltype(vecs)::value;
+        hipLaunchKernelGGL((row_norm_fwd_kernel<TA, TB, MODE, TEAM, NV>), grid,
+                           dim3(block_threads(TEAM)), 0, stream, p);
+    });
     return hipGetLastError();
 }
 
 template <typename T, typename TA, typename TB, NormMode MODE>
 hipError_t bwd_go(RowNormParams p, hipStream_t stream) {
-    const int W = waves_for(p.n, row_ve<TA, T>(1));
-    const dim3 grid(grid_of(p.rows, p.groups, W, true), static_cast<unsigned>(p.groups));
+    const RowTeam t = team_for(p.n, row_ve<TA, T>(64));
+    const dim3 grid(grid_of(p.rows, p.groups, t, true), static_cast<unsigned>(p.groups));
     const bool one = grid.x == 1 && p.dw_part != nullptr;
     if (one) p.dw_part = p.dw;  // one row of partial sums is the sum
-    const dim3 block(static_cast<unsigned>(block_threads(W)));
-    switch (W) {
-        case 1:
-            hipLaunchKernelGGL((row_norm_bwd_kernel<T, TA, TB, MODE, 1>), grid, block, 0, stream,
-                               p);
-            break;
-        case 4:
-            hipLaunchKernelGGL((row_norm_bwd_kernel<T, TA, TB, MODE, 4>), grid, block, 0, stream,
-                               p);
-            break;
-        default:
-            hipLaunchKernelGGL((row_norm_bwd_kernel<T, TA, TB, MODE, 16>), grid, block, 0, stream,
-                               p);
-    }
-    hipError_t e = hipGetLastError();
+    with_team(t, [&](auto team, auto vecs) {
+        constexpr int TEAM = decltype(team)::value, NV = decltype(vecs)::value;
+        hipLaunchKernelGGL((row_norm_bwd_kernel<T, TA, TB, MODE, TEAM, NV>), grid,
+                           dim3(block_threads(TEAM)), 0, stream, p);
+    });
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.dw_part == nullptr || one) return e;
-    return launch_column_sums(p.dw_part, static_cast<int>(grid.x),
-                              static_cast<int64_t>(p.groups) * p.n, p.dw, stream);
+    return launch_column_sums(p.dw_part, grid.x, static_cast<int64_t>(p.groups) * p.n, p.dw, stream);
 }
 
-// dw[c] = sum_r part[r][c]: a block takes 64 columns, its 16 wavefronts every 16th row each,
-// and their sums are added in wavefront order.
-__global__ __launch_bounds__(1024) void column_sums_kernel(const float* part, int rows,
-                                                           int64_t cols, float* dw) {
+// Sums of `span` rows of part[rows][cols] each, into the first of them (blockIdx.y: which), or of
+// all rows into dw: a block takes 64 columns, its 16 wavefronts every 16th row each, and their
+// sums are added in wavefront order.  Rows are `step` rows of the buffer apart.
+__global__ __launch_bounds__(1024) void column_sums_kernel(float* part, int64_t rows, int64_t step,
+                                                           int64_t span, int64_t cols, float* dw) {
     __shared__ float red[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+    const int64_t r0 = blockIdx.y * span, r1 = min(rows, r0 + span);
     float s = 0.0f;
     if (c < cols) {
 #pragma unroll 8
-        for (int r = wave; r < rows; r += 16)
-            s += part[MSEL_IDX(r * cols + c, static_cast<int64_t>(rows) * cols)];
+        for (int64_t r = r0 + wave; r < r1; r += 16)
+            s += part[MSEL_IDX(r * step * cols + c, ((rows - 1) * step + 1) * cols)];
     }
     red[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && c < cols) {
 #pragma unroll
         for (int i = 1; i < 16; ++i) s += red[i][lane];
-        dw[MSEL_IDX(c, cols)] = s;
+        if (dw != nullptr)
+            dw[MSEL_IDX(c, cols)] = s;
+        else
+            part[MSEL_IDX(r0 * cols + c, rows * cols)] = s;
     }
 }
 
 }  // namespace
 
-hipError_t launch_column_sums(const float* part, int rows, int64_t cols, float* dw,
+hipError_t launch_column_sums(float* part, int64_t rows, int64_t cols, float* dw,
                               hipStream_t stream) {
-    hipLaunchKernelGGL(column_sums_kernel, dim3(static_cast<unsigned>((cols + 63) / 64)),
-                       dim3(1024), 0, stream, part, rows, cols, dw);
+    const unsigned slabs = static_cast<unsigned>((cols + 63) / 64);
+    int64_t step = 1;
+    if (rows > kSumRows) {
+        // many rows under few columns: first over spans of rows, in place
+        const int64_t span = std::max<int64_t>(kSumSpan, (rows + kSumRows - 1) / kSumRows);
+        const int64_t spans = (rows + span - 1) / span;
+        hipLaunchKernelGGL(column_sums_kernel, dim3(slabs, static_cast<unsigned>(spans)), dim3(1024),
+                           0, stream, part, rows, int64_t(1), span, cols, nullptr);
+        step = span;
+        rows = spans;
+    }
+    hipLaunchKernelGGL(column_sums_kernel, dim3(slabs), dim3(1024), 0, stream, part, rows, step,
+                       rows, cols, dw);
     return hipGetLastError();
 }
 
 int row_norm_partials(int64_t rows, int groups, int n, NormMode mode, bool bf16, bool rbf16) {
     const bool narrow = bf16 && (mode != NormMode::kResidual || rbf16);
-    return static_cast<int>(grid_of(rows, groups, waves_for(n, narrow ? 8 : 4), true));
+    return static_cast<int>(grid_of(rows, groups, team_for(n, narrow ? 8 : 4), true));
 }
 
 hipError_t launch_row_norm_fwd(const RowNormParams& p, NormMode mode, bool bf16, bool rbf16,

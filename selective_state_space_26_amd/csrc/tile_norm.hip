@@ -48,7 +48,9 @@ __global__ __launch_bounds__(THREADS) void tile_norm_fwd_kernel(TileNormParams p
     __shared__ decltype(Vec::w) held[NL > 0 ? NL : 1][2][NL > 0 ? THREADS : 1];
     const int tid = threadIdx.x;
     const TileLane<T, SB, THREADS> me(p, tid);
-    const TilePlace<TT> at(p, static_cast<int>(xcd_order(blockIdx.x, gridDim.x)));
+    const int tile = tile_of_block();
+    if (tile >= p.B * p.tiles) return;  // block-uniform
+    const TilePlace<TT> at(p, tile);
     const int c0 = blockIdx.y * p.n;
 
     Vec x[NIT > 0 ? NIT : 1], z[NIT > 0 ? NIT : 1];
@@ -162,8 +164,8 @@ hipError_t tile_fwd_go(TileNormParams p, hipStream_t stream) {
     p.tiles = (p.L + Sh::TT - 1) / Sh::TT;
     hipLaunchKernelGGL(
         (tile_norm_fwd_kernel<T, FIRST, OUT_BLD, SB, THREADS, NIT, NL, STREAM>),
-        dim3(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles),
-             static_cast<unsigned>(p.groups)),
+        tile_grid(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles),
+                  static_cast<unsigned>(p.groups)),
         dim3(THREADS), 0, stream, p);
     return hipGetLastError();
 }

@@ -32,7 +32,8 @@ __global__ __launch_bounds__(THREADS) void tile_norm_bwd_kernel(TileNormParams p
     __shared__ decltype(Vec::w) held[NL > 0 ? NL : 1][3][NL > 0 ? THREADS : 1];
     const int tid = threadIdx.x;
     const TileLane<T, SB, THREADS> me(p, tid);
-    const int tile = static_cast<int>(xcd_order(blockIdx.x, gridDim.x));
+    const int tile = tile_of_block();
+    if (tile >= p.B * p.tiles) return;  // block-uniform
     const TilePlace<TT> at(p, tile);
     const int c0 = blockIdx.y * p.n;
 
@@ -188,10 +189,10 @@ hipError_t tile_bwd_go(TileNormParams p, hipStream_t stream) {
     if (one) p.dw_part = p.dw;  // one row of partial sums is the sum
     hipLaunchKernelGGL(
         (tile_norm_bwd_kernel<T, FIRST, DOUT_BLD, SB, THREADS, NIT, NL, STREAM>),
-        dim3(tiles, static_cast<unsigned>(p.groups)), dim3(THREADS), 0, stream, p);
+        tile_grid(tiles, static_cast<unsigned>(p.groups)), dim3(THREADS), 0, stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.dw_part == nullptr || one) return e;
-    return launch_column_sums(p.dw_part, static_cast<int>(tiles), p.D, p.dw, stream);
+    return launch_column_sums(p.dw_part, tiles, p.D, p.dw, stream);
 }
 
 template <typename T, bool FIRST, bool DOUT_BLD>

@@ -40,7 +40,7 @@ struct ShortPlace {
         C = kThreads / tg;
         t = tid % tg;
         c = tid / tg;
-        tile = static_cast<int>(xcd_order(blockIdx.x, gridDim.x));
+        tile = tile_of_block();
         b = tile / p.tiles;
         t0 = (tile - b * p.tiles) * tg;
         c0 = blockIdx.y * p.n;
@@ -72,6 +72,7 @@ __global__ __launch_bounds__(kThreads) void tile_short_fwd_kernel(TileNormParams
     __shared__ float red[kThreads];
     __shared__ T turn[OUT_BLD ? kThreads * U : 1];
     const ShortPlace me(p, tg);
+    if (me.tile >= p.B * p.tiles) return;  // block-uniform
     [[maybe_unused]] const int64_t elems = static_cast<int64_t>(p.B) * p.D * p.L;
     const T* x = static_cast<const T*>(p.x);
     const T* z = static_cast<const T*>(p.z);
@@ -135,6 +136,7 @@ __global__ __launch_bounds__(kThreads) void tile_short_bwd_kernel(TileNormParams
     __shared__ float dws[kThreads];
     __shared__ T turn[DOUT_BLD ? kThreads * U : 1];
     const ShortPlace me(p, tg);
+    if (me.tile >= p.B * p.tiles) return;  // block-uniform
     [[maybe_unused]] const int64_t elems = static_cast<int64_t>(p.B) * p.D * p.L;
     const T* x = static_cast<const T*>(p.x);
     const T* z = static_cast<const T*>(p.z);
@@ -242,7 +244,7 @@ hipError_t short_go(TileNormParams p, bool bwd, hipStream_t stream) {
     const int tg = short_tokens(p.B, p.groups, p.L);
     p.tiles = (p.L + tg - 1) / tg;
     const unsigned tiles = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles);
-    const dim3 grid(tiles, static_cast<unsigned>(p.groups));
+    const dim3 grid = tile_grid(tiles, static_cast<unsigned>(p.groups));
     if (!bwd) {
         hipLaunchKernelGGL((tile_short_fwd_kernel<T, FIRST, BLD>), grid, dim3(kThreads), 0, stream,
                            p, tg);
@@ -254,7 +256,7 @@ hipError_t short_go(TileNormParams p, bool bwd, hipStream_t stream) {
                        tg);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.dw_part == nullptr || one) return e;
-    return launch_column_sums(p.dw_part, static_cast<int>(tiles), p.D, p.dw, stream);
+    return launch_column_sums(p.dw_part, tiles, p.D, p.dw, stream);
 }
 
 template <typename T>

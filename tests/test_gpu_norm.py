@@ -20,9 +20,10 @@ from lm_helpers import DTYPES, assert_elementwise, assert_sum, host, normal  # n
 from oracle import lm  # noqa: E402
 
 PAIRS = [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")]
-# widths: one element, less than a vector, a vector and its neighbours, the last width of one
-# wavefront a row (1024 and 2048) and the next, of four (4096, 8192) and the next, the largest
-DIMS = [1, 3, 7, 8, 63, 64, 65, 768, 1023, 1024, 1025, 2048, 2049, 4097, 8192, 8195, 16384]
+# widths: one element, less than a vector, a vector and its neighbours, the last width of 16 lanes
+# a row (64 and 128) and the next, of one vector per lane of a wavefront (256 and 512), of four
+# (1024 and 2048), of four wavefronts (4096, 8192), the largest
+DIMS = [1, 3, 7, 8, 63, 64, 65, 128, 131, 255, 257, 512, 513, 768, 1023, 1024, 1025, 2048, 2049, 4097, 8192, 8195, 16384]
 
 
 @pytest.mark.parametrize("dim", DIMS)
