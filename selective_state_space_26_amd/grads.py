@@ -13,11 +13,13 @@ from .scan import _dtype_code
 
 class GradList:
     """The tensors of one model, checked once and kept as the library's list of them (with
-    references to the tensors, so that their memory stays theirs).  A program whose gradients
-    are the same tensors at every step builds it once."""
+    references to the tensors and their storages, so that the listed memory stays theirs).  A
+    program whose gradients are the same tensors at every step builds it once; one that replaces
+    a tensor or its storage builds a new list."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
+        self.storages = []
         self.device = None
         self.entries = (_lib.TensorEntry * len(self.tensors))()
         for i, t in enumerate(self.tensors):
@@ -31,6 +33,7 @@ class GradList:
                 raise ValueError(f"tensor {i} is on {t.device}, expected {self.device}")
             if not t.is_contiguous():
                 raise ValueError(f"tensor {i} must be contiguous")
+            self.storages.append(t.untyped_storage())
             self.entries[i] = _lib.TensorEntry(t.data_ptr(), t.numel(), _dtype_code(t.dtype), 0)
         if self.device is None:
             raise ValueError("a GradList needs at least one tensor")
