@@ -73,14 +73,22 @@ __device__ __forceinline__ RawVec<T, VE> from_f32(const float (&v)[VE]) {
     return r;
 }
 
-template <typename T, int VE>
+// PAST: a store past the caches, for outputs that leave them before anyone reads them anyway
+// (past_cache below).
+template <typename T, int VE, bool PAST = false>
 __device__ __forceinline__ void st_raw(T* p, const RawVec<T, VE>& r) {
-    __builtin_memcpy(p, &r.w, sizeof(r.w));
+    if constexpr (PAST) {
+        typedef typename Words<VE * static_cast<int>(sizeof(T))>::type U
+            __attribute__((aligned(sizeof(T))));
+        __builtin_nontemporal_store(r.w, reinterpret_cast<U*>(p));
+    } else {
+        __builtin_memcpy(p, &r.w, sizeof(r.w));
+    }
 }
 
-template <typename T, int VE>
+template <typename T, int VE, bool PAST = false>
 __device__ __forceinline__ void st_vec(T* p, const float (&v)[VE]) {
-    st_raw<T, VE>(p, from_f32<T, VE>(v));
+    st_raw<T, VE, PAST>(p, from_f32<T, VE>(v));
 }
 
 // The first `valid` of VE elements at p (the rest 0): element by element unless all are valid.
@@ -93,10 +101,10 @@ __device__ __forceinline__ RawVec<T, VE> ld_part(const T* p, int valid) {
     return from_f32<T, VE>(v);
 }
 
-template <typename T, int VE>
+template <typename T, int VE, bool PAST = false>
 __device__ __forceinline__ void st_part(T* p, const RawVec<T, VE>& r, int valid) {
     if (valid >= VE) {
-        st_raw<T, VE>(p, r);
+        st_raw<T, VE, PAST>(p, r);
         return;
     }
     float v[VE];
@@ -105,6 +113,11 @@ __device__ __forceinline__ void st_part(T* p, const RawVec<T, VE>& r, int valid)
     for (int k = 0; k < VE; ++k)
         if (k < valid) Elem<T>::store1(p + k, v[k]);
 }
+
+// Whether an output of so many bytes is stored past the caches: beyond half of the last-level
+// cache (256 MiB) little of it would be there for its reader, and what it pushes out is read again
+// (inputs whose lines are shared by tiles, gradients between norm and scaling).
+inline bool past_cache(int64_t bytes) { return bytes > (int64_t(128) << 20); }
 
 // Consecutive tiles on one XCD: blocks go to the 8 XCDs in turn, and neighbouring tiles share
 // cache lines wherever a tile's rows do not start and end on one.

@@ -36,7 +36,7 @@ __device__ __forceinline__ float kept_elem(const RawVec<T, VE>& a, const RawVec<
 // NIT: passes kept in registers, NL: passes after them kept in LDS (a thread's own words; no
 // barrier), STREAM: there may be more, which are read twice.
 template <typename T, bool FIRST, bool OUT_BLD, int SB, int THREADS, int NIT, int NL,
-          bool STREAM>
+          bool STREAM, bool PAST>
 __global__ __launch_bounds__(THREADS) void tile_norm_fwd_kernel(TileNormParams p) {
     using Sh = TileShape<T, SB, THREADS>;
     using Rows = RowLane<T, SB, THREADS>;
@@ -130,9 +130,9 @@ __global__ __launch_bounds__(THREADS) void tile_norm_fwd_kernel(TileNormParams p
             // one barrier per pass: a buffer is written again two passes later, after the barrier
             // of the pass between, hence after every read of it
             __syncthreads();
-            Rows::store(p, p.out, at, c0, c, tid, turn[i & 1].get_group(tid));
+            Rows::template store<PAST>(p, p.out, at, c0, c, tid, turn[i & 1].get_group(tid));
         } else {
-            me.store(p, p.out, at, c0, c, o);
+            me.template store<PAST>(p, p.out, at, c0, c, o);
         }
     };
 #pragma unroll
@@ -158,16 +158,29 @@ __global__ __launch_bounds__(THREADS) void tile_norm_fwd_kernel(TileNormParams p
 }
 
 template <typename T, bool FIRST, bool OUT_BLD, int SB, int THREADS, int NIT, int NL,
-          bool STREAM>
-hipError_t tile_fwd_go(TileNormParams p, hipStream_t stream) {
+          bool STREAM, bool PAST>
+hipError_t tile_fwd_launch(TileNormParams p, hipStream_t stream) {
     using Sh = TileShape<T, SB, THREADS>;
     p.tiles = (p.L + Sh::TT - 1) / Sh::TT;
     hipLaunchKernelGGL(
-        (tile_norm_fwd_kernel<T, FIRST, OUT_BLD, SB, THREADS, NIT, NL, STREAM>),
+        (tile_norm_fwd_kernel<T, FIRST, OUT_BLD, SB, THREADS, NIT, NL, STREAM, PAST>),
         tile_grid(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles),
                   static_cast<unsigned>(p.groups)),
         dim3(THREADS), 0, stream, p);
     return hipGetLastError();
+}
+
+template <typename T, bool FIRST, bool OUT_BLD, int SB, int THREADS, int NIT, int NL,
+          bool STREAM>
+hipError_t tile_fwd_go(const TileNormParams& p, hipStream_t stream) {
+    // Past the caches where a wavefront stores whole lines (rows, or wide tiles) and a block has a
+    // CU to itself: 5120 x 65536 bf16 515 us with it, 535 without; 8 x 640 x 16384 fp32, in smaller
+    // blocks, 214 and 210.
+    const int64_t bytes = static_cast<int64_t>(p.B) * p.D * p.L * static_cast<int64_t>(sizeof(T));
+    if constexpr (THREADS == 1024 && (OUT_BLD || SB == 128))
+        if (past_cache(bytes))
+            return tile_fwd_launch<T, FIRST, OUT_BLD, SB, THREADS, NIT, NL, STREAM, true>(p, stream);
+    return tile_fwd_launch<T, FIRST, OUT_BLD, SB, THREADS, NIT, NL, STREAM, false>(p, stream);
 }
 
 template <typename T, bool FIRST, bool OUT_BLD>

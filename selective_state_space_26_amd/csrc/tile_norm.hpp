@@ -177,10 +177,11 @@ struct TileLane {
         if (c + ch < p.n) r = ld_raw<T, VE>(static_cast<const T*>(q) + at(p, pl, c0, c));
         return r;
     }
+    template <bool PAST = false>
     __device__ __forceinline__ void store(const TileNormParams& p, void* q,
                                           const TilePlace<Sh::TT>& pl, int c0, int c,
                                           const RawVec<T, VE>& r) const {
-        if (c + ch < p.n) st_raw<T, VE>(static_cast<T*>(q) + at(p, pl, c0, c), r);
+        if (c + ch < p.n) st_raw<T, VE, PAST>(static_cast<T*>(q) + at(p, pl, c0, c), r);
     }
 };
 
@@ -258,12 +259,13 @@ struct RowLane {
             r = ld_part<T, VE>(static_cast<const T*>(q) + at(p, pl, c0, c, tid), left);
         return r;
     }
+    template <bool PAST = false>
     __device__ __forceinline__ static void store(const TileNormParams& p, void* q,
                                                  const TilePlace<Sh::TT>& pl, int c0, int c,
                                                  int tid, const RawVec<T, VE>& r) {
         const int left = p.n - c - tid % G * VE;
         if (left > 0)
-            st_part<T, VE>(static_cast<T*>(q) + at(p, pl, c0, c, tid), r, left);
+            st_part<T, VE, PAST>(static_cast<T*>(q) + at(p, pl, c0, c, tid), r, left);
     }
 };
 

@@ -19,7 +19,7 @@ namespace {
 // NIT: passes kept in registers, NL: passes after them kept in LDS (a thread's own words; no
 // barrier), STREAM: there may be more, which are read twice.
 template <typename T, bool FIRST, bool DOUT_BLD, int SB, int THREADS, int NIT, int NL,
-          bool STREAM>
+          bool STREAM, bool PAST>
 __global__ __launch_bounds__(THREADS) void tile_norm_bwd_kernel(TileNormParams p) {
     using Sh = TileShape<T, SB, THREADS>;
     using Rows = RowLane<T, SB, THREADS>;
@@ -154,8 +154,8 @@ __global__ __launch_bounds__(THREADS) void tile_norm_bwd_kernel(TileNormParams p
             set_pair(oz, k, gz[0], gz[1]);
             one_at_a_time();
         }
-        me.store(p, p.out, at, c0, c, ox);
-        me.store(p, p.dz, at, c0, c, oz);
+        me.template store<PAST>(p, p.out, at, c0, c, ox);
+        me.template store<PAST>(p, p.dz, at, c0, c, oz);
         if (part != nullptr) {
 #pragma unroll
             for (int m = 1; m < Sh::VL; m *= 2) dw += __shfl_xor(dw, m);
@@ -180,19 +180,32 @@ __global__ __launch_bounds__(THREADS) void tile_norm_bwd_kernel(TileNormParams p
 }
 
 template <typename T, bool FIRST, bool DOUT_BLD, int SB, int THREADS, int NIT, int NL,
-          bool STREAM>
-hipError_t tile_bwd_go(TileNormParams p, hipStream_t stream) {
+          bool STREAM, bool PAST>
+hipError_t tile_bwd_launch(TileNormParams p, hipStream_t stream) {
     using Sh = TileShape<T, SB, THREADS>;
     p.tiles = (p.L + Sh::TT - 1) / Sh::TT;
     const unsigned tiles = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles);
     const bool one = tiles == 1 && p.dw_part != nullptr;
     if (one) p.dw_part = p.dw;  // one row of partial sums is the sum
     hipLaunchKernelGGL(
-        (tile_norm_bwd_kernel<T, FIRST, DOUT_BLD, SB, THREADS, NIT, NL, STREAM>),
+        (tile_norm_bwd_kernel<T, FIRST, DOUT_BLD, SB, THREADS, NIT, NL, STREAM, PAST>),
         tile_grid(tiles, static_cast<unsigned>(p.groups)), dim3(THREADS), 0, stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.dw_part == nullptr || one) return e;
     return launch_column_sums(p.dw_part, tiles, p.D, p.dw, stream);
+}
+
+template <typename T, bool FIRST, bool DOUT_BLD, int SB, int THREADS, int NIT, int NL,
+          bool STREAM>
+hipError_t tile_bwd_go(const TileNormParams& p, hipStream_t stream) {
+    // Past the caches in wide tiles with a CU to themselves: 5120 x 16384 bf16 260 us with it, 277
+    // without; 8 x 512 x 16384, in two blocks per CU, 195 and 189, and 8 x 1536 x 8192 in narrow
+    // tiles, whose stores are half lines, 305 and 293.
+    const int64_t bytes = static_cast<int64_t>(p.B) * p.D * p.L * static_cast<int64_t>(sizeof(T));
+    if constexpr (THREADS == 1024 && SB == 128)
+        if (past_cache(2 * bytes))
+            return tile_bwd_launch<T, FIRST, DOUT_BLD, SB, THREADS, NIT, NL, STREAM, true>(p, stream);
+    return tile_bwd_launch<T, FIRST, DOUT_BLD, SB, THREADS, NIT, NL, STREAM, false>(p, stream);
 }
 
 template <typename T, bool FIRST, bool DOUT_BLD>
