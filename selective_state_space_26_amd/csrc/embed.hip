@@ -9,7 +9,8 @@
 //  1. a stable radix sort of (id, position), ids outside [0, vocab) and the padding id last.
 //     Digits of up to 9 bits; a block counts and places a run of consecutive tokens, ranks within
 //     a wavefront by ballots, so that the order is the tokens' own: deterministic.  Up to
-//     kOneBlock tokens are sorted by one block in one launch.  The sort needs few blocks and
+//     kOneBlock tokens are sorted by one block in one launch, and up to kSelfCount by blocks that
+//     each count all of them.  The sort needs few blocks and
 //     waits on latency, so the same launches fill dw (with base or 0) on the remaining CUs;
 //  2. segment sums: the sorted positions in chunks of `seg` entries; a team of lanes adds its
 //     chunk's rows in fp32.  An id's run inside a chunk is written to dw directly; a run that
@@ -33,7 +34,12 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kDigitBits = 9;
 constexpr int kBins = 1 << kDigitBits;
-constexpr int kMaxSortBlocks = 128;
+// Blocks of the sort: every one reads all blocks' counts, so fewer where there are many digits
+// (2^18 tokens of 17 ids: 36.2 us with 128 blocks, 34.8 with 256).
+constexpr int max_sort_blocks(int dbits) { return dbits <= 6 ? 256 : 128; }
+// Up to so many tokens every sort block counts all of them itself, which saves a launch per pass:
+// 8192 tokens of 50257 ids 41 us with it, 49 without; 32768 of 200 ids 33 and 26.
+constexpr int64_t kSelfCount = 8192;
 constexpr int kOneBlock = 2048;  // tokens that one block sorts alone
 constexpr int kFillBlocks = 512;
 constexpr int kSegBatch = 8;     // rows of a chunk in flight at a time
@@ -44,6 +50,7 @@ struct EmbedPlan {
     int passes, dbits, nblocks;
     int chunk;       // tokens per sort block
     int seg, nseg;   // sorted entries per segment-sum chunk, chunks
+    bool self;       // every block counts all tokens' digits itself
     int launches;    // of the sort, each with a share of the fill
     size_t key[2], pos[2], table, partial, bytes;  // offsets into the workspace
 };
@@ -63,10 +70,11 @@ EmbedPlan embed_plan(int64_t tokens, int vocab, int dim) {
     pl.passes = (bits + kDigitBits - 1) / kDigitBits;
     pl.dbits = (bits + pl.passes - 1) / pl.passes;
     const int64_t tiles = (tokens + kSortThreads - 1) / kSortThreads;
-    const int64_t blocks = tokens <= kOneBlock ? 1 : std::min<int64_t>(kMaxSortBlocks, tiles);
+    const int64_t blocks = tokens <= kOneBlock ? 1 : std::min<int64_t>(max_sort_blocks(pl.dbits), tiles);
     pl.chunk = static_cast<int>((tiles + blocks - 1) / blocks * kSortThreads);
     pl.nblocks = static_cast<int>((tokens + pl.chunk - 1) / pl.chunk);
-    pl.launches = pl.nblocks == 1 ? 1 : 2 * pl.passes;
+    pl.self = pl.nblocks > 1 && tokens <= kSelfCount;
+    pl.launches = pl.nblocks == 1 ? 1 : pl.self ? pl.passes : 2 * pl.passes;
     // short chunks while the teams would not fill the chip (a chunk is a team's work), long ones
     // for many rows, which leave fewer partial sums: 2048 x 1024 of 32000 ids took 32 us with 8
     // entries and 40 with 32, 262144 x 64 of 16 ids 48 and 36, 16384 x 768 of 50257 ids 53 with 16
@@ -180,16 +188,20 @@ __global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedParams p
         table[MSEL_IDX(static_cast<int>(blockIdx.x) * nb + d, kBins * pl.nblocks)] = cnt[d];
 }
 
-// Places the tokens of pass `pass` in digit order (stable); a block alone counts them itself and
-// makes all passes.
+// Where a placing block has the counts from: a block alone counts its tokens and makes all passes,
+// of several each counts all tokens itself, or reads the counts of the launch before.
+enum class Counts { kAlone, kSelf, kTable };
+
+// Places the tokens of pass `pass` in digit order (stable).
+template <Counts FROM>
 __global__ __launch_bounds__(kSortThreads) void embed_place_kernel(EmbedParams p, EmbedPlan pl,
                                                                    int pass) {
     __shared__ uint32_t run[kBins];  // next free place of each digit
     __shared__ uint32_t cnt[kSortWaves][kBins];
     __shared__ uint32_t wsum[kSortWaves];
-    const bool alone = pl.nblocks == 1;
+    constexpr bool alone = FROM == Counts::kAlone;
     if (static_cast<int>(blockIdx.x) >= pl.nblocks) {
-        fill_share(p, alone ? 0 : 2 * pass + 1, pl.launches, blockIdx.x - pl.nblocks,
+        fill_share(p, alone ? 0 : FROM == Counts::kSelf ? pass : 2 * pass + 1, pl.launches, blockIdx.x - pl.nblocks,
                    gridDim.x - pl.nblocks);
         return;
     }
@@ -202,9 +214,28 @@ __global__ __launch_bounds__(kSortThreads) void embed_place_kernel(EmbedParams p
         // where this block's tokens of each digit go: all smaller digits, then this digit in the
         // blocks before
         uint32_t total = 0, before = 0;
-        if (alone) {
+        if constexpr (alone) {
             count_digits(p, pl, pass, &cnt[0][0]);
             if (tid < nb) total = cnt[0][tid];
+            __syncthreads();
+        } else if constexpr (FROM == Counts::kSelf) {
+            // the tokens before this block's in rows 0..7 of cnt, the others in 8..15, two
+            // wavefronts a row
+            for (int i = tid; i < kSortWaves * nb; i += kSortThreads)
+                cnt[i >> pl.dbits][i & (nb - 1)] = 0;
+            __syncthreads();
+            const int shift = pass * pl.dbits;
+#pragma unroll 8
+            for (int64_t t = tid; t < p.tokens; t += kSortThreads)
+                atomicAdd(&cnt[(wave & 7) + (t < t0 ? 0 : 8)][(key_at(p, pl, pass, t) >> shift) & mask],
+                          1u);
+            __syncthreads();
+            if (tid < nb)
+#pragma unroll
+                for (int w = 0; w < kSortWaves; ++w) {
+                    total += cnt[w][tid];
+                    before += w < kSortWaves / 2 ? cnt[w][tid] : 0u;
+                }
             __syncthreads();
         } else {
             const uint32_t* table = part_of(p, pl.table);
@@ -476,12 +507,19 @@ hipError_t launch_embed_bwd(const EmbedParams& p, bool bf16, hipStream_t stream)
                                                     kFillBlocks));
     }
     const dim3 grid(static_cast<unsigned>(pl.nblocks + fill));
+    const auto place = [&](auto kernel, int pass) {
+        hipLaunchKernelGGL(kernel, grid, dim3(kSortThreads), 0, stream, p, pl, pass);
+    };
     if (pl.nblocks == 1) {
-        hipLaunchKernelGGL(embed_place_kernel, grid, dim3(kSortThreads), 0, stream, p, pl, 0);
+        place(embed_place_kernel<Counts::kAlone>, 0);
     } else {
         for (int pass = 0; pass < pl.passes; ++pass) {
-            hipLaunchKernelGGL(embed_count_kernel, grid, dim3(kSortThreads), 0, stream, p, pl, pass);
-            hipLaunchKernelGGL(embed_place_kernel, grid, dim3(kSortThreads), 0, stream, p, pl, pass);
+            if (pl.self) {
+                place(embed_place_kernel<Counts::kSelf>, pass);
+            } else {
+                place(embed_count_kernel, pass);
+                place(embed_place_kernel<Counts::kTable>, pass);
+            }
         }
     }
     {
