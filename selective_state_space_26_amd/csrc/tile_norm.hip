@@ -188,12 +188,15 @@ hipError_t tile_fwd_width(const TileNormParams& p, hipStream_t stream) {
     // Wide tiles where the group stays on the CU (n <= 1536 there) and enough of them fill the
     // chip: 8 x 1536 x 2048 bf16 33-36 us against 43 in tiles of 64 bytes.  Beyond that narrow
     // tiles hold twice the channels: 5120 x 65536 538 us against 597.  Narrow groups take smaller
-    // blocks, several on a CU: 8 groups of 640 x 65536 399 us against 427.
+    // blocks, several on a CU: 8 groups of 640 x 65536 399 us against 427; in narrow tiles 2000 x 64
+    // x 17 10 us against 25, 600 x 512 x 17 fp32 13 against 22.
     constexpr int kBytes = static_cast<int>(sizeof(T));
     const bool wide = p.L >= 128 / kBytes && tile_blocks<T, 128>(p) >= kWideBlocks;
     if (wide && p.n <= 64) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 128, 4, 0, false>(p, stream);
     if (wide && p.n <= 640) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 512, 10, 0, false>(p, stream);
     if (wide && p.n <= 1536) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 1024, 9, 3, true>(p, stream);
+    if (p.n <= 256) return tile_fwd_go<T, FIRST, OUT_BLD, 64, 256, 4, 0, false>(p, stream);
+    if (p.n <= 512) return tile_fwd_go<T, FIRST, OUT_BLD, 64, 512, 4, 0, false>(p, stream);
     return tile_fwd_go<T, FIRST, OUT_BLD, 64, 1024, 9, 3, true>(p, stream);
 }
 

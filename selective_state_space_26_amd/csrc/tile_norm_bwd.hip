@@ -213,13 +213,16 @@ hipError_t tile_bwd_width(const TileNormParams& p, hipStream_t stream) {
     // Wide tiles where the group stays on the CU (n <= 768 there) or does not in narrow ones
     // either (5120 x 16384 bf16: 273 us against 337); between the two narrow tiles hold it
     // (8 x 1536 x 2048 from [batch, seqlen, dim]: 72 us against 78).  Narrow groups take smaller
-    // blocks, several on a CU (64 x 128 x 4096 fp32: 186 us against 208).
+    // blocks, several on a CU (64 x 128 x 4096 fp32: 186 us against 208; in narrow tiles 2000 x 64
+    // x 17 bf16: 21 us against 41, 600 x 512 x 17 fp32: 31 against 38).
     constexpr int kBytes = static_cast<int>(sizeof(T));
     const bool wide = p.L >= 128 / kBytes && tile_blocks<T, 128>(p) >= kWideBlocks;
     if (wide && p.n <= 64) return tile_bwd_go<T, FIRST, DOUT_BLD, 128, 128, 4, 0, false>(p, stream);
     if (wide && p.n <= 256) return tile_bwd_go<T, FIRST, DOUT_BLD, 128, 512, 4, 0, false>(p, stream);
     if (wide && (p.n <= 768 || p.n > 1536))
         return tile_bwd_go<T, FIRST, DOUT_BLD, 128, 1024, 4, 2, true>(p, stream);
+    if (p.n <= 256) return tile_bwd_go<T, FIRST, DOUT_BLD, 64, 256, 4, 0, false>(p, stream);
+    if (p.n <= 512) return tile_bwd_go<T, FIRST, DOUT_BLD, 64, 512, 4, 0, false>(p, stream);
     return tile_bwd_go<T, FIRST, DOUT_BLD, 64, 1024, 4, 2, true>(p, stream);
 }
 

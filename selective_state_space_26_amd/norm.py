@@ -147,7 +147,7 @@ def msel_gated_norm_fwd(x, z, weight=None, eps=1e-5, groups=1, gate_first=True, 
     out_layout (default: layout) may be "bld" for "bdl" inputs.  Returns out."""
     a, shape = _gated_args(x, z, weight, eps, groups, gate_first, layout, out_layout or layout)
     dev = x.device
-    out = (torch.empty(shape, device=dev, dtype=x.dtype) if out is None
+    out = (x.new_empty(shape) if out is None
            else _need(out, "out", shape, x.dtype, dev))
     a.out = out.data_ptr()
     _lib.check("msel_gated_norm_fwd",

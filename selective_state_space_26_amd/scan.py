@@ -35,6 +35,9 @@ def _dtype_code(dt: torch.dtype) -> int:
 def _need(t, name, shape, dtype, device):
     if t is None:
         return None
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.device == device and t.is_contiguous()):
+        return t  # the common case, before the checks that say what is wrong
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:

@@ -62,7 +62,8 @@ BWD = [
     (33, 1, 9, "one"), (1000, 16, 64, "uniform"), (1024, 511, 40, "zipf"),
     (1025, 512, 33, "uniform"), (3000, 2000, 96, "outside"), (5000, 70000, 24, "zipf"),
     (40000, 11, 16, "uniform"), (9000, 300000, 3, "zipf"), (4096, 100, 768, "one"),
-    (2048, 50, 1030, "zipf"), (8192, 50, 16, "zipf"), (8193, 900, 12, "outside"), (700, 40, 2500, "outside"), (140000, 3000, 4, "zipf"),
+    (2048, 50, 1030, "zipf"), (8192, 50, 16, "zipf"), (8193, 900, 12, "outside"),
+    (700, 40, 2500, "outside"), (140000, 3000, 4, "zipf"),
 ]
 
 
