@@ -19,6 +19,9 @@
 // No floating-point atomics, and a frequent id costs no more than a rare one.  (Counting a pass's
 // digits with global atomics in the pass before saved a launch and cost 22 us: the most frequent
 // ids' counters are one address each.)
+// Measured: lookup of 16384 x 768, fp32 to bf16, 10 us (44 MB); gradient of 16384 bf16 rows of 50257
+// ids 53 us: 8 + 10 + 8 + 10 for the sort's launches, which the fill of 154 MB bounds, 12 for the
+// segment sums, 8 for the join; of 262144 fp32 rows of 64 for 16 ids 3 + 7, 14 and 10.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -70,7 +73,8 @@ EmbedPlan embed_plan(int64_t tokens, int vocab, int dim) {
     pl.passes = (bits + kDigitBits - 1) / kDigitBits;
     pl.dbits = (bits + pl.passes - 1) / pl.passes;
     const int64_t tiles = (tokens + kSortThreads - 1) / kSortThreads;
-    const int64_t blocks = tokens <= kOneBlock ? 1 : std::min<int64_t>(max_sort_blocks(pl.dbits), tiles);
+    const int64_t blocks =
+        tokens <= kOneBlock ? 1 : std::min<int64_t>(max_sort_blocks(pl.dbits), tiles);
     pl.chunk = static_cast<int>((tiles + blocks - 1) / blocks * kSortThreads);
     pl.nblocks = static_cast<int>((tokens + pl.chunk - 1) / pl.chunk);
     pl.self = pl.nblocks > 1 && tokens <= kSelfCount;
@@ -201,8 +205,8 @@ __global__ __launch_bounds__(kSortThreads) void embed_place_kernel(EmbedParams p
     __shared__ uint32_t wsum[kSortWaves];
     constexpr bool alone = FROM == Counts::kAlone;
     if (static_cast<int>(blockIdx.x) >= pl.nblocks) {
-        fill_share(p, alone ? 0 : FROM == Counts::kSelf ? pass : 2 * pass + 1, pl.launches, blockIdx.x - pl.nblocks,
-                   gridDim.x - pl.nblocks);
+        fill_share(p, alone ? 0 : FROM == Counts::kSelf ? pass : 2 * pass + 1, pl.launches,
+                   blockIdx.x - pl.nblocks, gridDim.x - pl.nblocks);
         return;
     }
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -227,8 +231,9 @@ __global__ __launch_bounds__(kSortThreads) void embed_place_kernel(EmbedParams p
             const int shift = pass * pl.dbits;
 #pragma unroll 8
             for (int64_t t = tid; t < p.tokens; t += kSortThreads)
-                atomicAdd(&cnt[(wave & 7) + (t < t0 ? 0 : 8)][(key_at(p, pl, pass, t) >> shift) & mask],
-                          1u);
+                atomicAdd(
+                    &cnt[(wave & 7) + (t < t0 ? 0 : 8)][(key_at(p, pl, pass, t) >> shift) & mask],
+                    1u);
             __syncthreads();
             if (tid < nb)
 #pragma unroll

@@ -253,7 +253,8 @@ hipError_t launch_grad_norm(const GradNormParams& p, bool clip, hipStream_t stre
                                    p.partials, total);
             else
                 hipLaunchKernelGGL(past ? grad_scale_kernel<true> : grad_scale_kernel<false>,
-                                   dim3(t.chunks), dim3(256), 0, stream, t, p.partials, self ? total : 0, factor, p.max_norm, p.eps, norm);
+                                   dim3(t.chunks), dim3(256), 0, stream, t, p.partials,
+                                   self ? total : 0, factor, p.max_norm, p.eps, norm);
             if (pass == 1) norm = nullptr;  // the first launch writes it
             base += t.chunks;
         }

@@ -16,6 +16,10 @@
 // dweight sums, stay in registers too; a block adds its dweight sums over its teams in LDS and
 // writes one row of partial sums, and a second kernel adds those in a fixed order (no atomics:
 // deterministic).
+// Measured: 16384 x 768 bf16 with an fp32 residual 25 us forward (151 MB) and 34 us backward, 5 more
+// for the sum (201 MB), both at the rate of a copy or above it, as a part is still in the last-level
+// cache; 4099 x 2561 fp32 forward 30 us (168 MB); 200000 x 64 bf16 backward 27 us (128 MB), 152 with
+// a wavefront per row; one row of 768 2.3 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -6,6 +6,9 @@
 // gate's exp and reciprocal are computed once for a pass in registers: gate first keeps v, in the
 // registers of x and z (as many in bf16); gate last keeps x and z, and needs the gate for the
 // output alone.
+// Measured: 5120 x 65536 bf16 to rows 513 us (2.01 GB, 3.9 TB/s; a copy moves 5.1), 8 x 1536 x 2048
+// 34 us (151 MB, 4.4 TB/s).  What is missing is overlap: at these widths a CU holds one tile, whose
+// loads, arithmetic (VALU busy 40% of the time) and stores follow one another.
 #include <hip/hip_runtime.h>
 
 #include "tile_norm.hpp"

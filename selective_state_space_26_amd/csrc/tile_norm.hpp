@@ -10,9 +10,10 @@
 // Rows in [batch, seqlen, dim] are turned through LDS, a pass at a time.
 //
 // A tile's first passes stay in registers and LDS from the sums to the outputs; passes beyond
-// them are read twice.  Reading is faster in wide tiles (two 671 MB tensors of 5120 rows in 221 us at SB = 256, 264 at 128, 306 at
-// 64, 400 at 32), but a wide tile holds fewer channels, and two blocks on a CU, one loading while
-// the other computes, are faster than one of twice the size.  The launchers choose by n.
+// them are read twice.  Reading is faster in wide tiles (two 671 MB tensors of 5120 rows in 221 us
+// at SB = 256, 264 at 128, 306 at 64, 400 at 32), but a wide tile holds fewer channels, and two
+// blocks on a CU, one loading while the other computes, are faster than one of twice the size.
+// The launchers choose by n.
 // Measured and not kept: blocks that walk tiles and load a pass of the next tile as they write
 // one of the current (neighbouring tiles then run apart and no longer share cache lines: 790 us
 // against 650 for the forward of 5120 x 65536 at SB = 32), and two kernels, sums and then outputs

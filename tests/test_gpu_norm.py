@@ -23,7 +23,8 @@ PAIRS = [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")]
 # widths: one element, less than a vector, a vector and its neighbours, the last width of 16 lanes
 # a row (64 and 128) and the next, of one vector per lane of a wavefront (256 and 512), of four
 # (1024 and 2048), of four wavefronts (4096, 8192), the largest
-DIMS = [1, 3, 7, 8, 63, 64, 65, 128, 131, 255, 257, 512, 513, 768, 1023, 1024, 1025, 2048, 2049, 4097, 8192, 8195, 16384]
+DIMS = [1, 3, 7, 8, 63, 64, 65, 128, 131, 255, 257, 512, 513, 768, 1023, 1024,
+        1025, 2048, 2049, 4097, 8192, 8195, 16384]
 
 
 @pytest.mark.parametrize("dim", DIMS)
@@ -105,7 +106,8 @@ LAYOUTS = [("bdl", "bdl"), ("bdl", "bld"), ("bld", "bld")]
 # batch, dim, seqlen, groups: one step; less than a vector of tokens; a tile and its neighbours;
 # channels around a pass of the tile; odd everything; groups of a few channels; more tiles than
 # one batch row; wide
-SHAPES = [(3, 24, 1, 1), (2, 5, 3, 1), (1, 1, 40, 1), (50, 70, 8, 1), (40, 300, 19, 1), (9, 40, 31, 8), (40, 33, 4, 1), (300, 7, 5, 1), (2, 64, 31, 2), (1, 129, 32, 1),
+SHAPES = [(3, 24, 1, 1), (2, 5, 3, 1), (1, 1, 40, 1), (50, 70, 8, 1),
+          (40, 300, 19, 1), (9, 40, 31, 8), (40, 33, 4, 1), (300, 7, 5, 1), (2, 64, 31, 2), (1, 129, 32, 1),
           (2, 130, 33, 1), (1, 1000, 77, 4), (3, 96, 250, 8), (1, 1536, 64, 1), (2, 1537, 70, 1),
           (1, 2050, 65, 2), (1, 5120, 48, 1), (1, 5121, 40, 1), (1, 16384, 36, 1)]
 
