@@ -56,7 +56,7 @@ msel_status check_workspace(const void* ws, size_t have, size_t need) {
 msel_status check_norm(const msel_norm_args* a) {
     if (a == nullptr) return MSEL_ERR_NULL;
     if (a->abi_version != MSEL_ABI_VERSION) return MSEL_ERR_VERSION;
-    if (a->dim < 1 || a->rows < 1 || a->rows > kMaxElems || a->rows * a->dim > kMaxElems)
+    if (a->dim < 1 || a->rows < 1 || a->rows > kMaxElems / a->dim)
         return MSEL_ERR_SHAPE;
     if (!is_dtype(a->dtype) || !is_dtype(a->residual_dtype)) return MSEL_ERR_DTYPE;
     if (a->residual_dtype != a->dtype && a->residual_dtype != MSEL_F32) return MSEL_ERR_DTYPE;
@@ -150,7 +150,7 @@ size_t gated_ws(const msel_gated_norm_args* a) {
         gated_by_rows(a)
             ? msel::row_norm_partials(static_cast<int64_t>(a->batch) * a->seqlen, a->groups,
                                       a->dim / a->groups, gated_mode(a), bf16, bf16)
-            : msel::tile_norm_partials(a->batch, a->groups, a->seqlen, bf16);
+            : msel::tile_norm_partials(a->batch, a->groups, a->dim / a->groups, a->seqlen, bf16);
     return static_cast<size_t>(parts) * static_cast<size_t>(a->dim) * sizeof(float);
 }
 

@@ -58,9 +58,11 @@ struct TileNormParams {
     float* dw;
 };
 // Rows of partial dweight sums that a backward over these sizes may write.
-int64_t tile_norm_partials(int B, int groups, int L, bool bf16);
-// Whether the launch goes to the kernels for few or short tiles (tile_short.hip).
+int64_t tile_norm_partials(int B, int groups, int n, int L, bool bf16);
+// Whether the launch goes to the kernels for few or short tiles (tile_short.hip), and else the
+// bytes of a channel's row in its narrowest tiles.
 bool tile_is_short(int B, int groups, int L, bool bf16);
+int narrow_bytes(int B, int groups, int n, int L, bool bf16);
 int64_t tile_short_partials(int B, int groups, int L);
 hipError_t launch_tile_short(const TileNormParams& p, bool gate_first, bool bf16, bool bwd,
                              hipStream_t stream);

@@ -198,6 +198,8 @@ hipError_t tile_fwd_width(const TileNormParams& p, hipStream_t stream) {
     if (wide && p.n <= 64) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 128, 4, 0, false>(p, stream);
     if (wide && p.n <= 640) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 512, 10, 0, false>(p, stream);
     if (wide && p.n <= 1536) return tile_fwd_go<T, FIRST, OUT_BLD, 128, 1024, 9, 3, true>(p, stream);
+    if (narrow_bytes(p.B, p.groups, p.n, p.L, kBytes == 2) == 32)
+        return tile_fwd_go<T, FIRST, OUT_BLD, 32, 1024, 9, 3, true>(p, stream);
     if (p.n <= 256) return tile_fwd_go<T, FIRST, OUT_BLD, 64, 256, 4, 0, false>(p, stream);
     if (p.n <= 512) return tile_fwd_go<T, FIRST, OUT_BLD, 64, 512, 4, 0, false>(p, stream);
     return tile_fwd_go<T, FIRST, OUT_BLD, 64, 1024, 9, 3, true>(p, stream);
@@ -217,6 +219,12 @@ hipError_t tile_fwd(const TileNormParams& p, bool gate_first, hipStream_t stream
 bool tile_is_short(int B, int groups, int L, bool bf16) {
     const int tt = 64 / (bf16 ? 2 : 4);
     return L < tt / 4 || static_cast<int64_t>(B) * groups * ((L + tt - 1) / tt) < kFewTiles;
+}
+
+int narrow_bytes(int B, int groups, int n, int L, bool bf16) {
+    const int tt = 64 / (bf16 ? 2 : 4);
+    const int64_t tiles = static_cast<int64_t>(B) * groups * ((L + tt - 1) / tt);
+    return n > kHalfWidth && tiles < kHalfTiles ? 32 : 64;
 }
 
 hipError_t launch_tile_norm_fwd(const TileNormParams& p, bool gate_first, bool bf16,

@@ -53,8 +53,14 @@ inline int64_t tile_blocks(const TileNormParams& p) {
     return static_cast<int64_t>(p.B) * p.groups * ((p.L + TT - 1) / TT);
 }
 constexpr int kWideBlocks = 224;
-// Fewer tiles of 64 bytes than this leave most of the chip idle (tile_short.hip).
-constexpr int kFewTiles = 33;
+// Fewer tiles of 64 bytes than this go to tile_short.hip (1 x 8192 x 31 bf16, one tile, backward:
+// 36 us there, 63 in tiles of 32; 1 x 5120 x 250, 8 tiles: 56 and 46).
+constexpr int kFewTiles = 6;
+// With fewer tiles of 64 bytes than this, wide groups go in tiles of 32: neighbouring tiles share
+// lines, and run on one XCD (5120 x 4096 bf16, 128 tiles of 64: forward 63 us, 48 in tiles of 32,
+// backward 119 and 89; 2560 x 6000, 188 tiles: 21 and 27, 50 and 64).
+constexpr int kHalfTiles = 160;
+constexpr int kHalfWidth = 512;
 
 // Element k of a vector as loaded, and the other way round for two neighbours: unlike to_f32 and
 // from_f32 these keep few fp32 values alive.

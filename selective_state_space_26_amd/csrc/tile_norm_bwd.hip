@@ -189,6 +189,10 @@ hipError_t tile_bwd_launch(TileNormParams p, hipStream_t stream) {
     p.tiles = (p.L + Sh::TT - 1) / Sh::TT;
     const unsigned tiles = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles);
     const bool one = tiles == 1 && p.dw_part != nullptr;
+    // the workspace has a row of partial sums for every tile
+    if (p.dw_part != nullptr &&
+        tiles > tile_norm_partials(p.B, p.groups, p.n, p.L, sizeof(T) == 2))
+        return hipErrorInvalidValue;
     if (one) p.dw_part = p.dw;  // one row of partial sums is the sum
     hipLaunchKernelGGL(
         (tile_norm_bwd_kernel<T, FIRST, DOUT_BLD, SB, THREADS, NIT, NL, STREAM, PAST>),
@@ -224,6 +228,8 @@ hipError_t tile_bwd_width(const TileNormParams& p, hipStream_t stream) {
     if (wide && p.n <= 256) return tile_bwd_go<T, FIRST, DOUT_BLD, 128, 512, 4, 0, false>(p, stream);
     if (wide && (p.n <= 768 || p.n > 1536))
         return tile_bwd_go<T, FIRST, DOUT_BLD, 128, 1024, 4, 2, true>(p, stream);
+    if (narrow_bytes(p.B, p.groups, p.n, p.L, kBytes == 2) == 32)
+        return tile_bwd_go<T, FIRST, DOUT_BLD, 32, 1024, 4, 2, true>(p, stream);
     if (p.n <= 256) return tile_bwd_go<T, FIRST, DOUT_BLD, 64, 256, 4, 0, false>(p, stream);
     if (p.n <= 512) return tile_bwd_go<T, FIRST, DOUT_BLD, 64, 512, 4, 0, false>(p, stream);
     return tile_bwd_go<T, FIRST, DOUT_BLD, 64, 1024, 4, 2, true>(p, stream);
@@ -240,9 +246,9 @@ hipError_t tile_bwd(const TileNormParams& p, bool gate_first, hipStream_t stream
 
 }  // namespace
 
-int64_t tile_norm_partials(int B, int groups, int L, bool bf16) {
+int64_t tile_norm_partials(int B, int groups, int n, int L, bool bf16) {
     if (tile_is_short(B, groups, L, bf16)) return tile_short_partials(B, groups, L);
-    const int tt = 64 / (bf16 ? 2 : 4);  // the narrowest tiles
+    const int tt = narrow_bytes(B, groups, n, L, bf16) / (bf16 ? 2 : 4);
     return static_cast<int64_t>(B) * ((L + tt - 1) / tt);
 }
 

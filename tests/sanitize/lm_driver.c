@@ -72,6 +72,8 @@ static void norm(void) {
     N(rows, INT64_MIN, MSEL_ERR_SHAPE);
     N(rows, INT64_MAX, MSEL_ERR_SHAPE);
     N(rows, (int64_t)1 << 40, MSEL_ERR_SHAPE);
+    WITH(msel_norm_args, a, rows, (int64_t)1 << 40,
+         (x.dim = INT32_MAX, msel_norm_fwd(&x, NULL)), MSEL_ERR_SHAPE);
     N(dtype, 2, MSEL_ERR_DTYPE);
     N(residual_dtype, -1, MSEL_ERR_DTYPE);
     for (int i = 0; i < 2; ++i) N(eps, bad_floats[i], MSEL_ERR_SHAPE);

@@ -107,7 +107,8 @@ LAYOUTS = [("bdl", "bdl"), ("bdl", "bld"), ("bld", "bld")]
 # channels around a pass of the tile; odd everything; groups of a few channels; more tiles than
 # one batch row; wide
 SHAPES = [(3, 24, 1, 1), (2, 5, 3, 1), (1, 1, 40, 1), (50, 70, 8, 1),
-          (40, 300, 19, 1), (9, 40, 31, 8), (40, 33, 4, 1), (300, 7, 5, 1), (2, 64, 31, 2), (1, 129, 32, 1),
+          (40, 300, 19, 1), (9, 40, 31, 8), (40, 33, 4, 1), (300, 7, 5, 1), (2, 64, 31, 2),
+          (40, 600, 40, 1), (3, 1030, 700, 1), (17, 1040, 70, 2), (37, 5121, 9, 1), (1, 129, 32, 1),
           (2, 130, 33, 1), (1, 1000, 77, 4), (3, 96, 250, 8), (1, 1536, 64, 1), (2, 1537, 70, 1),
           (1, 2050, 65, 2), (1, 5120, 48, 1), (1, 5121, 40, 1), (1, 16384, 36, 1)]
 
