@@ -70,6 +70,12 @@ CASES = {
     "gated_odd": lambda: _gated(2, 1537, 77, 1, "bf16", True, "bdl", "bld"),
     "gated_groups": lambda: _gated(1, 1000, 133, 4, "f32", False, "bdl", "bdl"),
     "gated_wide": lambda: _gated(1, 5121, 65, 1, "bf16", True, "bdl", "bld"),
+    "gated_half_tiles": lambda: _gated(3, 1030, 700, 1, "bf16", True, "bdl", "bld"),
+    "gated_half_tiles_f32": lambda: _gated(40, 1201, 21, 1, "f32", False, "bdl", "bdl"),
+    "gated_small_blocks": lambda: _gated(300, 300, 19, 1, "bf16", True, "bdl", "bld"),
+    "norm_narrow": lambda: _norm(5000, 20, "bf16", "bf16"),
+    "embed_self_count": lambda: _embed(5000, 3000, 24, "bf16"),
+    "embed_many_blocks": lambda: _embed(270000, 16, 8, "f32"),
     "gated_narrow_wide_tiles": lambda: _gated(3, 40, 5000, 1, "bf16", True, "bdl", "bld"),
     "gated_wide_tiles": lambda: _gated(1, 1601, 14500, 1, "bf16", True, "bdl", "bld"),
     "gated_wide_tiles_groups": lambda: _gated(2, 2400, 1000, 8, "f32", False, "bdl", "bdl"),
@@ -94,3 +100,40 @@ def test_in_range_and_equal_to_release(name):
         assert count == 0, f"{count} out-of-range indexes, the first at {f}:{line}"
     for a, b in zip(ref, got):
         assert torch.equal(a, b)
+
+
+WORKSPACES = {
+    "gated": lambda b, d, L, g, t, w: msel.msel_gated_norm_bwd(
+        *(normal((b, d, L), t, i) for i in (1, 2)), None, normal((b, L, d), t, 3), 1e-5, g, True,
+        "bdl", "bld", workspace=w),
+    "norm": lambda b, d, L, g, t, w: msel.msel_norm_bwd(
+        normal((b * L, d), "f32", 1), None, normal((b * L, d), t, 2), workspace=w),
+    "embed": lambda b, d, L, g, t, w: msel.msel_embed_bwd(
+        torch.arange(b * L, device="cuda") % (b + g), normal((b * L, d), t, 2), b + g, workspace=w),
+}
+# few and many tiles of every width, short sequences, narrow and wide groups
+SIZES = [(3, 1030, 700, 1), (40, 600, 40, 1), (30, 1030, 40, 2), (60, 520, 9, 1), (1, 1536, 300, 1),
+         (2, 700, 3, 1), (600, 24, 17, 2), (9, 2000, 130, 4), (5, 520, 1500, 1), (230, 70, 64, 1)]
+
+
+@pytest.mark.parametrize("op", list(WORKSPACES))
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nothing_is_written_behind_the_workspace(op, dtype):
+    guard = 1 << 20
+    for size in SIZES:
+        log(f"workspace {op} {dtype} {size}")
+        asked = []
+
+        def ask(workspace, need, dev):
+            asked.append(need)
+            buf = torch.full((need + guard,), 0x5A, device=dev, dtype=torch.uint8)
+            asked.append(buf)
+            return buf, need  # the library is told of the size that it asked for
+
+        with pytest.MonkeyPatch.context() as m:
+            for mod in ("norm", "embed"):
+                m.setattr(f"selective_state_space_26_amd.{mod}._workspace", ask)
+            WORKSPACES[op](*size, dtype, None)
+        torch.cuda.synchronize()
+        need, buf = asked
+        assert need > 0 and bool((buf[need:] == 0x5A).all()), size
