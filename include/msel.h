@@ -75,7 +75,8 @@ typedef enum {
     MSEL_ERR_HIP = 8,         /* the HIP runtime reported an error at launch               */
     MSEL_ERR_VERSION = 9,     /* args->abi_version != MSEL_ABI_VERSION                     */
     MSEL_ERR_TOO_LARGE = 10   /* msel_scan_bwd_noalloc: the problem's workspace would exceed */
-                              /* MSEL_NOALLOC_SCRATCH_BYTES                                 */
+                              /* MSEL_NOALLOC_SCRATCH_BYTES; msel_grad_clip: no host memory  */
+                              /* to compare a long list's addresses                         */
 } msel_status;
 
 typedef enum { MSEL_F32 = 0, MSEL_BF16 = 1 } msel_dtype;
@@ -644,7 +645,9 @@ typedef struct {
     int32_t count;          /* 0..MSEL_MAX_GRAD_TENSORS                                    */
     const msel_tensor *tensors; /* required when count > 0                                 */
     const msel_tensor *outs;/* clip: where each scaled tensor goes, numel and dtype as in
-                               tensors; may equal tensors, or its data the same (in place) */
+                               tensors; may equal tensors, or its data the same (in place).
+                               Nothing else may share memory with it: no other entry of either
+                               list (so nothing is listed twice), not norm, not the workspace */
     float max_norm;         /* clip: >= 0 (infinity: no bound)                              */
     float eps;              /* clip: >= 0                                                  */
     float *norm;            /* required output [1]                                         */
@@ -652,6 +655,8 @@ typedef struct {
 
 msel_status msel_validate_grad_norm(const msel_grad_args *args, const void *workspace,
                                     size_t workspace_bytes);
+/* Refuses equal addresses (MSEL_ERR_ALIAS); msel_grad_clip itself also refuses ranges that
+ * overlap in part. */
 msel_status msel_validate_grad_clip(const msel_grad_args *args, const void *workspace,
                                     size_t workspace_bytes);
 /* Bytes of workspace the two entry points need (partial sums; 0 for invalid arguments). */

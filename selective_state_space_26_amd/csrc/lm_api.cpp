@@ -2,12 +2,15 @@
 // include/msel.h: the norms, the embedding, the gradient norm and clipping.
 //
 // As in msel_api.cpp, every entry point validates its arguments on the host (no HIP call, no
-// device memory touched) and only then enqueues kernels on the caller's stream; nothing is
-// allocated, kept between calls or synchronized.
+// device memory touched) and only then enqueues kernels on the caller's stream; no device memory
+// is allocated, and nothing is kept between calls or synchronized.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <new>
 
 #include "lm_kernels.hpp"
 #include "msel.h"
@@ -213,6 +216,56 @@ msel_status check_grads(const msel_grad_args* a) {
     return MSEL_OK;
 }
 
+// A stretch of memory; ranges by their addresses.
+struct Range {
+    uintptr_t begin, end;
+    bool operator<(const Range& o) const { return begin < o.begin; }
+    bool meets(const Range& o) const { return begin < o.end && o.begin < end; }
+};
+constexpr size_t kStackRanges = 1024;  // longer lists take the host's heap
+
+// Whether something that clipping writes (a destination, norm, the workspace) shares memory with
+// anything else that it reads or writes; a destination may be its own entry's source.  The blocks
+// of a launch scale their chunks in no order, so such calls would have no one result.  whole: the
+// ranges are the tensors' bytes; else their first ones, which finds equal addresses alone.
+// In the order of addresses, a range meets an earlier one if it begins below the largest end so
+// far.  Lists are mostly in that order already, and are sorted only where they are not.
+msel_status check_overlap(const msel_grad_args* a, const void* ws, size_t ws_bytes, bool whole) {
+    Range stack[kStackRanges];
+    const size_t most = 2 * static_cast<size_t>(a->count);
+    Range* const heap = most > kStackRanges ? new (std::nothrow) Range[most] : nullptr;
+    if (most > kStackRanges && heap == nullptr) return MSEL_ERR_TOO_LARGE;
+    const auto range = [&](const void* p, size_t bytes) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        return Range{at, at + (whole ? bytes : 1)};
+    };
+    // destinations from the front, the sources that are none from the middle
+    Range* const dst = heap != nullptr ? heap : stack;
+    Range* const src = dst + a->count;
+    size_t nd = 0, ns = 0;
+    for (int32_t i = 0; i < a->count; ++i) {
+        const msel_tensor& t = a->tensors[i];
+        if (t.numel == 0) continue;
+        const size_t bytes = static_cast<size_t>(t.numel) * (t.dtype == MSEL_BF16 ? 2 : 4);
+        dst[nd++] = range(a->outs[i].data, bytes);
+        if (t.data != a->outs[i].data) src[ns++] = range(t.data, bytes);
+    }
+    if (!std::is_sorted(dst, dst + nd)) std::sort(dst, dst + nd);
+    if (!std::is_sorted(src, src + ns)) std::sort(src, src + ns);
+    const Range norm = range(a->norm, sizeof(float)), work = range(ws, ws_bytes);
+    bool meet = norm.meets(work);
+    uintptr_t any = 0, written = 0;  // the largest ends so far
+    for (size_t i = 0, j = 0; (i < nd || j < ns) && !meet;) {
+        const bool out = j == ns || (i < nd && dst[i] < src[j]);
+        const Range& r = out ? dst[i++] : src[j++];
+        meet = r.begin < (out ? any : written) || r.meets(norm) || r.meets(work);
+        any = std::max(any, r.end);
+        if (out) written = std::max(written, r.end);
+    }
+    delete[] heap;
+    return meet ? MSEL_ERR_ALIAS : MSEL_OK;
+}
+
 msel::GradNormParams grad_params(const msel_grad_args* a, void* ws) {
     msel::GradNormParams p{};
     p.count = a->count;
@@ -224,6 +277,39 @@ msel::GradNormParams grad_params(const msel_grad_args* a, void* ws) {
     p.norm = a->norm;
     p.partials = static_cast<double*>(ws);
     return p;
+}
+
+size_t grad_ws(const msel_grad_args* a) {
+    // one more for the scaling factor
+    return static_cast<size_t>(msel::grad_partials(grad_params(a, nullptr)) + 1) * sizeof(double);
+}
+
+msel_status check_norm_call(const msel_grad_args* a, const void* ws, size_t ws_bytes, size_t& need) {
+    const msel_status s = check_grads(a);
+    if (s != MSEL_OK) return s;
+    if (a->norm == nullptr) return MSEL_ERR_NULL;
+    if (!aligned(a->norm, 4)) return MSEL_ERR_ALIGN;
+    for (int32_t i = 0; i < a->count; ++i)
+        if (a->tensors[i].numel > 0 &&
+            (a->tensors[i].data == a->norm || a->tensors[i].data == ws))
+            return MSEL_ERR_ALIAS;
+    need = grad_ws(a);
+    return check_workspace(ws, ws_bytes, need);
+}
+
+msel_status check_clip_call(const msel_grad_args* a, const void* ws, size_t ws_bytes, bool whole) {
+    size_t need = 0;
+    const msel_status s = check_norm_call(a, ws, ws_bytes, need);
+    if (s != MSEL_OK) return s;
+    if (!not_negative(a->max_norm) || !not_negative(a->eps)) return MSEL_ERR_SHAPE;
+    if (a->count > 0 && a->outs == nullptr) return MSEL_ERR_NULL;
+    for (int32_t i = 0; i < a->count; ++i) {
+        const msel_status t = check_tensor(a->outs[i]);
+        if (t != MSEL_OK) return t;
+        if (a->outs[i].numel != a->tensors[i].numel) return MSEL_ERR_SHAPE;
+        if (a->outs[i].dtype != a->tensors[i].dtype) return MSEL_ERR_DTYPE;
+    }
+    return check_overlap(a, ws, need, whole);
 }
 
 }  // namespace
@@ -431,39 +517,18 @@ msel_status msel_embed_bwd(const msel_embed_args* a, const msel_embed_grads* g, 
 }
 
 size_t msel_grad_workspace_bytes(const msel_grad_args* a) {
-    if (check_grads(a) != MSEL_OK) return 0;
-    // one more for the scaling factor
-    return static_cast<size_t>(msel::grad_partials(grad_params(a, nullptr)) + 1) * sizeof(double);
+    return check_grads(a) == MSEL_OK ? grad_ws(a) : 0;
 }
 
 msel_status msel_validate_grad_norm(const msel_grad_args* a, const void* workspace,
                                     size_t workspace_bytes) {
-    const msel_status s = check_grads(a);
-    if (s != MSEL_OK) return s;
-    if (a->norm == nullptr) return MSEL_ERR_NULL;
-    if (!aligned(a->norm, 4)) return MSEL_ERR_ALIGN;
-    for (int32_t i = 0; i < a->count; ++i)
-        if (a->tensors[i].numel > 0 &&
-            (a->tensors[i].data == a->norm || a->tensors[i].data == workspace))
-            return MSEL_ERR_ALIAS;
-    return check_workspace(workspace, workspace_bytes, msel_grad_workspace_bytes(a));
+    size_t need = 0;
+    return check_norm_call(a, workspace, workspace_bytes, need);
 }
 
 msel_status msel_validate_grad_clip(const msel_grad_args* a, const void* workspace,
                                     size_t workspace_bytes) {
-    const msel_status s = msel_validate_grad_norm(a, workspace, workspace_bytes);
-    if (s != MSEL_OK) return s;
-    if (!not_negative(a->max_norm) || !not_negative(a->eps)) return MSEL_ERR_SHAPE;
-    if (a->count > 0 && a->outs == nullptr) return MSEL_ERR_NULL;
-    for (int32_t i = 0; i < a->count; ++i) {
-        const msel_status t = check_tensor(a->outs[i]);
-        if (t != MSEL_OK) return t;
-        if (a->outs[i].numel != a->tensors[i].numel) return MSEL_ERR_SHAPE;
-        if (a->outs[i].dtype != a->tensors[i].dtype) return MSEL_ERR_DTYPE;
-        if (a->outs[i].numel > 0 && (a->outs[i].data == a->norm || a->outs[i].data == workspace))
-            return MSEL_ERR_ALIAS;
-    }
-    return MSEL_OK;
+    return check_clip_call(a, workspace, workspace_bytes, false);
 }
 
 msel_status msel_grad_norm(const msel_grad_args* a, void* workspace, size_t workspace_bytes,
@@ -479,7 +544,7 @@ msel_status msel_grad_norm(const msel_grad_args* a, void* workspace, size_t work
 
 msel_status msel_grad_clip(const msel_grad_args* a, void* workspace, size_t workspace_bytes,
                            hipStream_t stream) {
-    const msel_status s = msel_validate_grad_clip(a, workspace, workspace_bytes);
+    const msel_status s = check_clip_call(a, workspace, workspace_bytes, true);
     if (s != MSEL_OK) return s;
     return hip_status(msel::launch_grad_norm(grad_params(a, workspace), true, stream));
 }

@@ -228,7 +228,7 @@ const char* msel_status_string(msel_status s) {
         case MSEL_ERR_VERSION: return "MSEL_ERR_VERSION: ABI version or reserved field mismatch";
         case MSEL_ERR_TOO_LARGE:
             return "MSEL_ERR_TOO_LARGE: the problem needs more than the library's static scratch "
-                   "(MSEL_NOALLOC_SCRATCH_BYTES)";
+                   "(MSEL_NOALLOC_SCRATCH_BYTES), or host memory for a list";
     }
     return "MSEL_ERR_UNKNOWN";
 }

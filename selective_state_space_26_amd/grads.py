@@ -71,7 +71,9 @@ def msel_grad_norm(grads, norm=None, workspace=None):
 def msel_grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=None):
     """Scales every tensor by min(1, max_norm / (norm + eps)), in place or into `out` (a GradList
     or tensors of the same sizes and dtypes), and returns the norm before scaling as
-    msel_grad_norm does.  Nothing is read back: a norm that is not finite is in the result."""
+    msel_grad_norm does.  Nothing is read back: a norm that is not finite is in the result.
+    What is written shares no memory with anything else: a tensor listed twice, views that
+    overlap or another entry's tensor in `out` are refused."""
     grads = _as_list(grads)
     outs = grads if out is None else _as_list(out)
     if len(outs) != len(grads):

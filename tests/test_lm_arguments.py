@@ -1,0 +1,95 @@
+"""Arguments that the operators around the scan must refuse before anything reaches the GPU: lists
+of tensors that share memory (CPU; the addresses are fake and never dereferenced)."""
+import ctypes
+import random
+
+import pytest
+import torch
+
+from selective_state_space_26_amd import _lib
+
+OK, ALIAS = 0, 7
+BASE, WS, NORM = 1 << 40, 1 << 30, 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+def _entries(items):
+    e = (_lib.TensorEntry * len(items))()
+    for i, (data, n, dt) in enumerate(items):
+        e[i] = _lib.TensorEntry(data, n, dt, 0)
+    return e
+
+
+def _clip(lib, tensors, outs=None, call=False, norm=NORM, ws=WS):
+    """The status of clipping these (data, numel, dtype): the check, or the entry point itself
+    where there is no GPU that could be sent to the fake addresses."""
+    if call and torch.cuda.device_count() > 0:
+        pytest.skip("fake addresses, a GPU is present")
+    e = _entries(tensors)
+    a = _lib.GradArgs(1, len(e), e, e if outs is None else _entries(outs), 1.0, 1e-6, norm)
+    need = lib.msel_grad_workspace_bytes(ctypes.byref(a))
+    if call:
+        return lib.msel_grad_clip(ctypes.byref(a), ws, need, None)
+    return lib.msel_validate_grad_clip(ctypes.byref(a), ws, need)
+
+
+def _list(n, at=BASE, step=1 << 16, seed=None):
+    items = [(at + i * step, 1000 + i, i % 2) for i in range(n)]
+    if seed is not None:
+        random.Random(seed).shuffle(items)
+    return items
+
+
+@pytest.mark.parametrize("n", [3, 90, 511, 513, 5000])  # the host's stack and heap
+@pytest.mark.parametrize("seed", [None, 1])
+def test_lists_that_share_nothing(lib, n, seed):
+    t = _list(n, seed=seed)
+    assert _clip(lib, t) == OK
+    beside = [(p + (1 << 15), k, d) for p, k, d in t]
+    assert _clip(lib, t, beside) == OK
+    half = n // 2  # some in place, some beside
+    assert _clip(lib, t, t[:half] + beside[half:]) == OK
+    # an empty tensor has no memory, whatever its address says
+    assert _clip(lib, t + [(t[0][0], 0, 0)]) == OK
+
+
+@pytest.mark.parametrize("n", [3, 90, 513])
+@pytest.mark.parametrize("seed", [None, 1])
+def test_a_tensor_listed_twice(lib, n, seed):
+    t = [(p, 1000, 0) for p, _, _ in _list(n, seed=seed)]
+    other = [(p + (1 << 50), 1000, 0) for p, _, _ in t]
+    for i, j in ((0, n - 1), (n - 1, 0), (n // 2, n // 2 - 1)):
+        twice = list(t)
+        twice[i] = t[j]
+        assert _clip(lib, twice) == ALIAS
+        assert _clip(lib, twice, call=True) == ALIAS
+        # as a source alone it may be: both copies come out the same
+        assert _clip(lib, twice, other) == OK
+        # as a destination it may not
+        assert _clip(lib, other, twice) == ALIAS
+
+
+def test_lists_in_another_order(lib):
+    """A destination that is another entry's source."""
+    t = [(BASE + i * 65536, 1000, 0) for i in range(4)]
+    assert _clip(lib, t, [t[1], t[0], t[2], t[3]]) == ALIAS
+    assert _clip(lib, t, t[1:] + [(BASE << 1, 1000, 0)]) == ALIAS
+    assert _clip(lib, t, t[1:] + [(BASE << 1, 1000, 0)], call=True) == ALIAS
+
+
+@pytest.mark.parametrize("offset", [4, 3996, -3996])
+def test_ranges_that_overlap_in_part(lib, offset):
+    """The entry point compares whole ranges: views into one buffer that share elements."""
+    a, b, c = ((BASE + i * 65536, 1000, 0) for i in range(3))
+    near = (a[0] + offset, 1000, 0)
+    assert _clip(lib, [a, near], call=True) == ALIAS
+    assert _clip(lib, [a, b], [c, near], call=True) == ALIAS  # another entry's source
+    assert _clip(lib, [a], [near], call=True) == ALIAS        # its own, shifted
+    assert _clip(lib, [b, c], [a, near], call=True) == ALIAS  # another destination
+    assert _clip(lib, [a], call=True, norm=a[0] + 400) == ALIAS
+    assert _clip(lib, [b], [a], call=True, norm=a[0] + 400) == ALIAS
+    assert _clip(lib, [a], call=True, ws=a[0] + 256) == ALIAS
