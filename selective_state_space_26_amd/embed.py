@@ -14,8 +14,8 @@ import ctypes
 import torch
 
 from . import _lib
-from .norm import _at, _handle, _workspace
-from .scan import _dtype_code, _need
+from .norm import _at, _handle
+from .scan import _dtype_code, _need, _workspace
 
 
 def _embed_args(ids, vocab, dim, scale, padding_idx, code, wcode):

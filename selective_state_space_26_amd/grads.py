@@ -7,8 +7,8 @@ import ctypes
 import torch
 
 from . import _lib
-from .norm import _at, _handle, _workspace
-from .scan import _dtype_code
+from .norm import _at, _handle
+from .scan import _dtype_code, _workspace
 
 
 class GradList:

@@ -19,7 +19,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .scan import _dtype_code, _need, _stream
+from .scan import _dtype_code, _need, _stream, _workspace
 
 _LAYOUTS = {"bdl": 0, "bld": 1}
 
@@ -36,15 +36,6 @@ def _handle(dev):
 
 def _at(t):
     return None if t is None else t.data_ptr()
-
-
-def _workspace(workspace, need, dev):
-    """A workspace of at least `need` bytes: the given one if it is large enough."""
-    if need == 0:
-        return None, 0
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _rows(t, name):

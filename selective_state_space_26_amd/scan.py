@@ -51,6 +51,24 @@ def _need(t, name, shape, dtype, device):
     return t
 
 
+def _workspace(workspace, need, dev):
+    """(workspace, its size in bytes) of at least `need` bytes: the given one if it is large
+    enough, which then has to be contiguous memory of that GPU."""
+    if need == 0:
+        return None, 0
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch.Tensor")
+        size = workspace.numel() * workspace.element_size()
+        if size >= need:
+            if workspace.device != dev:
+                raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+            return workspace, size
+    return torch.empty(need, device=dev, dtype=torch.uint8), need
+
+
 def chunk_len() -> int:
     return int(_lib.load().msel_chunk_len())
 

@@ -56,3 +56,22 @@ def test_clip_neighbours_and_repeated_sources():
     n = msel.msel_grad_clip([t, t], 0.5, out=out)
     assert abs(float(n) - 2 ** 0.5 * float(msel.msel_grad_norm([t]))) <= 2.0 ** -22 * float(n)
     assert torch.equal(out[0], out[1]) and bool(out[0].any())
+
+
+@pytest.mark.parametrize("op", ["norm", "gated", "embed", "clip"])
+@pytest.mark.parametrize("kind", ["host", "expanded"])
+def test_refuses_a_workspace_of_another_kind(op, kind):
+    log(f"workspace {op} {kind}")
+    size = 1 << 22
+    ws = (torch.empty(size, dtype=torch.uint8, pin_memory=True) if kind == "host" else
+          torch.empty(1, device="cuda", dtype=torch.uint8).expand(size))
+    x, w = normal((6, 40, 90), "bf16", 1), normal((40,), "f32", 2)
+    call = {
+        "norm": lambda: msel.msel_norm_bwd(x, None, x, workspace=ws),
+        "gated": lambda: msel.msel_gated_norm_bwd(x, x, w, x, workspace=ws),
+        "embed": lambda: msel.msel_embed_bwd(torch.zeros(6, 40, device="cuda", dtype=torch.int64),
+                                             x, 5, workspace=ws),
+        "clip": lambda: msel.msel_grad_clip([x], 1.0, workspace=ws),
+    }[op]
+    with pytest.raises(ValueError):
+        call()

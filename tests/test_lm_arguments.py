@@ -1,6 +1,8 @@
 """Arguments that the operators around the scan must refuse before anything reaches the GPU: lists
-of tensors that share memory (CPU; the addresses are fake and never dereferenced)."""
+of tensors that share memory (the addresses are fake and never dereferenced), and workspaces that
+are no memory of the GPU.  All of it runs on the CPU."""
 import ctypes
+import importlib
 import random
 
 import pytest
@@ -93,3 +95,36 @@ def test_ranges_that_overlap_in_part(lib, offset):
     assert _clip(lib, [a], call=True, norm=a[0] + 400) == ALIAS
     assert _clip(lib, [b], [a], call=True, norm=a[0] + 400) == ALIAS
     assert _clip(lib, [a], call=True, ws=a[0] + 256) == ALIAS
+
+
+@pytest.mark.parametrize("module", ["norm", "embed", "grads"])
+@pytest.mark.parametrize("kind", ["host", "expanded", "strided", "none"])
+def test_workspace_of_another_kind(module, kind):
+    """A host tensor's address, or a view that has fewer bytes than elements, never gets to a
+    kernel."""
+    ask = importlib.import_module(f"selective_state_space_26_amd.{module}")._workspace
+    here, gpu = torch.device("cpu"), torch.device("cuda", 0)
+    if kind == "host":
+        with pytest.raises(ValueError):
+            ask(torch.empty(4096, dtype=torch.uint8), 1024, gpu)
+    elif kind == "expanded":
+        with pytest.raises(ValueError):
+            ask(torch.empty(1).expand(4096), 1024, here)
+    elif kind == "strided":
+        with pytest.raises(ValueError):
+            ask(torch.empty(64, 64).t(), 1024, here)
+    else:
+        with pytest.raises(TypeError):
+            ask(ctypes.create_string_buffer(4096), 1024, here)
+
+
+@pytest.mark.parametrize("module", ["norm", "embed", "grads"])
+def test_workspace_that_fits_or_does_not(module):
+    ask = importlib.import_module(f"selective_state_space_26_amd.{module}")._workspace
+    here = torch.device("cpu")
+    given = torch.empty(300)
+    assert ask(given, 1200, here) == (given, 1200)
+    assert ask(given, 0, here) == (None, 0)
+    got, size = ask(given, 1201, here)  # too small: replaced
+    assert got is not given and size == 1201 and got.numel() == 1201
+    assert ask(None, 77, here)[1] == 77
