@@ -330,12 +330,10 @@ def msel_scan_complex_bwd(u, delta, A, B, C, dout, chunk_states=None, D=None, z=
         setattr(g, k, _ptr(r[k]))
     lib = _lib.load()
     need = int(lib.msel_scan_bwd_workspace_bytes(ctypes.byref(a)))
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    workspace, ws_bytes = _workspace(workspace, need, dev)
     _lib.check("msel_scan_complex_bwd",
                lib.msel_scan_complex_bwd(ctypes.byref(a), ctypes.byref(g), _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(),
-                                         _stream(dev)))
+                                         ws_bytes, _stream(dev)))
     return r
 
 
@@ -380,10 +378,8 @@ def msel_scan_trap_bwd(u, delta, lam, A, B, C, dout, chunk_states=None, D=None, 
     tr.lambda_, tr.u_prev, tr.B_prev = _ptr(lam), _ptr(u_prev), _ptr(B_prev)
     lib = _lib.load()
     need = int(lib.msel_scan_bwd_workspace_bytes(ctypes.byref(a)))
-    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    ws_ptr = _ptr(workspace) if need > 0 else None
-    ws_bytes = workspace.numel() * workspace.element_size() if need > 0 else 0
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    ws_ptr = _ptr(workspace)
     _lib.check("msel_scan_trap_bwd",
                lib.msel_scan_trap_bwd(ctypes.byref(a), ctypes.byref(tr), ctypes.byref(g),
                                       ctypes.byref(tg), ws_ptr, ws_bytes, _stream(dev)))
@@ -421,10 +417,8 @@ def msel_scan_bwd(u, delta, A, B, C, dout, D=None, z=None, delta_bias=None,
         setattr(g, k, _ptr(r[k]))
     lib = _lib.load()
     need = int(lib.msel_scan_bwd_workspace_bytes(ctypes.byref(a)))
-    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    ws_ptr = _ptr(workspace) if need > 0 else None
-    ws_bytes = workspace.numel() * workspace.element_size() if need > 0 else 0
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    ws_ptr = _ptr(workspace)
     if main_events is None:
         _lib.check("msel_scan_bwd", lib.msel_scan_bwd(ctypes.byref(a), ctypes.byref(g), ws_ptr,
                                                       ws_bytes, _stream(dev)))
