@@ -15,7 +15,7 @@ import torch
 
 from . import _lib
 from .norm import _at, _handle
-from .scan import _dtype_code, _need, _workspace
+from .scan import _dtype_code, _int32, _need, _workspace
 
 
 def _embed_args(ids, vocab, dim, scale, padding_idx, code, wcode):
@@ -27,9 +27,11 @@ def _embed_args(ids, vocab, dim, scale, padding_idx, code, wcode):
     if dev.type != "cuda":
         raise ValueError("tensors must be on the GPU")
     _need(ids, "ids", ids.shape, ids.dtype, dev)
-    return _lib.EmbedArgs(_lib.ABI_VERSION, vocab, dim, 1 if ids.dtype == torch.int64 else 0,
-                          ids.numel(), -1 if padding_idx is None else padding_idx, code, wcode,
-                          scale, 0, ids.data_ptr(), None, None)
+    if padding_idx is None or not 0 <= padding_idx < vocab:
+        padding_idx = -1  # none: other ids give no gradient anyway
+    return _lib.EmbedArgs(_lib.ABI_VERSION, _int32(vocab, "vocab"), _int32(dim, "dim"),
+                          1 if ids.dtype == torch.int64 else 0, ids.numel(), padding_idx, code,
+                          wcode, scale, 0, ids.data_ptr(), None, None)
 
 
 def msel_embed_fwd(ids, weight, scale=1.0, dtype=None, out=None):

@@ -19,7 +19,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .scan import _dtype_code, _need, _stream, _workspace
+from .scan import _dtype_code, _int32, _need, _stream, _workspace
 
 _LAYOUTS = {"bdl": 0, "bld": 1}
 
@@ -43,7 +43,8 @@ def _rows(t, name):
         raise ValueError(f"{name} must be a non-empty [..., dim] tensor")
     if t.device.type != "cuda":
         raise ValueError("tensors must be on the GPU")
-    return t.shape, t.shape[-1], t.numel() // t.shape[-1]
+    dim = _int32(t.shape[-1], "dim")
+    return t.shape, dim, t.numel() // dim
 
 
 def msel_norm_fwd(x, weight=None, residual=None, scale=1.0, eps=1e-5, residual_dtype=None,
@@ -124,9 +125,10 @@ def _gated_args(x, z, weight, eps, groups, gate_first, layout, out_layout):
         raise TypeError("z must be a torch.Tensor")
     _need(z, "z", x.shape, dt, dev)
     _need(weight, "weight", (dim,), torch.float32, dev)
-    a = _lib.GatedNormArgs(_lib.ABI_VERSION, bsz, dim, L, groups, code, _LAYOUTS[layout],
-                           _LAYOUTS[out_layout], 1 if gate_first else 0, eps, x.data_ptr(),
-                           z.data_ptr(), _at(weight), None)
+    a = _lib.GatedNormArgs(_lib.ABI_VERSION, _int32(bsz, "batch"), _int32(dim, "dim"),
+                           _int32(L, "seqlen"), _int32(groups, "groups"), code,
+                           _LAYOUTS[layout], _LAYOUTS[out_layout], 1 if gate_first else 0, eps,
+                           x.data_ptr(), z.data_ptr(), _at(weight), None)
     return a, ((bsz, dim, L) if out_layout == "bdl" else (bsz, L, dim))
 
 

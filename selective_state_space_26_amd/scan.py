@@ -51,6 +51,13 @@ def _need(t, name, shape, dtype, device):
     return t
 
 
+def _int32(value, name):
+    """A size as the library takes it (ctypes would take it modulo 2^32)."""
+    if not -1 << 31 <= value < 1 << 31:
+        raise ValueError(f"{name} is {value}, beyond 32 bits")
+    return value
+
+
 def _workspace(workspace, need, dev):
     """(workspace, its size in bytes) of at least `need` bytes: the given one if it is large
     enough, which then has to be contiguous memory of that GPU."""

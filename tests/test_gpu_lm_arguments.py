@@ -75,3 +75,43 @@ def test_refuses_a_workspace_of_another_kind(op, kind):
     }[op]
     with pytest.raises(ValueError):
         call()
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """The library's sizes are 32-bit: a larger one is refused, not taken modulo 2^32."""
+    log("sizes beyond 32 bits")
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GiB of free GPU memory")
+    n = (1 << 32) + 8
+    x = torch.zeros(n, device="cuda", dtype=torch.bfloat16)
+    out = torch.empty_like(x)
+    ids, row = torch.zeros(3, device="cuda", dtype=torch.int64), normal((3, 1), "f32", 1)
+    small = normal((2, 6, 4), "f32", 2)
+    refused = (ValueError, _lib.MselError)
+    with pytest.raises(refused):
+        msel.msel_norm_fwd(x.view(1, n), out=out.view(1, n))
+    with pytest.raises(refused):
+        msel.msel_norm_bwd(x.view(1, n), None, x.view(1, n), want_dresidual=False,
+                           want_dweight=False)
+    for shape in ((1, n, 1), (1, 1, n), (n, 1, 1)):
+        with pytest.raises(refused):
+            msel.msel_gated_norm_fwd(x.view(shape), x.view(shape), out=out.view(shape))
+    for groups in ((1 << 32) + 2, 2 - (1 << 32)):
+        with pytest.raises(refused):
+            msel.msel_gated_norm_fwd(small, small, groups=groups)
+    with pytest.raises(refused):
+        msel.msel_embed_fwd(ids, x.view(n, 1))
+    with pytest.raises(refused):
+        msel.msel_embed_fwd(ids, x.view(1, n))
+    with pytest.raises(refused):
+        msel.msel_embed_bwd(ids, row, (1 << 32) + 5)
+    with pytest.raises(refused):
+        msel.msel_embed_bwd(ids, row, 5 - (1 << 32), dweight=row)
+
+
+def test_padding_idx_outside_the_table_is_none():
+    log("padding_idx outside")
+    ids, dout = torch.arange(6, device="cuda") % 3, normal((6, 8), "f32", 1)
+    ref = msel.msel_embed_bwd(ids, dout, 3)
+    for padding in (3, -1, 1 << 64, (1 << 64) + 1, -(1 << 64) + 1):
+        assert torch.equal(ref, msel.msel_embed_bwd(ids, dout, 3, padding_idx=padding)), padding
