@@ -16,7 +16,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .scan import _dtype_code, _need, _ptr, _stream
+from .scan import _dtype_code, _int32, _need, _ptr, _stream
 
 
 def _conv_args(x, weight, bias, state, activation):
@@ -35,7 +35,8 @@ def _conv_args(x, weight, bias, state, activation):
     _need(state, "state", (bsz, dim, W - 1), dt, dev)
     a = _lib.ConvArgs()
     a.abi_version = _lib.ABI_VERSION
-    a.batch, a.dim, a.seqlen, a.width = int(bsz), int(dim), int(L), int(W)
+    a.batch, a.dim = _int32(bsz, "batch"), _int32(dim, "dim")
+    a.seqlen, a.width = _int32(L, "seqlen"), _int32(W, "width")
     a.dtype = _dtype_code(dt)
     a.activation = 1 if activation else 0
     a.reserved = 0

@@ -81,7 +81,7 @@ def chunk_len() -> int:
 
 
 def num_chunks(seqlen: int) -> int:
-    return int(_lib.load().msel_num_chunks(int(seqlen)))
+    return int(_lib.load().msel_num_chunks(_int32(int(seqlen), "seqlen")))
 
 
 def _args(u, delta, A, B, C, D, z, delta_bias, h0, delta_softplus):
@@ -103,7 +103,8 @@ def _args(u, delta, A, B, C, D, z, delta_bias, h0, delta_softplus):
     _need(h0, "h0", (bsz, dim, N), torch.float32, dev)
     a = _lib.ScanArgs()
     a.abi_version = _lib.ABI_VERSION
-    a.batch, a.dim, a.dstate, a.seqlen = int(bsz), int(dim), int(N), int(L)
+    a.batch, a.dim = _int32(bsz, "batch"), _int32(dim, "dim")
+    a.dstate, a.seqlen = _int32(N, "dstate"), _int32(L, "seqlen")
     a.dtype = _dtype_code(dt)
     a.delta_softplus = 1 if delta_softplus else 0
     a.reserved = 0
@@ -279,7 +280,8 @@ def _shape_args(u, A, chunk_states_given):
     bsz, dim, L = u.shape
     a = _lib.ScanArgs()
     a.abi_version = _lib.ABI_VERSION
-    a.batch, a.dim, a.dstate, a.seqlen = int(bsz), int(dim), int(A.shape[1]), int(L)
+    a.batch, a.dim = _int32(bsz, "batch"), _int32(dim, "dim")
+    a.dstate, a.seqlen = _int32(A.shape[1], "dstate"), _int32(L, "seqlen")
     a.dtype = _dtype_code(u.dtype)
     a.delta_softplus, a.reserved = 1, 0
     # the answer depends only on the shapes; non-null placeholders satisfy the argument checks
