@@ -16,9 +16,10 @@
 //     chunk's rows in fp32.  An id's run inside a chunk is written to dw directly; a run that
 //     crosses chunks leaves one partial sum per chunk;
 //  3. the partial sums of each crossing run are added in chunk order.
-// No floating-point atomics, and a frequent id costs no more than a rare one.  (Counting a pass's
-// digits with global atomics in the pass before saved a launch and cost 22 us: the most frequent
-// ids' counters are one address each.)
+// No floating-point atomics.  The segment sums take the same time whatever the ids; a run is
+// joined by one block per slab of columns, so a batch of mostly one id takes longer (2^18 x 64 fp32
+// of 16 ids 32 us, of one id 80).  (Counting a pass's digits with global atomics in the pass before
+// saved a launch and cost 22 us: the most frequent ids' counters are one address each.)
 // Measured: lookup of 16384 x 768, fp32 to bf16, 10 us (44 MB); gradient of 16384 bf16 rows of 50257
 // ids 53 us: 8 + 10 + 8 + 10 for the sort's launches, which the fill of 154 MB bounds, 12 for the
 // segment sums, 8 for the join; of 262144 fp32 rows of 64 for 16 ids 3 + 7, 14 and 10.
@@ -47,6 +48,8 @@ constexpr int kOneBlock = 2048;  // tokens that one block sorts alone
 constexpr int kFillBlocks = 512;
 constexpr int kSegBatch = 8;     // rows of a chunk in flight at a time
 constexpr int kJoinThreads = 256;
+// Partial sums of a run in flight per lane: 2^18 x 768 fp32 of one id 530 us with 8, 440 with 16.
+constexpr int kJoinBatch = 16;
 constexpr int kJoinBlocks = 1024;  // blocks per slab of columns that look for runs to join
 
 struct EmbedPlan {
@@ -409,10 +412,12 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedParams p, EmbedPlan
 
 // The runs that cross chunks: for each of the block's `look` (up to 64 at a time) chunks that such
 // a run starts in, the block adds the run's partial sums, its row lanes every RL-th row each, then
-// the row lanes in order.
+// the row lanes in order.  A run of m tokens has m / seg partial sums, and a lane may add thousands
+// of them one after another: a batch in a tree in fp32, the batches in fp64 (with fp32 alone the
+// gradient of 2^18 equal rows of one id was off by 500 x 2^-24 of itself).
 __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedParams p, EmbedPlan pl,
                                                                   int S, int nvec, int look) {
-    __shared__ float red[kJoinThreads][4];
+    __shared__ double red[4][kJoinThreads];
     const uint32_t* key = part_of(p, pl.key[(pl.passes - 1) & 1]);
     const float* part = reinterpret_cast<const float*>(part_of(p, pl.partial));
     const int64_t seg = pl.seg;
@@ -448,28 +453,49 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedParams p,
                 stride /= 64;
             }
             const int64_t n = at + m - c;
-            float acc[4] = {};
-#pragma unroll 8
-            for (int64_t j = rl; j < n; j += RL) {
-                // row 0 is the run's part in its first chunk, the others the heads of the next ones
+            // row 0 is the run's part in its first chunk, the others the heads of the next ones
+            const auto part_row = [&](int64_t j) {
+                RawVec<float, 4> v;
+                v.w = 0;
                 const int64_t row = j == 0 ? c * 2 + 1 : (c + j) * 2;
-                float v[4];
-                to_f32<float, 4>(
-                    ld_part<float, 4>(
-                        part + MSEL_IDX(row, static_cast<int64_t>(pl.nseg) * 2) * p.dim + e0, left),
-                    v);
+                if (j < n)
+                    v = ld_part<float, 4>(
+                        part + MSEL_IDX(row, static_cast<int64_t>(pl.nseg) * 2) * p.dim + e0, left);
+                return v;
+            };
+            float s[kJoinBatch][4];
+            double acc[4] = {};
+            if (n <= RL) {  // block-uniform: most runs, one row per row lane
+                to_f32<float, 4>(part_row(rl), s[0]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) acc[q] += v[q];
+                for (int q = 0; q < 4; ++q) acc[q] = static_cast<double>(s[0][q]);
+            } else {
+                for (int64_t j0 = rl; j0 < n; j0 += kJoinBatch * RL) {
+#pragma unroll
+                    for (int i = 0; i < kJoinBatch; ++i)
+                        to_f32<float, 4>(part_row(j0 + i * RL), s[i]);
+#pragma unroll
+                    for (int h = kJoinBatch / 2; h > 0; h /= 2)
+#pragma unroll
+                        for (int i = 0; i < h; ++i)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) s[i][q] += s[i + h][q];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[q] += static_cast<double>(s[0][q]);
+                }
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) red[threadIdx.x][q] = acc[q];
+            for (int q = 0; q < 4; ++q) red[q][threadIdx.x] = acc[q];
             __syncthreads();
             if (rl == 0 && left > 0) {
                 const int rows = static_cast<int>(min(static_cast<int64_t>(RL), n));
                 for (int r = 1; r < rows; ++r)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[q] += red[r * S + lane][q];
-                write_row<4>(p, k, e0, left, acc);
+                    for (int q = 0; q < 4; ++q) acc[q] += red[q][r * S + lane];
+                float sum[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sum[q] = static_cast<float>(acc[q]);
+                write_row<4>(p, k, e0, left, sum);
             }
             __syncthreads();  // red is free again
         }
