@@ -2,17 +2,18 @@
 // than a 16-byte vector and for calls of a few tiles: forward and backward (the formulas stand in
 // tile_norm.hip and tile_norm_bwd.hip).
 //
-// A block takes `tg` tokens of one batch row and group, a thread one token and every C-th
+// A block takes `tg` tokens of one batch row and group, 1 to 7, a thread one token and every C-th
 // channel, C = kThreads / tg: neighbouring threads hold neighbouring tokens, so a step of the
-// block reads C runs of tg elements, and a short sequence is read whole.  Such calls are small:
-// what counts is the number of blocks and of loads in flight (U per tensor and thread), not the
-// width of a load.  Blocks that share cache lines run on one XCD.  Sums over channels: each
-// thread over its steps, then a tree over the C threads of a token in LDS.  Rows in
-// [batch, seqlen, dim] pass through LDS, U steps at a time.  Measured: 3 x 6016 x 4 bf16 forward
-// 11 us, backward 23; 1 x 8192 x 31 16 and 36, latency of a few blocks all of them.
+// block reads C runs of tg elements.  A short sequence is read whole where there are blocks enough;
+// otherwise tg is small, mostly 1: a thread reads single elements a row apart, and the blocks of
+// neighbouring tokens read the same lines, which their XCD's cache holds (xcd_order).  Such calls
+// are small: what counts is the number of blocks and of loads in flight (U per tensor and thread),
+// not the width of a load.  Sums over channels: each thread over its steps, then a tree over the C
+// threads of a token in LDS.  Rows in [batch, seqlen, dim] pass through LDS, U steps at a time.
+// Measured: 3 x 6016 x 4 bf16 forward 10 us, backward 22; 1 x 8192 x 31 14 and 34, latency of a few
+// blocks all of them.
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
 #include <type_traits>
 
 #include "lm_device.hpp"
@@ -228,12 +229,16 @@ __global__ __launch_bounds__(kThreads) void tile_short_bwd_kernel(TileNormParams
     }
 }
 
-// Tokens per block: up to 32, fewer until the launch has 160 blocks.  With fewer blocks CUs stand
-// idle (1 x 8192 x 31 bf16, backward: 59 us in 8 blocks of 4 tokens, 41 in 31 of one; 4 x 2048 x
-// 256: 35 us in 128 blocks, 28 in 256); with more, too many blocks read each line (1 x 3712 x 853:
-// 49 us in 214 blocks of 4 tokens, 77 in 427 of 2).
+// Tokens per block: all of a sequence below a vector (less than 8), fewer until the launch has 160
+// blocks.  With fewer blocks CUs stand idle (bf16, forward and backward: 20 x 8192 x 7 47 and 87 us
+// in 20 blocks of 7 tokens, 17 and 37 in 80 of 2, 12 and 28 in 140 of one; 64 x 2048 x 7 15 and 29
+// in 64 blocks, 9 and 18 in 256); with more, too many blocks read each line (512 x 2048 x 7 26 and
+// 68 us in 512 blocks of 7, 61 and 196 in 3584 of one).  Longer sequences come here in so few tiles
+// that even blocks of one token are 160 at most (1 x 8192 x 31: 188 and 442 us in one block, 14 and
+// 34 in 31).
+constexpr int kShort = 8;
 int short_tokens(int B, int groups, int L) {
-    int tg = std::min(L, 32);
+    int tg = L < kShort ? L : 1;
     while (tg > 1 && static_cast<int64_t>(B) * groups * ((L + tg - 1) / tg) < 160) tg = (tg + 1) / 2;
     return tg;
 }
