@@ -13,9 +13,14 @@ from .scan import _dtype_code, _workspace
 
 class GradList:
     """The tensors of one model, checked once and kept as the library's list of them (with
-    references to the tensors and their storages, so that the listed memory stays theirs).  A
-    program whose gradients are the same tensors at every step builds it once; one that replaces
-    a tensor or its storage builds a new list."""
+    references to the tensors and their storages, so that the listed memory stays theirs).
+
+    A program whose gradients are the same tensors at every step builds it once.  PyTorch's
+    zero_grad() drops the gradients and the next backward makes new ones: the list then still
+    names the old ones, and clipping it leaves the new ones as they are.  Such a program calls
+    zero_grad(set_to_none=False), which keeps them, or passes the gradients themselves to every
+    call (a list of 266 tensors takes 0.3 ms of the host to build).  One that replaces or resizes
+    a listed tensor's storage builds a new list; check() finds the tensors it did that to."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
@@ -43,6 +48,14 @@ class GradList:
 
     def __len__(self):
         return len(self.tensors)
+
+    def check(self):
+        """Raises if a listed tensor's memory, size or dtype is no longer what the list has."""
+        for i, (t, e) in enumerate(zip(self.tensors, self.entries)):
+            if (t.data_ptr() != (e.data or 0) or t.numel() != e.numel or not t.is_contiguous()
+                    or _dtype_code(t.dtype) != e.dtype
+                    or t.untyped_storage().nbytes() < t.numel() * t.element_size()):
+                raise ValueError(f"tensor {i} has changed since the list was built")
 
 
 def _as_list(grads):

@@ -115,3 +115,40 @@ def test_padding_idx_outside_the_table_is_none():
     ref = msel.msel_embed_bwd(ids, dout, 3)
     for padding in (3, -1, 1 << 64, (1 << 64) + 1, -(1 << 64) + 1):
         assert torch.equal(ref, msel.msel_embed_bwd(ids, dout, 3, padding_idx=padding)), padding
+
+
+def test_gradient_list_finds_changed_tensors():
+    log("gradient list, changed tensors")
+    t = [normal((40, 3), "f32", 1), normal((9,), "bf16", 2), torch.empty(0, device="cuda")]
+    grads = msel.GradList(t)
+    grads.check()
+    msel.msel_grad_clip(grads, 0.5)
+    grads.check()
+    t[1].data = normal((9,), "bf16", 3)
+    with pytest.raises(ValueError, match="tensor 1"):
+        grads.check()
+    for change in (lambda x: x.resize_(50, 3), lambda x: x.t_(),
+                   lambda x: x.untyped_storage().resize_(0)):
+        x = normal((40, 3), "f32", 1)
+        grads = msel.GradList([x])
+        change(x)
+        with pytest.raises(ValueError, match="tensor 0"):
+            grads.check()
+
+
+def test_gradient_list_kept_over_zero_grad():
+    """With set_to_none=False a list built once clips the gradients of every step; with the default
+    its tensors are the first step's."""
+    log("gradient list over steps")
+    w = torch.nn.Parameter(normal((60, 50), "f32", 1))
+    opt = torch.optim.SGD([w], lr=0.0)
+    for keep in (True, False):
+        opt.zero_grad()
+        grads = None
+        for step in range(3):
+            w.square().sum().backward()
+            grads = grads or msel.GradList([w.grad])
+            msel.msel_grad_clip(grads, 0.25)
+            clipped = abs(float(w.grad.norm()) - 0.25) < 1e-5
+            assert clipped == (keep or step == 0)
+            opt.zero_grad(set_to_none=not keep)
