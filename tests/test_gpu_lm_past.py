@@ -16,96 +16,8 @@ if not torch.cuda.is_available():  # pragma: no cover
 import selective_state_space_26_amd as msel  # noqa: E402
 from selective_state_space_26_amd import _lib  # noqa: E402
 
-from lm_helpers import DTYPES, U32, U_OUT  # noqa: E402
-
-EPS = 1e-5
-SLICE = 512
-
-
-def _uniform(shape, dtype, seed, lo=-1.0, hi=1.0):
-    g = torch.Generator(device="cuda").manual_seed(seed)
-    return torch.empty(shape, device="cuda", dtype=DTYPES[dtype]).uniform_(lo, hi, generator=g)
-
-
-def _bound(got, ref, size, what):
-    """Element by element, as lm_helpers.assert_elementwise."""
-    room = U_OUT[got.dtype] * 1.001 * ref.abs() + 128.0 * U32 * size + 1e-37
-    off = (got.double() - ref).abs() / room
-    worst = float(off.max())
-    assert worst <= 1.0, f"{what}: {worst:.2f} of the bound"  # also false for NaN
-
-
-def _groups(t, groups, bld):
-    """A slice of tokens as [batch, groups, n, tokens] in fp64."""
-    t = t.transpose(1, 2) if bld else t
-    return t.double().reshape(t.shape[0], groups, -1, t.shape[2])
-
-
-def _cut(t, bld, a, b):
-    return t[:, a:b] if bld else t[:, :, a:b]
-
-
-def _inputs(bsz, groups, n, L, dtype):
-    shape = (bsz, groups * n, L)
-    return (_uniform(shape, dtype, 1), _uniform(shape, dtype, 2, -4.0, 4.0),
-            _uniform((groups * n,), "f32", 3, 0.5, 1.5))
-
-
-def _gate(z):
-    s = torch.sigmoid(z)
-    return z * s, s * (1.0 + z * (1.0 - s)), s * (1.0 + z.abs() * (1.0 - s))
-
-
-def _check_forward(case, first, out_bld):
-    bsz, groups, n, L, dtype = case
-    x, z, w = _inputs(*case)
-    out = msel.msel_gated_norm_fwd(x, z, w, EPS, groups, first, "bdl", "bld" if out_bld else "bdl")
-    assert out.numel() * out.element_size() > 128 << 20
-    ww = w.double().reshape(1, groups, n, 1)
-    for a in range(0, L, SLICE):
-        b = min(L, a + SLICE)
-        xs, (gate, _, _) = _groups(x[:, :, a:b], groups, False), _gate(z[:, :, a:b].double())
-        gate = gate.reshape(xs.shape)
-        v = xs * gate if first else xs
-        ref = v * (v.square().mean(2, keepdim=True) + EPS) ** -0.5 * ww
-        if not first:
-            ref = ref * gate
-        got = _cut(out, out_bld, a, b)
-        _bound((got.transpose(1, 2) if out_bld else got).reshape(ref.shape), ref, ref.abs(),
-               f"out {a}")
-
-
-def _check_backward(case, first, bld):
-    bsz, groups, n, L, dtype = case
-    x, z, w = _inputs(*case)
-    dout = _uniform((bsz, L, groups * n) if bld else (bsz, groups * n, L), dtype, 4)
-    g = msel.msel_gated_norm_bwd(x, z, w, dout, EPS, groups, first, "bdl", "bld" if bld else "bdl")
-    assert 2 * x.numel() * x.element_size() > 128 << 20
-    ww = w.double().reshape(1, groups, n, 1)
-    dw, dw_terms = 0.0, 0.0
-    for a in range(0, L, SLICE):
-        b = min(L, a + SLICE)
-        xs = _groups(x[:, :, a:b], groups, False)
-        gate, slope, slope_terms = (t.reshape(xs.shape) for t in _gate(z[:, :, a:b].double()))
-        dy = _groups(_cut(dout, bld, a, b), groups, bld)
-        v = xs * gate if first else xs
-        r = (v.square().mean(2, keepdim=True) + EPS) ** -0.5
-        p = dy * ww if first else dy * ww * gate
-        dv = r * (p - v * r * r * (p * v).mean(2, keepdim=True))
-        dvt = r * (p.abs() + v.abs() * r * r * (p * v).abs().mean(2, keepdim=True))
-        if first:
-            dx, dz, t = dv * gate, dv * xs * slope, dy * v * r
-            dxt, dzt = dvt * gate.abs(), dvt * xs.abs() * slope_terms
-        else:
-            dx, dz, t = dv, dy * ww * v * r * slope, dy * gate * v * r
-            dxt, dzt = dvt, (dy * ww * v * r).abs() * slope_terms
-        _bound(g["dx"][:, :, a:b].reshape(dx.shape), dx, dxt, f"dx {a}")
-        _bound(g["dz"][:, :, a:b].reshape(dz.shape), dz, dzt, f"dz {a}")
-        dw = dw + t.sum((0, 3)).reshape(-1)
-        dw_terms = dw_terms + t.abs().sum((0, 3)).reshape(-1)
-    off = float(((g["dweight"].double() - dw).abs() / (128.0 * U32 * dw_terms)).max())
-    assert off <= 1.0, f"dweight: {off:.2f} of the bound"
-
+from lm_gpu_ref import EPS, check_backward, check_forward, inputs, uniform  # noqa: E402
+from lm_helpers import U32, U_OUT  # noqa: E402
 
 # batch, groups, channels of a group, length: tiles of 128 bytes whose group fits a CU; of 64 bytes,
 # with passes that are read twice; of 32 bytes (few tiles of the widest groups)
@@ -127,7 +39,7 @@ def _name(v):
 @pytest.mark.parametrize("first", [True, False])
 def test_forward(case, layout, first):
     log(f"past the caches, forward {case} {layout} {first}")
-    _check_forward(case, first, layout == "bld")
+    assert check_forward(case, first, layout == "bld") > 128 << 20
 
 
 @pytest.mark.parametrize("case", BACK, ids=_name)
@@ -135,14 +47,14 @@ def test_forward(case, layout, first):
 @pytest.mark.parametrize("first", [True, False])
 def test_backward(case, layout, first):
     log(f"past the caches, backward {case} {layout} {first}")
-    _check_backward(case, first, layout == "bld")
+    assert check_backward(case, first, layout == "bld") > 128 << 20
 
 
 @pytest.mark.parametrize("dtype,n", [("f32", (40 << 20) + 3), ("bf16", (80 << 20) + 5)])
 def test_clip(dtype, n):
     """One tensor of more than 128 MiB between small ones, beside its input and in place."""
     log(f"past the caches, clip {dtype}")
-    t = [_uniform((7, 11), dtype, 1), _uniform((n,), dtype, 2), _uniform((13,), dtype, 3)]
+    t = [uniform((7, 11), dtype, 1), uniform((n,), dtype, 2), uniform((13,), dtype, 3)]
     out = [torch.full_like(x, 7.0) for x in t]
     norm = msel.msel_grad_clip(t, 0.5, out=out)
     want = sum(float(x.double().square().sum()) for x in t) ** 0.5
@@ -165,7 +77,7 @@ CHECKED = [("fwd", WIDE[0], "bdl", True), ("fwd", WIDE[1], "bld", False),
 def test_in_the_checked_build(what):
     log(f"past the caches, checked build {what}")
     if what[0] == "clip":
-        t = [_uniform(((40 << 20) + 3,), "f32", 1)]
+        t = [uniform(((40 << 20) + 3,), "f32", 1)]
 
         def run():
             out = [torch.empty_like(x) for x in t]
@@ -173,9 +85,9 @@ def test_in_the_checked_build(what):
     else:
         kind, case, layout, first = what
         bsz, groups, n, L, dtype = case
-        x, z, w = _inputs(*case)
+        x, z, w = inputs(*case)
         a = (EPS, groups, first, "bdl", layout)
-        dout = _uniform((bsz, L, groups * n) if layout == "bld" else x.shape, dtype, 4)
+        dout = uniform((bsz, L, groups * n) if layout == "bld" else x.shape, dtype, 4)
 
         def run():
             return ([msel.msel_gated_norm_fwd(x, z, w, *a)] if kind == "fwd" else
