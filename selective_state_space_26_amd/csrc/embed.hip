@@ -21,8 +21,8 @@
 // of 16 ids 32 us, of one id 80).  (Counting a pass's digits with global atomics in the pass before
 // saved a launch and cost 22 us: the most frequent ids' counters are one address each.)
 // Measured: lookup of 16384 x 768, fp32 to bf16, 10 us (44 MB); gradient of 16384 bf16 rows of 50257
-// ids 53 us: 8 + 10 + 8 + 10 for the sort's launches, which the fill of 154 MB bounds, 12 for the
-// segment sums, 8 for the join; of 262144 fp32 rows of 64 for 16 ids 3 + 7, 14 and 10.
+// ids 53 to 60 us: 8 + 10 + 8 + 10 for the sort's launches, which the fill of 154 MB bounds, 12 for
+// the segment sums, 7 for the join; of 262144 fp32 rows of 64 for 16 ids 3 + 7, 14 and 9.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

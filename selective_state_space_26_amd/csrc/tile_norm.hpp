@@ -16,9 +16,9 @@
 // The launchers choose by n.
 // Measured and not kept: blocks that walk tiles and load a pass of the next tile as they write
 // one of the current (neighbouring tiles then run apart and no longer share cache lines: 790 us
-// against 650 for the forward of 5120 x 65536 at SB = 32), and two kernels, sums and then outputs
-// with all inputs read twice at SB = 256 (663 against 621 us there; 52 against 43 for
-// 8 x 1536 x 2048).
+// against 650 for the forward of 5120 x 65536 at SB = 32), and, for the forward, two kernels, sums
+// and then outputs with all inputs read twice at SB = 256 (663 against 621 us there; 52 against 43
+// for 8 x 1536 x 2048; with outputs through the caches).
 //
 // A last tile that is not full starts early, at seqlen - TT, and does the tokens it shares with
 // the tile before it again (the same values in the same order, so the same bits; the backward
@@ -45,8 +45,13 @@ struct TileShape {
     static_assert(64 % VL == 0, "whole vectors of tokens");
 };
 
-// Blocks of a launch in tiles of SB bytes, and how many make wide tiles worth it: 2048 x 2047
-// x 4 bf16 forward, 128 blocks, took 34 us wide and 22 narrow.
+// Blocks of a launch in tiles of SB bytes, and how many wide ones (SB = 128) make them worth it.
+// us in wide tiles against the narrower ones, bf16 to and from rows:
+//   128 blocks: 700 channels forward 14 and 11, backward 26 and 21; 5120 backward 185 and 167
+//   192 blocks: 700 forward 16 and 17, backward 30 and 34; 5120 backward 229 and 250
+//   256 blocks: 700 forward 17 and 19, backward 33 and 39; 5120 backward 265 and 291
+//   800 blocks: 700 forward 58 and 62, backward 113 and 138; 5120 backward 889 and 860
+// (with 256 channels and fewer the two differ by 10% at most at any of these).
 template <typename T, int SB>
 inline int64_t tile_blocks(const TileNormParams& p) {
     constexpr int TT = SB / static_cast<int>(sizeof(T));
