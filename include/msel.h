@@ -69,7 +69,8 @@ typedef enum {
     MSEL_ERR_ALIGN = 4,       /* an activation pointer is not 16-byte aligned              */
     MSEL_ERR_UNSUPPORTED = 5, /* dstate outside 1..MSEL_MAX_DSTATE, a convolution width     */
                               /* outside 1..MSEL_MAX_CONV_WIDTH, a normed or embedded width */
-                              /* above MSEL_MAX_NORM_DIM, or an unsupported layout pair     */
+                              /* above MSEL_MAX_NORM_DIM, an unsupported layout pair, or    */
+                              /* more than MSEL_MAX_TOP likeliest tokens                    */
     MSEL_ERR_WORKSPACE = 6,   /* workspace NULL or smaller than msel_scan_bwd_workspace_bytes */
     MSEL_ERR_ALIAS = 7,       /* an output pointer equals an input pointer                 */
     MSEL_ERR_HIP = 8,         /* the HIP runtime reported an error at launch               */
@@ -665,6 +666,135 @@ msel_status msel_grad_norm(const msel_grad_args *args, void *workspace, size_t w
                            hipStream_t stream);
 msel_status msel_grad_clip(const msel_grad_args *args, void *workspace, size_t workspace_bytes,
                            hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * A gated linear recurrence, one state per channel: a mixer beside the selective scan, for blocks
+ * whose gates alone are functions of the input (page 1, the selection mechanism; page 3, the
+ * recurrent mode).  Per batch row b, channel d and step t:
+ *
+ *   r = sigmoid(gate_a_t),  i = sigmoid(gate_x_t)
+ *   a = exp(lam[d] * r),    m = sqrt(1 - a^2)
+ *   h_t = a * h_{t-1} + m * i * x_t            (h_{-1} = h0 or 0)
+ *   out_t = h_t
+ *
+ * lam is at most 0 (a positive one gives NaN).  Layouts as for the scan: x, gate_a, gate_x, out
+ * and their gradients [batch, dim, seqlen] in the activation dtype (16-byte aligned); lam, dlam
+ * [dim] fp32; h0, final_state, dfinal_state, dh0 [batch, dim] fp32; chunk_states [batch, dim,
+ * msel_num_chunks(seqlen)] fp32, entry c the state before step c * msel_chunk_len().  States and
+ * sums are fp32.
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+    int32_t abi_version;    /* must be MSEL_ABI_VERSION                                    */
+    int32_t batch;          /* >= 1                                                        */
+    int32_t dim;            /* channels, >= 1; batch * dim up to 2^30                       */
+    int32_t seqlen;         /* 1..MSEL_MAX_SEQLEN                                          */
+    int32_t dtype;          /* msel_dtype of x, gate_a, gate_x, out and of their gradients  */
+    int32_t reserved;       /* must be 0                                                   */
+    const void *x;          /* required                                                    */
+    const void *gate_a;     /* required                                                    */
+    const void *gate_x;     /* required                                                    */
+    const float *lam;       /* required                                                    */
+    const float *h0;        /* optional; NULL means 0                                      */
+    void *out;              /* fwd: required output; ignored by the backward               */
+    float *final_state;     /* fwd: optional output; may equal h0 (updated in place); ignored by
+                               the backward                                                */
+    float *chunk_states;    /* fwd: optional output; bwd: optional input (rebuilt into the
+                               workspace if NULL)                                          */
+} msel_lru_args;
+
+/* Gradients of a scalar loss given dL/dout and dL/dfinal_state.  With q_t the gradient of
+ * log a_t, the slope of m taken as 0 where m = 0.  Every output is overwritten. */
+typedef struct {
+    const void *dout;          /* required                                                 */
+    const float *dfinal_state; /* optional; NULL means 0                                   */
+    void *dx;                  /* required output                                          */
+    void *dgate_a;             /* required output                                          */
+    void *dgate_x;             /* required output                                          */
+    float *dlam;               /* optional output                                          */
+    float *dh0;                /* optional output (computed even when args->h0 is NULL)      */
+} msel_lru_grads;
+
+/* Host-only argument checks of the entry points below (no HIP call, no device access). */
+msel_status msel_validate_lru_fwd(const msel_lru_args *args, const void *workspace,
+                                  size_t workspace_bytes);
+msel_status msel_validate_lru_bwd(const msel_lru_args *args, const msel_lru_grads *grads,
+                                  const void *workspace, size_t workspace_bytes);
+
+/* Bytes of workspace msel_lru_fwd needs: 0 unless long rows are few, whose segments are then
+ * composed first (also 0 for invalid sizes). */
+size_t msel_lru_fwd_workspace_bytes(const msel_lru_args *args);
+
+/* Deterministic.  seqlen == 1 is the decode step.  The workspace is 256-byte aligned. */
+msel_status msel_lru_fwd(const msel_lru_args *args, void *workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/* Bytes of workspace msel_lru_bwd needs (0 for invalid sizes): dlam's parts, segments, and the
+ * chunk states when args->chunk_states is NULL. */
+size_t msel_lru_bwd_workspace_bytes(const msel_lru_args *args);
+
+/* Its backward, recomputing the states from the chunk states.  Deterministic. */
+msel_status msel_lru_bwd(const msel_lru_args *args, const msel_lru_grads *grads, void *workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Log probabilities of tokens under a model's logits: the loss of its training and the scores of
+ * its answers, at the other end of the model from the embedding.  Per row x of `vocab` logits:
+ *
+ *   lse = log sum_j exp(scale * x_j),  p_j = exp(scale * x_j - lse)
+ *   logprob = scale * x[id] - lse                 for the token id asked for
+ *   entropy = - sum_j p_j log p_j
+ *   top_ids, top_logprobs: the `top` likeliest tokens, by logit and, where equal, by the lowest id
+ *
+ * An id outside [0, vocab) asks for nothing: its logprob is 0 and gives no gradient.  A logit of
+ * -inf is masked: p = 0.  A row without any other has lse and logprob -inf, entropy 0 and no
+ * gradient.  A logit that is NaN or +inf makes the row's values NaN (a NaN counts as the largest
+ * for top_ids).  Rows may be strided (logits of a padded vocabulary).  Layouts: logits
+ * [rows, vocab], `stride` elements from row to row; ids [rows]; logprob, lse, entropy [rows] fp32;
+ * top_ids [rows, top] int64; top_logprobs [rows, top] fp32.  Pointers are aligned to their element.
+ * ---------------------------------------------------------------------------------------- */
+#define MSEL_MAX_TOP 64
+
+typedef struct {
+    int32_t abi_version;    /* must be MSEL_ABI_VERSION                                    */
+    int32_t vocab;          /* 1..2^30                                                     */
+    int64_t rows;           /* >= 1, up to 2^30                                            */
+    int64_t stride;         /* >= vocab, rows * stride up to 2^40                          */
+    int32_t dtype;          /* msel_dtype of logits, dlogits                               */
+    int32_t ids_64bit;      /* 1: ids are int64; 0: int32                                   */
+    int32_t top;            /* fwd: 0..min(MSEL_MAX_TOP, vocab); ignored by the backward    */
+    float scale;            /* > 0 and finite                                              */
+    const void *logits;     /* required                                                    */
+    const void *ids;        /* optional (fwd: required with logprob; bwd: with dlogprob)    */
+    float *logprob;         /* fwd: optional output; ignored by the backward               */
+    float *lse;             /* fwd: optional output; bwd: required input, the forward's     */
+    float *entropy;         /* fwd: optional output; bwd: input, required with dentropy     */
+    int64_t *top_ids;       /* fwd: required output if top > 0                              */
+    float *top_logprobs;    /* fwd: required output if top > 0                              */
+} msel_logprob_args;
+
+/* dlogits_j = scale * (dlogprob * (1[j = id] - p_j) + dlse * p_j - dentropy * p_j (log p_j +
+ * entropy)).  Where |lse| >= 1024 the row's sum is formed again, since an fp32 lse has too few
+ * digits there. */
+typedef struct {
+    const float *dlogprob;  /* [rows], optional; NULL means 0                              */
+    const float *dlse;      /* [rows], optional; NULL means 0                              */
+    const float *dentropy;  /* [rows], optional; NULL means 0                              */
+    void *dlogits;          /* required output [rows, vocab]; may equal args->logits (in place,
+                               dstride == stride then), and shares no memory with it else  */
+    int64_t dstride;        /* >= vocab, rows * dstride up to 2^40                         */
+} msel_logprob_grads;
+
+msel_status msel_validate_logprob_fwd(const msel_logprob_args *args, const void *workspace,
+                                      size_t workspace_bytes);
+msel_status msel_validate_logprob_bwd(const msel_logprob_args *args,
+                                      const msel_logprob_grads *grads);
+/* Bytes of workspace msel_logprob_fwd needs: 0 unless few rows are shared by several blocks. */
+size_t msel_logprob_fwd_workspace_bytes(const msel_logprob_args *args);
+/* Both deterministic; the workspace is 256-byte aligned. */
+msel_status msel_logprob_fwd(const msel_logprob_args *args, void *workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+msel_status msel_logprob_bwd(const msel_logprob_args *args, const msel_logprob_grads *grads,
+                             hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -107,6 +107,31 @@ class GradArgs(ctypes.Structure):
                 ("max_norm", ctypes.c_float), ("eps", ctypes.c_float), ("norm", _P)]
 
 
+class LruArgs(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x", _P), ("gate_a", _P), ("gate_x", _P),
+                ("lam", _P), ("h0", _P), ("out", _P), ("final_state", _P), ("chunk_states", _P)]
+
+
+class LruGrads(ctypes.Structure):
+    _fields_ = [("dout", _P), ("dfinal_state", _P), ("dx", _P), ("dgate_a", _P),
+                ("dgate_x", _P), ("dlam", _P), ("dh0", _P)]
+
+
+class LogprobArgs(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("ids_64bit", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("logits", _P), ("ids", _P), ("logprob", _P),
+                ("lse", _P), ("entropy", _P), ("top_ids", _P), ("top_logprobs", _P)]
+
+
+class LogprobGrads(ctypes.Structure):
+    _fields_ = [("dlogprob", _P), ("dlse", _P), ("dentropy", _P), ("dlogits", _P),
+                ("dstride", ctypes.c_int64)]
+
+
 class MselError(RuntimeError):
     def __init__(self, fn: str, code: int, text: str):
         super().__init__(f"{fn} returned {STATUS.get(code, code)}: {text}")
@@ -134,7 +159,10 @@ EXPORTS = ["msel_abi_version", "msel_chunk_len", "msel_num_chunks", "msel_status
            "msel_validate_embed_fwd", "msel_validate_embed_bwd", "msel_embed_fwd",
            "msel_embed_bwd_workspace_bytes", "msel_embed_bwd", "msel_validate_grad_norm",
            "msel_validate_grad_clip", "msel_grad_workspace_bytes", "msel_grad_norm",
-           "msel_grad_clip"]
+           "msel_grad_clip", "msel_validate_lru_fwd", "msel_validate_lru_bwd",
+           "msel_lru_fwd_workspace_bytes", "msel_lru_fwd", "msel_lru_bwd_workspace_bytes",
+           "msel_lru_bwd", "msel_validate_logprob_fwd", "msel_validate_logprob_bwd",
+           "msel_logprob_fwd_workspace_bytes", "msel_logprob_fwd", "msel_logprob_bwd"]
 
 
 def default_path() -> str:
@@ -255,6 +283,26 @@ def load(path: str | None = None) -> ctypes.CDLL:
     for fn in ("msel_grad_norm", "msel_grad_clip"):
         getattr(lib, fn).restype = ctypes.c_int
         getattr(lib, fn).argtypes = [pn, _P, ctypes.c_size_t, _P]
+    for op, args, grads in (("lru", LruArgs, LruGrads),):
+        pa, pg = ctypes.POINTER(args), ctypes.POINTER(grads)
+        for fn, res, argtypes in (
+                (f"msel_validate_{op}_fwd", ctypes.c_int, [pa, _P, ctypes.c_size_t]),
+                (f"msel_validate_{op}_bwd", ctypes.c_int, [pa, pg, _P, ctypes.c_size_t]),
+                (f"msel_{op}_fwd_workspace_bytes", ctypes.c_size_t, [pa]),
+                (f"msel_{op}_fwd", ctypes.c_int, [pa, _P, ctypes.c_size_t, _P]),
+                (f"msel_{op}_bwd_workspace_bytes", ctypes.c_size_t, [pa]),
+                (f"msel_{op}_bwd", ctypes.c_int, [pa, pg, _P, ctypes.c_size_t, _P])):
+            getattr(lib, fn).restype = res
+            getattr(lib, fn).argtypes = argtypes
+    pa, pg = ctypes.POINTER(LogprobArgs), ctypes.POINTER(LogprobGrads)
+    for fn, res, argtypes in (
+            ("msel_validate_logprob_fwd", ctypes.c_int, [pa, _P, ctypes.c_size_t]),
+            ("msel_validate_logprob_bwd", ctypes.c_int, [pa, pg]),
+            ("msel_logprob_fwd_workspace_bytes", ctypes.c_size_t, [pa]),
+            ("msel_logprob_fwd", ctypes.c_int, [pa, _P, ctypes.c_size_t, _P]),
+            ("msel_logprob_bwd", ctypes.c_int, [pa, pg, _P])):
+        getattr(lib, fn).restype = res
+        getattr(lib, fn).argtypes = argtypes
     if lib.msel_abi_version() != ABI_VERSION:
         raise RuntimeError("libmsel.so ABI version mismatch")
     if path is None:
