@@ -69,8 +69,9 @@ typedef enum {
     MSEL_ERR_ALIGN = 4,       /* an activation pointer is not 16-byte aligned              */
     MSEL_ERR_UNSUPPORTED = 5, /* dstate outside 1..MSEL_MAX_DSTATE, a convolution width     */
                               /* outside 1..MSEL_MAX_CONV_WIDTH, a normed or embedded width */
-                              /* above MSEL_MAX_NORM_DIM, an unsupported layout pair, or    */
-                              /* more than MSEL_MAX_TOP likeliest tokens                    */
+                              /* above MSEL_MAX_NORM_DIM, an unsupported layout pair, more */
+                              /* than MSEL_MAX_TOP likeliest tokens, or a feed-forward width */
+                              /* above MSEL_MAX_MLP_WIDTH                                   */
     MSEL_ERR_WORKSPACE = 6,   /* workspace NULL or smaller than msel_scan_bwd_workspace_bytes */
     MSEL_ERR_ALIAS = 7,       /* an output pointer equals an input pointer                 */
     MSEL_ERR_HIP = 8,         /* the HIP runtime reported an error at launch               */
@@ -795,6 +796,57 @@ msel_status msel_logprob_fwd(const msel_logprob_args *args, void *workspace,
                              size_t workspace_bytes, hipStream_t stream);
 msel_status msel_logprob_bwd(const msel_logprob_args *args, const msel_logprob_grads *grads,
                              hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The gated feed-forward block that alternates with the mixers (page 5, the Mamba-3 posts: "the
+ * SSM and MLP layers alternate"): both projections, the activation and the product in one kernel.
+ *
+ *   out = act(x Wg^T) * (x Wu^T)          act: silu, or gelu in its tanh form
+ *
+ * Layouts: x, dx [tokens, dim], w_gate, w_up and their gradients [hidden, dim], out, dout
+ * [tokens, hidden], all in `dtype` (16-byte aligned).  The products are MFMA products of `dtype`
+ * with fp32 sums; the activation and the product are fp32.
+ * ---------------------------------------------------------------------------------------- */
+#define MSEL_MAX_MLP_WIDTH (1 << 17)
+
+typedef struct {
+    int32_t abi_version;    /* must be MSEL_ABI_VERSION                                    */
+    int32_t dim;            /* 1..MSEL_MAX_MLP_WIDTH                                       */
+    int32_t hidden;         /* 1..MSEL_MAX_MLP_WIDTH                                       */
+    int32_t dtype;          /* msel_dtype of every tensor                                  */
+    int64_t tokens;         /* 1..2^24, times the larger width up to 2^40                  */
+    int32_t activation;     /* 0: silu; 1: gelu (tanh form)                                */
+    int32_t reserved;       /* must be 0                                                   */
+    const void *x;          /* required                                                    */
+    const void *w_gate;     /* required                                                    */
+    const void *w_up;       /* required                                                    */
+    void *out;              /* fwd: required output; ignored by the backward               */
+} msel_gated_mlp_args;
+
+/* With G = x Wg^T and U = x Wu^T formed again: dG = dout * U * act'(G), dU = dout * act(G), both
+ * rounded to `dtype` (they are operands of products), and
+ *   dx = dG Wg + dU Wu,  dw_gate = dG^T x,  dw_up = dU^T x. */
+typedef struct {
+    const void *dout;       /* required                                                    */
+    void *dx;               /* optional output                                             */
+    void *dw_gate;          /* optional output, with dw_up                                 */
+    void *dw_up;            /* optional output, with dw_gate                               */
+} msel_gated_mlp_grads;
+
+msel_status msel_validate_gated_mlp_fwd(const msel_gated_mlp_args *args, const void *workspace,
+                                        size_t workspace_bytes);
+msel_status msel_validate_gated_mlp_bwd(const msel_gated_mlp_args *args,
+                                        const msel_gated_mlp_grads *grads, const void *workspace,
+                                        size_t workspace_bytes);
+/* Bytes of workspace the two entry points need (0 for invalid sizes): copies of operands whose
+ * rows are no multiple of a tile's, and in the backward of transposed ones and of dG and dU. */
+size_t msel_gated_mlp_fwd_workspace_bytes(const msel_gated_mlp_args *args);
+size_t msel_gated_mlp_bwd_workspace_bytes(const msel_gated_mlp_args *args);
+/* Both deterministic; the workspace is 256-byte aligned. */
+msel_status msel_gated_mlp_fwd(const msel_gated_mlp_args *args, void *workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+msel_status msel_gated_mlp_bwd(const msel_gated_mlp_args *args, const msel_gated_mlp_grads *grads,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -4,7 +4,7 @@
     from selective_state_space_26_amd import msel_conv1d_fwd, msel_conv1d_bwd
     from selective_state_space_26_amd import msel_norm_fwd, msel_gated_norm_fwd, msel_embed_fwd
     from selective_state_space_26_amd import GradList, msel_grad_clip
-    from selective_state_space_26_amd import msel_lru_fwd, msel_logprob_fwd
+    from selective_state_space_26_amd import msel_lru_fwd, msel_logprob_fwd, msel_gated_mlp_fwd
 
 The kernels live in ``csrc/``; ``build.py`` compiles them in-tree.  Importing this package does
 not load the library; the first call does, and raises if it is not built.
@@ -12,6 +12,7 @@ not load the library; the first call does, and raises if it is not built.
 from .conv import msel_conv1d_bwd, msel_conv1d_fwd  # noqa: F401
 from .embed import msel_embed_bwd, msel_embed_fwd  # noqa: F401
 from .grads import GradList, msel_grad_clip, msel_grad_norm  # noqa: F401
+from .gated_mlp import msel_gated_mlp_bwd, msel_gated_mlp_fwd  # noqa: F401
 from .logprob import msel_logprob_bwd, msel_logprob_fwd  # noqa: F401
 from .lru import msel_lru_bwd, msel_lru_fwd  # noqa: F401
 from .norm import (msel_gated_norm_bwd, msel_gated_norm_fwd, msel_norm_bwd,  # noqa: F401
@@ -31,4 +32,5 @@ __all__ = ["msel_scan_fwd", "msel_scan_bwd", "msel_scan_chunk_carry", "chunk_len
            "bound_violations", "bounds_selftest", "bwd_fused", "set_bwd_fused", "msel_norm_fwd",
            "msel_norm_bwd", "msel_gated_norm_fwd", "msel_gated_norm_bwd", "msel_embed_fwd",
            "msel_embed_bwd", "GradList", "msel_grad_norm", "msel_grad_clip",
-           "msel_lru_fwd", "msel_lru_bwd", "msel_logprob_fwd", "msel_logprob_bwd"]
+           "msel_lru_fwd", "msel_lru_bwd", "msel_logprob_fwd", "msel_logprob_bwd",
+           "msel_gated_mlp_fwd", "msel_gated_mlp_bwd"]

@@ -132,6 +132,18 @@ class LogprobGrads(ctypes.Structure):
                 ("dstride", ctypes.c_int64)]
 
 
+class GatedMlpArgs(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("tokens", ctypes.c_int64), ("activation", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x", _P), ("w_gate", _P), ("w_up", _P),
+                ("out", _P)]
+
+
+class GatedMlpGrads(ctypes.Structure):
+    _fields_ = [("dout", _P), ("dx", _P), ("dw_gate", _P), ("dw_up", _P)]
+
+
 class MselError(RuntimeError):
     def __init__(self, fn: str, code: int, text: str):
         super().__init__(f"{fn} returned {STATUS.get(code, code)}: {text}")
@@ -162,7 +174,10 @@ EXPORTS = ["msel_abi_version", "msel_chunk_len", "msel_num_chunks", "msel_status
            "msel_grad_clip", "msel_validate_lru_fwd", "msel_validate_lru_bwd",
            "msel_lru_fwd_workspace_bytes", "msel_lru_fwd", "msel_lru_bwd_workspace_bytes",
            "msel_lru_bwd", "msel_validate_logprob_fwd", "msel_validate_logprob_bwd",
-           "msel_logprob_fwd_workspace_bytes", "msel_logprob_fwd", "msel_logprob_bwd"]
+           "msel_logprob_fwd_workspace_bytes", "msel_logprob_fwd", "msel_logprob_bwd",
+           "msel_validate_gated_mlp_fwd", "msel_validate_gated_mlp_bwd",
+           "msel_gated_mlp_fwd_workspace_bytes", "msel_gated_mlp_fwd",
+           "msel_gated_mlp_bwd_workspace_bytes", "msel_gated_mlp_bwd"]
 
 
 def default_path() -> str:
@@ -283,7 +298,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     for fn in ("msel_grad_norm", "msel_grad_clip"):
         getattr(lib, fn).restype = ctypes.c_int
         getattr(lib, fn).argtypes = [pn, _P, ctypes.c_size_t, _P]
-    for op, args, grads in (("lru", LruArgs, LruGrads),):
+    for op, args, grads in (("lru", LruArgs, LruGrads),
+                            ("gated_mlp", GatedMlpArgs, GatedMlpGrads)):
         pa, pg = ctypes.POINTER(args), ctypes.POINTER(grads)
         for fn, res, argtypes in (
                 (f"msel_validate_{op}_fwd", ctypes.c_int, [pa, _P, ctypes.c_size_t]),

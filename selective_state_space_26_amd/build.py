@@ -25,7 +25,7 @@ ARCH = "gfx950"
 SOURCES = ["msel_api.cpp", "scan_fwd.hip", "chunk_carry.hip", "scan_bwd.hip", "conv1d.hip",
            "scan_cplx.hip", "scan_cplx_bwd.hip", "lm_api.cpp", "row_norm.hip", "tile_norm.hip",
            "tile_norm_bwd.hip", "tile_short.hip", "embed.hip", "grads.hip",
-           "block_api.cpp", "lru.hip", "logprob.hip"]
+           "block_api.cpp", "lru.hip", "logprob.hip", "gated_mlp.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -1,5 +1,5 @@
-// block_api.cpp -- the extern "C" entry points of the gated linear recurrence and of the log
-// probabilities of tokens, declared in include/msel.h.
+// block_api.cpp -- the extern "C" entry points of the gated linear recurrence, the log
+// probabilities of tokens and the gated feed-forward block, declared in include/msel.h.
 //
 // As in msel_api.cpp, every entry point validates its arguments on the host (no HIP call, no
 // device memory touched) and only then enqueues kernels on the caller's stream; no device memory
@@ -156,6 +156,38 @@ msel::LogprobParams logprob_params(const msel_logprob_args* a) {
     p.scale = a->scale;
     p.logits = a->logits;
     p.ids = a->ids;
+    return p;
+}
+
+// ---- the gated feed-forward block ----------------------------------------------------------
+
+msel_status check_mlp_sizes(const msel_gated_mlp_args* a) {
+    if (a == nullptr) return MSEL_ERR_NULL;
+    if (a->abi_version != MSEL_ABI_VERSION || a->reserved != 0) return MSEL_ERR_VERSION;
+    if (a->dim < 1 || a->hidden < 1 || a->tokens < 1 || a->tokens > (int64_t(1) << 24))
+        return MSEL_ERR_SHAPE;
+    if (a->dim > MSEL_MAX_MLP_WIDTH || a->hidden > MSEL_MAX_MLP_WIDTH) return MSEL_ERR_UNSUPPORTED;
+    if (a->tokens > kMaxElems / std::max(a->dim, a->hidden)) return MSEL_ERR_SHAPE;
+    return is_dtype(a->dtype) && is_flag(a->activation) ? MSEL_OK : MSEL_ERR_DTYPE;
+}
+
+msel_status check_mlp(const msel_gated_mlp_args* a) {
+    const msel_status s = check_mlp_sizes(a);
+    if (s != MSEL_OK) return s;
+    if (any_null({a->x, a->w_gate, a->w_up})) return MSEL_ERR_NULL;
+    return all_aligned({a->x, a->w_gate, a->w_up}, 16) ? MSEL_OK : MSEL_ERR_ALIGN;
+}
+
+msel::MlpParams mlp_params(const msel_gated_mlp_args* a, void* ws) {
+    msel::MlpParams p{};
+    p.M = a->tokens;
+    p.D = a->dim;
+    p.F = a->hidden;
+    p.gelu = a->activation;
+    p.x = a->x;
+    p.wg = a->w_gate;
+    p.wu = a->w_up;
+    p.ws = ws;
     return p;
 }
 
@@ -318,6 +350,64 @@ msel_status msel_logprob_bwd(const msel_logprob_args* a, const msel_logprob_grad
     p.dlogits = g->dlogits;
     p.dstride = g->dstride;
     return hip_status(msel::launch_logprob_bwd(p, a->dtype == MSEL_BF16, stream));
+}
+
+msel_status msel_validate_gated_mlp_fwd(const msel_gated_mlp_args* a, const void* workspace,
+                                        size_t workspace_bytes) {
+    const msel_status s = check_mlp(a);
+    if (s != MSEL_OK) return s;
+    if (a->out == nullptr) return MSEL_ERR_NULL;
+    if (!aligned(a->out, 16)) return MSEL_ERR_ALIGN;
+    if (aliased({a->out}, {a->x, a->w_gate, a->w_up})) return MSEL_ERR_ALIAS;
+    return check_workspace(workspace, workspace_bytes, msel_gated_mlp_fwd_workspace_bytes(a),
+                           {a->x, a->w_gate, a->w_up, a->out});
+}
+
+size_t msel_gated_mlp_fwd_workspace_bytes(const msel_gated_mlp_args* a) {
+    if (check_mlp_sizes(a) != MSEL_OK) return 0;
+    return msel::mlp_fwd_workspace_bytes(mlp_params(a, nullptr), a->dtype == MSEL_BF16);
+}
+
+msel_status msel_gated_mlp_fwd(const msel_gated_mlp_args* a, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
+    const msel_status s = msel_validate_gated_mlp_fwd(a, workspace, workspace_bytes);
+    if (s != MSEL_OK) return s;
+    msel::MlpParams p = mlp_params(a, workspace);
+    p.out = a->out;
+    return hip_status(msel::launch_mlp_fwd(p, a->dtype == MSEL_BF16, stream));
+}
+
+size_t msel_gated_mlp_bwd_workspace_bytes(const msel_gated_mlp_args* a) {
+    if (check_mlp_sizes(a) != MSEL_OK) return 0;
+    return msel::mlp_bwd_workspace_bytes(mlp_params(a, nullptr), a->dtype == MSEL_BF16);
+}
+
+msel_status msel_validate_gated_mlp_bwd(const msel_gated_mlp_args* a,
+                                        const msel_gated_mlp_grads* g, const void* workspace,
+                                        size_t workspace_bytes) {
+    const msel_status s = check_mlp(a);
+    if (s != MSEL_OK) return s;
+    if (g == nullptr || g->dout == nullptr) return MSEL_ERR_NULL;
+    if ((g->dw_gate == nullptr) != (g->dw_up == nullptr) ||
+        (g->dx == nullptr && g->dw_gate == nullptr))
+        return MSEL_ERR_NULL;
+    if (!all_aligned({g->dout, g->dx, g->dw_gate, g->dw_up}, 16)) return MSEL_ERR_ALIGN;
+    if (aliased({g->dx, g->dw_gate, g->dw_up}, {a->x, a->w_gate, a->w_up, g->dout}))
+        return MSEL_ERR_ALIAS;
+    return check_workspace(workspace, workspace_bytes, msel_gated_mlp_bwd_workspace_bytes(a),
+                           {a->x, a->w_gate, a->w_up, g->dout, g->dx, g->dw_gate, g->dw_up});
+}
+
+msel_status msel_gated_mlp_bwd(const msel_gated_mlp_args* a, const msel_gated_mlp_grads* g,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const msel_status s = msel_validate_gated_mlp_bwd(a, g, workspace, workspace_bytes);
+    if (s != MSEL_OK) return s;
+    msel::MlpParams p = mlp_params(a, workspace);
+    p.dout = g->dout;
+    p.dx = g->dx;
+    p.dwg = g->dw_gate;
+    p.dwu = g->dw_up;
+    return hip_status(msel::launch_mlp_bwd(p, a->dtype == MSEL_BF16, stream));
 }
 
 }  // extern "C"

@@ -25,6 +25,7 @@ __attribute__((weak)) hipError_t take_bounds_embed(BoundsRecord* r);
 __attribute__((weak)) hipError_t take_bounds_grads(BoundsRecord* r);
 __attribute__((weak)) hipError_t take_bounds_lru(BoundsRecord* r);
 __attribute__((weak)) hipError_t take_bounds_logprob(BoundsRecord* r);
+__attribute__((weak)) hipError_t take_bounds_mlp(BoundsRecord* r);
 }  // namespace msel
 
 static_assert(MSEL_MAX_DSTATE == msel::kMaxN, "the kernels' state limit is the boundary's");
@@ -631,7 +632,7 @@ msel_status msel_bound_violations(unsigned long long* count, uint32_t* file, uin
                             msel::take_bounds_tile_norm_bwd, msel::take_bounds_tile_short,
                             msel::take_bounds_embed,
                             msel::take_bounds_grads,     msel::take_bounds_lru,
-                            msel::take_bounds_logprob};
+                            msel::take_bounds_logprob,   msel::take_bounds_mlp};
     msel_status s = MSEL_OK;
     for (uint32_t i = 0; i < sizeof(takers) / sizeof(takers[0]); ++i) {
         msel::BoundsRecord r{};
