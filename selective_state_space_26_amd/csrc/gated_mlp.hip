@@ -8,10 +8,11 @@
 // together read one chunk of 8 rows, which then lie in 8 different places.  In the fused product the
 // B rows of a wavefront are 32 rows of Wg and the same 32 of Wu, so that a lane holds G and U of the
 // same elements and the activation and the product need no exchange.
-// The MFMA's rows are C's columns: a lane then holds 4 consecutive columns of a row of C.
+// The MFMA's rows are C's columns, so that a lane holds consecutive columns of a row of C.  The
+// backward's products over the hidden width and over the tokens read their operands by rows of k, as
+// they lie in memory; LDS turns them (the transposing reads of gfx950).
 //
-// Operands whose rows are no multiple of a stage are copied into padded rows first; the backward's
-// products over the hidden width and over the tokens read transposed copies.
+// Operands whose rows are no multiple of a stage are copied into padded rows first.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -49,37 +50,43 @@ __device__ __forceinline__ void mfma_step(const float*, const u32x4& a, const u3
 
 // act(z) and its derivative.  gelu in its tanh form is z s, s = sigmoid(2 c (z + 0.044715 z^3)).
 constexpr float kTwoC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-template <bool GELU>
-__device__ __forceinline__ float act_of(float z) {
-    if constexpr (!GELU) return silu_f(z);
-    return z * sigmoid_f(kTwoC * z * fmaf(0.044715f * z, z, 1.0f));
+__device__ __forceinline__ float act_of(float z, int gelu) {
+    return z * sigmoid_f(gelu ? kTwoC * z * fmaf(0.044715f * z, z, 1.0f) : z);
 }
-template <bool GELU>
-__device__ __forceinline__ void act_grad(float z, float& v, float& slope) {
-    if constexpr (!GELU) {
-        silu_grad_f(z, v, slope);
-    } else {
-        const float s = sigmoid_f(kTwoC * z * fmaf(0.044715f * z, z, 1.0f));
-        v = z * s;
-        slope = fmaf(v * (1.0f - s), kTwoC * fmaf(0.134145f * z, z, 1.0f), s);
-    }
+__device__ __forceinline__ void act_grad(float z, int gelu, float& v, float& slope) {
+    const float s = sigmoid_f(gelu ? kTwoC * z * fmaf(0.044715f * z, z, 1.0f) : z);
+    v = z * s;
+    slope = fmaf(v * (1.0f - s), gelu ? kTwoC * fmaf(0.134145f * z, z, 1.0f) : 1.0f, s);
 }
 
-enum class Epi { kPlain, kGate, kGateGrad };
+// What a product is, which also says how its operands lie: with consecutive k (rows of A and B), or
+// by rows of k (columns of A and B are consecutive).
+enum class Kind {
+    kGate,      // out = act(G) * U: A = x, B = Wg and Wu, all with consecutive k
+    kGateGrad,  // dG and dU from G, U and dout: the same
+    kInput,     // dx = dG Wg + dU Wu: A = (dG, dU) with consecutive k, B = Wg, then Wu by rows of k
+    kWeights,   // dW = (dG, dU)^T x: both by rows of k, the tokens
+};
+constexpr bool dual(Kind k) { return k == Kind::kGate || k == Kind::kGateGrad; }
 
 struct ProductParams {
-    int64_t M;       // rows of A and C
-    int N;           // kPlain: rows of B; else the hidden width (rows of each weight)
-    int64_t K;       // a multiple of a stage
-    const void* a;   // [M, lda]
-    const void* b0;  // [N, ldb]
+    int64_t M;       // rows of C
+    int N;           // columns of C; in the fused products the hidden width
+    int64_t K;       // along k: elements of a row, or rows (of each part of B)
+    const void* a;
+    const void* b0;
     const void* b1;  // the other weight
     int64_t lda, ldb;
-    void* c0;        // rows below `split`
-    void* c1;        // rows from `split` on (kPlain)
-    int64_t split, ldc;
+    int64_t wa, wb;  // elements of a row of A and B that may be read, where they lie by rows of k
+    int stages, half;  // stages in all, and of one part of B
+    int per_split;     // stages of a block
+    void* c0;        // rows [0, rows0) of C
+    void* c1;        // rows from `split` on; those between go nowhere
+    int64_t rows0, split, ldc;
+    float* part;       // not null: C goes there, [splits][M][N]
     const void* dout;  // kGateGrad: [M, N]
     int hp;            // kGateGrad: dG in columns [0, hp) of C, dU in [hp, 2 hp)
+    int gelu;
     int tm, tn;        // tiles
 };
 
@@ -100,57 +107,101 @@ __device__ __forceinline__ bool tile_at(const ProductParams& p, int& m, int& n) 
     return true;
 }
 
-// 4 values into columns [col, col + 4) of a row of n columns.
+// 8 values into columns [col, col + 8) of a row of n columns.
 template <typename T>
-__device__ __forceinline__ void store4(T* row, int col, int n, const float (&v)[4]) {
-    if (col + 4 <= n) {
-        if constexpr (sizeof(T) == 4) {
-            st_vec<float, 4>(row + MSEL_SPAN(col, 4, n), v);
-        } else {
-            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-            const u32x2 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-            __builtin_memcpy(row + MSEL_SPAN(col, 4, n), &w, 8);
-        }
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (col + k < n) Elem<T>::store1(row + col + k, v[k]);
-}
-
-template <typename T>
-__device__ __forceinline__ void load4(const T* row, int col, int n, float (&v)[4]) {
-    if (col + 4 <= n) {
-        if constexpr (sizeof(T) == 4) {
-            to_f32<float, 4>(ld_raw<float, 4>(row + MSEL_SPAN(col, 4, n)), v);
-        } else {
-            uint32_t w[2];
-            __builtin_memcpy(w, row + MSEL_SPAN(col, 4, n), 8);
-            v[0] = bf16lo(w[0]);
-            v[1] = bf16hi(w[0]);
-            v[2] = bf16lo(w[1]);
-            v[3] = bf16hi(w[1]);
-        }
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = col + k < n ? Elem<T>::load1(row + col + k) : 0.0f;
+__device__ __forceinline__ void store8(T* row, int col, int n, const float (&v)[8]) {
+    const RawVec<T, 8> r = from_f32<T, 8>(v);
+    if (col + 8 <= n)
+        st_raw<T, 8>(row + MSEL_SPAN(col, 8, n), r);
+    else if (col < n)
+        st_part<T, 8>(row + col, r, n - col);
 }
 
 typedef __attribute__((address_space(1))) const void GlobalVoid;
 typedef __attribute__((address_space(3))) void LdsVoid;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 LdsS16x4;
+
+// MFMA row i of a fragment of B is column order32(i) of its 32 columns of C: the result's rows
+// 8 g + 4 h + e, which a lane of half h holds in order of g and e, are then 16 consecutive columns.
+__device__ __forceinline__ int order32(int i) {
+    return ((i >> 2) & 1) * 16 + (i >> 3) * 4 + (i & 3);
+}
+
+// An operand of W rows (or columns of C's side) per stage in LDS, by chunks of 16 bytes.
+//
+// Consecutive k: [W][8 chunks], chunk c of row r at place c ^ (r & 7): the 8 lanes that LDS serves
+// together read one chunk of 8 rows, in 8 different places.  ORDER: rows in the order order32.
+//
+// By rows of k: [rows of k][W columns].  bf16 fragments are read with the transposing read, which
+// gives each lane of 16 the 4 values of its column from 4 rows of 16 columns; two such groups read
+// 64 bytes of 4 rows, which the swizzle puts in different quarters of the banks.  fp32 fragments
+// are single values: 32 columns of rows k and k + 4, in different halves of the banks.
+template <typename T, int W, bool BY_ROWS, bool ORDER>
+struct Operand {
+    static constexpr int kBytes = W * kStageBytes;
+    static constexpr int kPerChunk = 16 / static_cast<int>(sizeof(T));
+    static constexpr int kChunks = BY_ROWS ? W / kPerChunk : 8;  // of a row in LDS
+
+    __device__ __forceinline__ static int swizzle(int r) {
+        if constexpr (!BY_ROWS) return r & 7;
+        if constexpr (sizeof(T) == 4) return ((r >> 2) & 1) << 3;
+        return kChunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
+    }
+    // fragment f (32 rows) of step s: 16 bytes per lane
+    __device__ __forceinline__ static u32x4 read(const char* at, int f, int s, int lane) {
+        const int h = lane >> 5;
+        if constexpr (!BY_ROWS) {
+            const int r = f * 32 + (lane & 31);
+            return *reinterpret_cast<const u32x4*>(at + r * kStageBytes +
+                                                   (((2 * s + h) ^ (lane & 7)) * 16));
+        } else if constexpr (sizeof(T) == 4) {
+            const int c = f * 32 + (ORDER ? order32(lane & 31) : lane & 31);
+            u32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int k = 8 * s + 4 * h + e;
+                const int chunk = (c >> 2) ^ swizzle(k);
+                v[e] = *reinterpret_cast<const uint32_t*>(at + k * (W * 4) + chunk * 16 +
+                                                          (c & 3) * 4);
+            }
+            return v;
+        } else {
+            const int q = (lane >> 4) & 1, t = lane & 15, seg = t & 3;
+            // where the 4 columns lie that this lane's address stands for
+            const int c = f * 32 + (ORDER ? 16 * (seg & 1) + 4 * (2 * q + (seg >> 1))
+                                          : 16 * q + 4 * seg);
+            u32x4 v;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int k = 16 * s + 8 * h + 4 * e + (t >> 2);
+                const int chunk = (c >> 3) ^ swizzle(k);
+                const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (LdsS16x4*)(at + k * (W * 2) + chunk * 16 + (c & 4) * 2));
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                const u32x2 u = __builtin_bit_cast(u32x2, w);
+                v[2 * e] = u[0];
+                v[2 * e + 1] = u[1];
+            }
+            return v;
+        }
+    }
+};
 
 // WM x WN wavefronts, each MI x 2 MFMA tiles of 32 x 32: a block computes WM MI 32 rows by
-// WN 64 rows of B (in the fused products WN 32 columns of both weights).
-template <typename T, int WM, int WN, int MI, Epi EPI, bool GELU>
+// WN 64 columns (in the fused products WN 32 columns of both weights).
+template <typename T, int WM, int WN, int MI, Kind KIND>
 __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p) {
     constexpr int kThreads = WM * WN * 64;
     constexpr int BM = WM * MI * 32, BN = WN * 64;
-    constexpr int kRound = kThreads / 8;  // rows that the block loads at once
-    constexpr int LA = BM / kRound, LB = BN / kRound;
-    constexpr bool kDual = EPI != Epi::kPlain;
-    constexpr int kStage = (BM + BN) * kStageBytes;
-    static_assert(BM % kRound == 0 && BN % kRound == 0, "whole rounds");
+    constexpr bool kDual = dual(KIND);
+    constexpr bool kRowsA = KIND == Kind::kWeights, kRowsB = !kDual;
+    using OpA = Operand<T, BM, kRowsA, false>;
+    using OpB = Operand<T, BN, kRowsB, true>;
+    constexpr int LA = OpA::kBytes / 16 / kThreads, LB = OpB::kBytes / 16 / kThreads;
+    constexpr int kStage = OpA::kBytes + OpB::kBytes;
+    static_assert(LA * kThreads * 16 == OpA::kBytes && LB * kThreads * 16 == OpB::kBytes,
+                  "whole rounds");
     extern __shared__ __align__(16) char lds[];
 
     int tile_m, tile_n;
@@ -160,33 +211,61 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     const int64_t m0 = static_cast<int64_t>(tile_m) * BM;
     const int n0 = tile_n * (kDual ? BN / 2 : BN);
 
-    // this thread's chunks of a stage: row r of a round, place tid % 8; rows past the end repeat
-    // the last one (their results are not stored)
+    // this thread's chunks of the first stage.  Rows and columns past the end repeat the last ones
+    // (their results are not stored); rows of k past the end are zeroed in LDS.
     const char* src[LA + LB];
 #pragma unroll
-    for (int i = 0; i < LA + LB; ++i) {
-        const int r = (i < LA ? i : i - LA) * kRound + (tid >> 3);
-        const int chunk = (tid & 7) ^ (r & 7);
-        const T* row;
-        if (i < LA) {
-            const int64_t m = min(m0 + r, p.M - 1);
-            row = static_cast<const T*>(p.a) + MSEL_IDX(m, p.M) * p.lda;
-        } else if (kDual) {
-            const int n = min(n0 + (r >> 6) * 32 + (r & 31), p.N - 1);
-            row = static_cast<const T*>((r & 32) ? p.b1 : p.b0) +
-                  static_cast<int64_t>(MSEL_IDX(n, p.N)) * p.ldb;
+    for (int i = 0; i < LA; ++i) {
+        const int at = i * kThreads + tid, r = at / OpA::kChunks;
+        const int chunk = (at % OpA::kChunks) ^ OpA::swizzle(r);
+        const T* a = static_cast<const T*>(p.a);
+        if constexpr (kRowsA) {
+            const int64_t c = min(m0 + chunk * OpA::kPerChunk, p.wa - OpA::kPerChunk);
+            src[i] = reinterpret_cast<const char*>(a + r * p.lda + MSEL_SPAN(c, OpA::kPerChunk, p.wa));
         } else {
-            const int n = min(n0 + r, p.N - 1);
-            row = static_cast<const T*>(p.b0) + static_cast<int64_t>(MSEL_IDX(n, p.N)) * p.ldb;
+            const int64_t m = min(m0 + r, p.M - 1);
+            src[i] = reinterpret_cast<const char*>(a + MSEL_IDX(m, p.M) * p.lda) + chunk * 16;
         }
-        src[i] = reinterpret_cast<const char*>(row) + chunk * 16;
     }
-    const auto load_stage = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+        const int at = i * kThreads + tid, r = at / OpB::kChunks;
+        const int chunk = (at % OpB::kChunks) ^ OpB::swizzle(r);
+        const T* b = static_cast<const T*>(p.b0);
+        if constexpr (kRowsB) {
+            const int64_t c = min<int64_t>(n0 + chunk * OpB::kPerChunk, p.wb - OpB::kPerChunk);
+            src[LA + i] =
+                reinterpret_cast<const char*>(b + r * p.ldb + MSEL_SPAN(c, OpB::kPerChunk, p.wb));
+        } else {
+            if (r & 32) b = static_cast<const T*>(p.b1);
+            const int64_t n = min(n0 + (r >> 6) * 32 + order32(r & 31), p.N - 1);
+            src[LA + i] = reinterpret_cast<const char*>(b + MSEL_IDX(n, p.N) * p.ldb) + chunk * 16;
+        }
+    }
+    const int64_t step_a = kRowsA ? kStageK<T> * p.lda * static_cast<int64_t>(sizeof(T)) : kStageBytes;
+    const int64_t step_b = kRowsB ? kStageK<T> * p.ldb * static_cast<int64_t>(sizeof(T)) : kStageBytes;
+    // rows of k that stage k has, where it has not all
+    const auto rows_of = [&](int k) -> int {
+        const int64_t left = p.K - static_cast<int64_t>(k < p.half ? k : k - p.half) * kStageK<T>;
+        return left < kStageK<T> ? static_cast<int>(left) : kStageK<T>;
+    };
+    const auto load_stage = [&](int k, int buf) {
+        const int kb = k < p.half ? k : k - p.half;
+        const int64_t other = k < p.half ? 0
+                                         : static_cast<const char*>(p.b1) -
+                                               static_cast<const char*>(p.b0);
+        const int rows = rows_of(k);
 #pragma unroll
         for (int i = 0; i < LA + LB; ++i) {
+            const bool a = i < LA;
+            const char* g = src[i] + (a ? k * step_a : kb * step_b + (kDual ? 0 : other));
+            if ((a ? kRowsA : kRowsB) && rows < kStageK<T>) {  // uniform
+                const int r = a ? (i * kThreads + tid) / OpA::kChunks
+                                : ((i - LA) * kThreads + tid) / OpB::kChunks;
+                if (r >= rows) g -= (r - rows + 1) * (a ? p.lda : p.ldb) * static_cast<int64_t>(sizeof(T));
+            }
             const int at = buf * kStage + (i * kThreads + wave * 64) * 16;
-            __builtin_amdgcn_global_load_lds((GlobalVoid*)src[i], (LdsVoid*)(lds + at), 16, 0, 0);
-            src[i] += kStageBytes;
+            __builtin_amdgcn_global_load_lds((GlobalVoid*)g, (LdsVoid*)(lds + at), 16, 0, 0);
         }
     };
 
@@ -198,26 +277,34 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-    const int row_a = wm * MI * 32 + (lane & 31), row_b = wn * 64 + (lane & 31);
-    const int stages = static_cast<int>(p.K / kStageK<T>);
-    load_stage(0);
-    for (int k = 0; k < stages; ++k) {
+    const int first = blockIdx.z * p.per_split, last = min(p.stages, first + p.per_split);
+    load_stage(first, 0);
+    for (int k = first; k < last; ++k) {
+        const int buf = (k - first) & 1;
         __syncthreads();  // the stage has landed, and the other buffer has been read
-        if (k + 1 < stages) load_stage((k + 1) & 1);
-        const char* sa = lds + (k & 1) * kStage;
-        const char* sb = sa + BM * kStageBytes;
+        if (kRowsB) {
+            const int rows = rows_of(k);
+            if (rows < kStageK<T>) {  // uniform
+                const u32x4 zero = {0, 0, 0, 0};
+                char* at = lds + buf * kStage;
+                if (kRowsA)
+                    for (int i = rows * OpA::kChunks + tid; i < OpA::kBytes / 16; i += kThreads)
+                        *reinterpret_cast<u32x4*>(at + i * 16) = zero;
+                for (int i = rows * OpB::kChunks + tid; i < OpB::kBytes / 16; i += kThreads)
+                    *reinterpret_cast<u32x4*>(at + OpA::kBytes + i * 16) = zero;
+                __syncthreads();
+            }
+        }
+        if (k + 1 < last) load_stage(k + 1, buf ^ 1);
+        const char* sa = lds + buf * kStage;
+        const char* sb = sa + OpA::kBytes;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int c = 2 * s + (lane >> 5);
             u32x4 fa[MI], fb[2];
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
-                fa[i] = *reinterpret_cast<const u32x4*>(sa + (row_a + i * 32) * kStageBytes +
-                                                        ((c ^ (lane & 7)) * 16));
+            for (int i = 0; i < MI; ++i) fa[i] = OpA::read(sa, wm * MI + i, s, lane);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                fb[j] = *reinterpret_cast<const u32x4*>(sb + (row_b + j * 32) * kStageBytes +
-                                                        ((c ^ (lane & 7)) * 16));
+            for (int j = 0; j < 2; ++j) fb[j] = OpB::read(sb, wn * 2 + j, s, lane);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -226,46 +313,99 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
         }
     }
 
-    // D: lane l holds column l % 32 (a row of C) and rows 8 g + 4 (l / 32) + 0..3 (columns of C)
+    // lane l holds 16 columns from 16 (l / 32) on of row l % 32
+    const int h = lane >> 5;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const int64_t m = m0 + wm * MI * 32 + i * 32 + (lane & 31);
+        const int64_t m = m0 + (wm * MI + i) * 32 + (lane & 31);
         if (m >= p.M) continue;
+        if (!kDual && m >= p.rows0 && m < p.split) continue;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int in = 8 * g + 4 * (lane >> 5);
-            if constexpr (EPI == Epi::kPlain) {
+        for (int q = 0; q < 2; ++q) {  // 8 columns each
+            if constexpr (!kDual) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int n = n0 + wn * 64 + j * 32 + in;
-                    T* row = m < p.split ? static_cast<T*>(p.c0) + m * p.ldc
-                                         : static_cast<T*>(p.c1) + (m - p.split) * p.ldc;
-                    const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1],
-                                        acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-                    store4(row, n, p.N, v);
-                }
-            } else if constexpr (EPI == Epi::kGate) {
-                const int n = n0 + wn * 32 + in;
-                float v[4];
+                    const int n = n0 + wn * 64 + j * 32 + 16 * h + 8 * q;
+                    float v[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = act_of<GELU>(acc[i][0][4 * g + e]) * acc[i][1][4 * g + e];
-                store4(static_cast<T*>(p.c0) + m * p.ldc, n, p.N, v);
+                    for (int e = 0; e < 8; ++e) v[e] = acc[i][j][8 * q + e];
+                    if (p.part != nullptr) {
+                        store8(p.part + (blockIdx.z * p.M + m) * p.N, n, p.N, v);
+                    } else {
+                        T* row = m < p.rows0 ? static_cast<T*>(p.c0) + m * p.ldc
+                                             : static_cast<T*>(p.c1) + (m - p.split) * p.ldc;
+                        store8(row, n, p.N, v);
+                    }
+                }
             } else {
-                const int n = n0 + wn * 32 + in;
-                float d[4], dg[4], du[4];
-                load4(static_cast<const T*>(p.dout) + m * p.N, n, p.N, d);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v, slope;
-                    act_grad<GELU>(acc[i][0][4 * g + e], v, slope);
-                    // columns behind the weights' last row are 0: the next product reads them
-                    dg[e] = n + e < p.N ? d[e] * acc[i][1][4 * g + e] * slope : 0.0f;
-                    du[e] = n + e < p.N ? d[e] * v : 0.0f;
-                }
+                const int n = n0 + wn * 32 + 16 * h + 8 * q;
                 T* row = static_cast<T*>(p.c0) + m * p.ldc;
-                store4(row, n, p.hp, dg);
-                store4(row + p.hp, n, p.hp, du);
+                float g[8], u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    g[e] = acc[i][0][8 * q + e];
+                    u[e] = acc[i][1][8 * q + e];
+                }
+                if constexpr (KIND == Kind::kGate) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] = act_of(g[e], p.gelu) * u[e];
+                    store8(row, n, p.N, g);
+                } else {
+                    const T* dout = static_cast<const T*>(p.dout) + m * p.N;
+                    float d[8] = {};
+                    if (n < p.N) {
+                        if (n + 8 <= p.N)
+                            to_f32<T, 8>(ld_raw<T, 8>(dout + MSEL_SPAN(n, 8, p.N)), d);
+                        else
+                            to_f32<T, 8>(ld_part<T, 8>(dout + n, p.N - n), d);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float v, slope;
+                        act_grad(g[e], p.gelu, v, slope);
+                        // columns behind the weights' last row are 0: the next products read them
+                        const bool in = n + e < p.N;
+                        g[e] = in ? d[e] * u[e] * slope : 0.0f;
+                        u[e] = in ? d[e] * v : 0.0f;
+                    }
+                    store8(row, n, p.hp, g);
+                    store8(row + p.hp, n, p.hp, u);
+                }
+            }
+        }
+    }
+}
+
+// Rows [0, rows0) of C to c0 and those from `split` on to c1, as sums of their parts in order.
+template <typename T>
+__global__ __launch_bounds__(256) void join_kernel(const float* part, int splits, int64_t M, int N,
+                                                   int64_t rows0, int64_t split, T* c0, T* c1) {
+    const int64_t n = M * N, end0 = rows0 * N, n1 = (M - split) * N;
+    const int64_t first = blockIdx.y == 0 ? 0 : split * N, len = blockIdx.y == 0 ? end0 : n1;
+    T* const c = blockIdx.y == 0 ? c0 : c1;
+    const float* const from = part + first;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < len;
+         i += static_cast<int64_t>(gridDim.x) * 1024) {
+        if (i + 4 <= len) {
+            float v[4] = {};
+            for (int s = 0; s < splits; ++s) {
+                float w[4];
+                to_f32<float, 4>(
+                    ld_raw<float, 4>(from + s * n + MSEL_SPAN(i, 4, n - first)), w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += w[e];
+            }
+            if constexpr (sizeof(T) == 4) {
+                st_vec<T, 4>(c + MSEL_SPAN(i, 4, len), v);
+            } else {
+                const uint32_t w[2] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                __builtin_memcpy(c + MSEL_SPAN(i, 4, len), w, 8);
+            }
+        } else {
+            for (int e = 0; i + e < len; ++e) {
+                float v = 0.0f;
+                for (int s = 0; s < splits; ++s) v += from[s * n + MSEL_IDX(i + e, n - first)];
+                Elem<T>::store1(c + MSEL_IDX(i + e, len), v);
             }
         }
     }
@@ -284,32 +424,6 @@ __global__ __launch_bounds__(256) void pad_kernel(const T* src, int64_t rows, in
     }
 }
 
-// dst[c][r] = src[r][c] for r < rows, 0 up to fill (<= ldd), over tiles of 64 x 64.
-template <typename T>
-__global__ __launch_bounds__(256) void transpose_kernel(const T* src, int64_t rows, int64_t cols,
-                                                        int64_t lds_, T* dst, int64_t ldd,
-                                                        int64_t fill) {
-    __shared__ T tile[64][66];
-    const int64_t tr = (fill + 63) / 64, tc = (cols + 63) / 64;
-    for (int64_t t = blockIdx.x; t < tr * tc; t += gridDim.x) {
-        const int64_t r0 = t % tr * 64, c0 = t / tr * 64;
-        const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-#pragma unroll 4
-        for (int k = y; k < 64; k += 4) {
-            T v{};
-            if (r0 + k < rows && c0 + x < cols)
-                v = src[MSEL_IDX((r0 + k) * lds_ + c0 + x, (rows - 1) * lds_ + cols)];
-            tile[k][x] = v;
-        }
-        __syncthreads();
-#pragma unroll 4
-        for (int k = y; k < 64; k += 4)
-            if (c0 + k < cols && r0 + x < fill)
-                dst[MSEL_IDX((c0 + k) * ldd + r0 + x, (cols - 1) * ldd + fill)] = tile[x][k];
-        __syncthreads();
-    }
-}
-
 constexpr unsigned kMaxBlocks = 1u << 20;
 
 template <typename T>
@@ -321,162 +435,218 @@ void pad(const void* src, int64_t rows, int64_t cols, void* dst, int64_t ldd, hi
                        static_cast<T*>(dst), ldd);
 }
 
-template <typename T>
-void transpose(const void* src, int64_t rows, int64_t cols, int64_t lds_, void* dst, int64_t ldd,
-               int64_t fill, hipStream_t stream) {
-    const int64_t tiles = (fill + 63) / 64 * ((cols + 63) / 64);
-    hipLaunchKernelGGL(transpose_kernel<T>,
-                       dim3(static_cast<unsigned>(std::min<int64_t>(tiles, kMaxBlocks))),
-                       dim3(256), 0, stream, static_cast<const T*>(src), rows, cols, lds_,
-                       static_cast<T*>(dst), ldd, fill);
+// ---- plans -------------------------------------------------------------------------------------
+
+int64_t over(int64_t n, int64_t q) { return (n + q - 1) / q; }
+
+// Tiles of a product and how its stages are split over blocks.
+struct ProductPlan {
+    int tile;    // 0: 256 x 256, 1: 128 x 128, 2: 64 x 128
+    int splits;
+};
+
+// The cheapest by a model in cycles: the rounds of blocks that the chip takes, each with its
+// stages' MFMA time at the share of the peak that such tiles reach and a fixed part, and for split
+// stages the parts' way through the last-level cache.
+ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf16) {
+    constexpr int rows_of[] = {256, 128, 64}, cols_of[] = {256, 128, 128};
+    constexpr double share16[] = {0.8, 0.65, 0.5}, share32[] = {0.95, 0.9, 0.85};
+    constexpr int kCus = 256;
+    ProductPlan best{1, 1};
+    double least = 0.0;
+    for (int t = 0; t < 3; ++t) {
+        const int64_t tiles = over(M, rows_of[t]) * over(cols, cols_of[t]);
+        const double stage = rows_of[t] * cols_of[t] * (bf16 ? 64 / 2048.0 / share16[t]
+                                                             : 32 / 128.0 / share32[t]);
+        for (int s = 1; s <= (dual(kind) ? 1 : 16) && (s == 1 || stages / s >= 4); ++s) {
+            // blocks that a CU holds together share its matrix cores: they take turns here
+            const double per = over(stages, s) * stage + 1000.0 + rows_of[t] * cols_of[t] / 12.0;
+            double cost = static_cast<double>(over(tiles * s, kCus)) * per;
+            if (s > 1) cost += 6000.0 + static_cast<double>(s) * M * cols * 8 / 3000.0;
+            if (least == 0.0 || cost < least) {
+                least = cost;
+                best = {t, s};
+            }
+        }
+    }
+    best.splits = static_cast<int>(over(stages, over(stages, best.splits)));
+    return best;
 }
 
-template <typename T, int WM, int WN, int MI, Epi EPI, bool GELU>
-hipError_t launch_tiles(ProductParams p, hipStream_t stream) {
+template <typename T, int WM, int WN, int MI, Kind KIND>
+hipError_t launch_tiles(ProductParams p, int splits, hipStream_t stream) {
     constexpr int BM = WM * MI * 32, BN = WN * 64;
     constexpr int bytes = 2 * (BM + BN) * kStageBytes;
-    const int bn = EPI == Epi::kPlain ? BN : BN / 2;
-    p.tm = static_cast<int>((p.M + BM - 1) / BM);
-    const int cols = EPI == Epi::kGateGrad ? p.hp : p.N;
-    p.tn = (cols + bn - 1) / bn;
-    const hipError_t e = allow_dynamic_lds<product_kernel<T, WM, WN, MI, EPI, GELU>>(bytes);
+    const int bn = dual(KIND) ? BN / 2 : BN;
+    p.tm = static_cast<int>(over(p.M, BM));
+    p.tn = static_cast<int>(over(KIND == Kind::kGateGrad ? p.hp : p.N, bn));
+    p.per_split = static_cast<int>(over(p.stages, splits));
+    const hipError_t e = allow_dynamic_lds<product_kernel<T, WM, WN, MI, KIND>>(bytes);
     if (e != hipSuccess) return e;
     const int64_t tiles = static_cast<int64_t>(p.tm) * p.tn;
-    const dim3 grid = tiles <= kMaxBlocks
-                          ? dim3(static_cast<unsigned>(tiles))
-                          : dim3(kMaxBlocks, static_cast<unsigned>((tiles + kMaxBlocks - 1) / kMaxBlocks));
-    hipLaunchKernelGGL((product_kernel<T, WM, WN, MI, EPI, GELU>), grid, dim3(WM * WN * 64), bytes,
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tiles, kMaxBlocks)),
+                    static_cast<unsigned>(over(tiles, kMaxBlocks)), static_cast<unsigned>(splits));
+    hipLaunchKernelGGL((product_kernel<T, WM, WN, MI, KIND>), grid, dim3(WM * WN * 64), bytes,
                        stream, p);
     return hipGetLastError();
 }
 
-// Tiles of 256 x 256 where they fill the chip, else of 128 x 128.
-template <typename T, Epi EPI, bool GELU>
-hipError_t launch_product(const ProductParams& p, hipStream_t stream) {
-    const int64_t cols = EPI == Epi::kPlain ? p.N : 2 * static_cast<int64_t>(p.N);
-    const int64_t wide = (p.M + 255) / 256 * ((cols + 255) / 256);
-    if (wide >= 256) return launch_tiles<T, 2, 4, 4, EPI, GELU>(p, stream);
-    return launch_tiles<T, 2, 2, 2, EPI, GELU>(p, stream);
+template <typename T, Kind KIND>
+hipError_t launch_product(const ProductParams& p, const ProductPlan& q, hipStream_t stream) {
+    switch (q.tile) {
+        case 0: return launch_tiles<T, 2, 4, 4, KIND>(p, q.splits, stream);
+        case 1: return launch_tiles<T, 2, 2, 2, KIND>(p, q.splits, stream);
+        default: return launch_tiles<T, 2, 2, 1, KIND>(p, q.splits, stream);
+    }
 }
 
-// ---- workspaces --------------------------------------------------------------------------------
+// A product whose stages may be split: its parts in `part`, then their sum.
+template <typename T, Kind KIND>
+hipError_t launch_split(ProductParams p, const ProductPlan& q, float* part, hipStream_t stream) {
+    if (q.splits == 1) return launch_product<T, KIND>(p, q, stream);
+    p.part = part;
+    const hipError_t e = launch_product<T, KIND>(p, q, stream);
+    if (e != hipSuccess) return e;
+    const int64_t blocks = std::min<int64_t>(over(p.rows0 * p.N, 1024), kMaxBlocks);
+    hipLaunchKernelGGL(join_kernel<T>, dim3(static_cast<unsigned>(blocks), p.split < p.M ? 2 : 1),
+                       dim3(256), 0, stream, part, q.splits, p.M, p.N, p.rows0, p.split,
+                       static_cast<T*>(p.c0), static_cast<T*>(p.c1));
+    return hipGetLastError();
+}
 
-int64_t up_to(int64_t n, int64_t q) { return (n + q - 1) / q * q; }
-
-// Offsets in bytes; absent parts take none.
+// Parts of the workspace: offsets in bytes, absent parts take none.
 struct MlpSpace {
-    int64_t dp, hp, mp;  // padded width, hidden width, tokens
-    size_t x = 0, wg = 0, wu = 0, wt = 0, dgu = 0, dgu_t = 0, x_t = 0, all = 0;
-    MlpSpace(const MlpParams& p, size_t elem, bool bwd) {
+    int64_t dp, hp;  // width and hidden width in whole stages
+    size_t x = 0, wg = 0, wu = 0, dgu = 0, part = 0, all = 0;
+    ProductPlan gate, input, weights;
+    MlpSpace(const MlpParams& p, bool bf16, bool bwd) {
+        const size_t elem = bf16 ? 2 : 4;
         const int64_t q = kStageBytes / static_cast<int64_t>(elem);
-        dp = up_to(p.D, q);
-        hp = up_to(p.F, q);
-        mp = up_to(p.M, q);
-        const auto take = [&](int64_t elems) {
+        dp = over(p.D, q) * q;
+        hp = over(p.F, q) * q;
+        const auto take = [&](size_t bytes) {
             const size_t at = all;
-            all += (static_cast<size_t>(elems) * elem + 255) / 256 * 256;
+            all += (bytes + 255) / 256 * 256;
             return at;
         };
         if (dp != p.D) {
-            x = take(p.M * dp);
-            wg = take(p.F * dp);
-            wu = take(p.F * dp);
+            x = take(static_cast<size_t>(p.M * dp) * elem);
+            wg = take(static_cast<size_t>(p.F * dp) * elem);
+            wu = take(static_cast<size_t>(p.F * dp) * elem);
         }
+        gate = plan_product(bwd ? Kind::kGateGrad : Kind::kGate, p.M, 2 * (bwd ? hp : p.F),
+                            static_cast<int>(dp / q), bf16);
         if (!bwd) return;
-        dgu = take(p.M * 2 * hp);
-        wt = take(p.D * 2 * hp);
-        dgu_t = take(2 * p.F * mp);
-        x_t = take(p.D * mp);
+        dgu = take(static_cast<size_t>(p.M * 2 * hp) * elem);
+        input = plan_product(Kind::kInput, p.M, p.D, static_cast<int>(2 * hp / q), bf16);
+        weights = plan_product(Kind::kWeights, hp + p.F, p.D,
+                               static_cast<int>(over(p.M, q)), bf16);
+        size_t parts = 0;  // of one product at a time
+        if (input.splits > 1) parts = static_cast<size_t>(input.splits) * p.M * p.D;
+        if (weights.splits > 1)
+            parts = std::max(parts, static_cast<size_t>(weights.splits) * (hp + p.F) * p.D);
+        part = take(parts * sizeof(float));
     }
 };
 
-template <typename T, bool GELU>
-hipError_t gate(const MlpParams& p, const MlpSpace& w, bool grad, hipStream_t stream) {
+// The operands with rows of whole stages.
+struct Padded {
+    const void* x;
+    const void* wg;
+    const void* wu;
+};
+template <typename T>
+Padded padded(const MlpParams& p, const MlpSpace& w, hipStream_t stream) {
+    if (w.dp == p.D) return {p.x, p.wg, p.wu};
     char* const ws = static_cast<char*>(p.ws);
+    pad<T>(p.x, p.M, p.D, ws + w.x, w.dp, stream);
+    pad<T>(p.wg, p.F, p.D, ws + w.wg, w.dp, stream);
+    pad<T>(p.wu, p.F, p.D, ws + w.wu, w.dp, stream);
+    return {ws + w.x, ws + w.wg, ws + w.wu};
+}
+
+template <typename T>
+ProductParams gate_params(const MlpParams& p, const MlpSpace& w, const Padded& o) {
     ProductParams q{};
     q.M = p.M;
     q.N = p.F;
     q.K = w.dp;
+    q.stages = q.half = static_cast<int>(w.dp / kStageK<T>);
     q.lda = q.ldb = w.dp;
-    q.a = p.x;
-    q.b0 = p.wg;
-    q.b1 = p.wu;
-    if (w.dp != p.D) {
-        pad<T>(p.x, p.M, p.D, ws + w.x, w.dp, stream);
-        pad<T>(p.wg, p.F, p.D, ws + w.wg, w.dp, stream);
-        pad<T>(p.wu, p.F, p.D, ws + w.wu, w.dp, stream);
-        q.a = ws + w.x;
-        q.b0 = ws + w.wg;
-        q.b1 = ws + w.wu;
-    }
-    if (!grad) {
-        q.c0 = p.out;
-        q.ldc = p.F;
-        return launch_product<T, Epi::kGate, GELU>(q, stream);
-    }
-    q.c0 = ws + w.dgu;
-    q.ldc = 2 * w.hp;
-    q.hp = static_cast<int>(w.hp);
-    q.dout = p.dout;
-    return launch_product<T, Epi::kGateGrad, GELU>(q, stream);
-}
-
-template <typename T>
-hipError_t backward(const MlpParams& p, hipStream_t stream) {
-    const MlpSpace w(p, sizeof(T), true);
-    char* const ws = static_cast<char*>(p.ws);
-    hipError_t e = p.gelu ? gate<T, true>(p, w, true, stream) : gate<T, false>(p, w, true, stream);
-    if (e != hipSuccess) return e;
-    if (p.dx != nullptr) {  // dx[m][d] = sum over 2 hp of dgu[m] wt[d]
-        T* const wt = reinterpret_cast<T*>(ws + w.wt);
-        transpose<T>(p.wg, p.F, p.D, p.D, wt, 2 * w.hp, w.hp, stream);
-        transpose<T>(p.wu, p.F, p.D, p.D, wt + w.hp, 2 * w.hp, w.hp, stream);
-        ProductParams q{};
-        q.M = q.split = p.M;
-        q.N = p.D;
-        q.K = q.lda = q.ldb = 2 * w.hp;
-        q.a = ws + w.dgu;
-        q.b0 = wt;
-        q.c0 = p.dx;
-        q.ldc = p.D;
-        e = launch_product<T, Epi::kPlain, false>(q, stream);
-        if (e != hipSuccess) return e;
-    }
-    if (p.dwg != nullptr) {  // dw[f][d] = sum over tokens of dgu_t[f] x_t[d]
-        T* const gt = reinterpret_cast<T*>(ws + w.dgu_t);
-        const T* const dgu = reinterpret_cast<const T*>(ws + w.dgu);
-        transpose<T>(dgu, p.M, p.F, 2 * w.hp, gt, w.mp, w.mp, stream);
-        transpose<T>(dgu + w.hp, p.M, p.F, 2 * w.hp, gt + p.F * w.mp, w.mp, w.mp, stream);
-        transpose<T>(p.x, p.M, p.D, p.D, ws + w.x_t, w.mp, w.mp, stream);
-        ProductParams q{};
-        q.M = 2 * static_cast<int64_t>(p.F);
-        q.split = p.F;
-        q.N = p.D;
-        q.K = q.lda = q.ldb = w.mp;
-        q.a = gt;
-        q.b0 = ws + w.x_t;
-        q.c0 = p.dwg;
-        q.c1 = p.dwu;
-        q.ldc = p.D;
-        e = launch_product<T, Epi::kPlain, false>(q, stream);
-    }
-    return e;
+    q.a = o.x;
+    q.b0 = o.wg;
+    q.b1 = o.wu;
+    q.gelu = p.gelu;
+    return q;
 }
 
 template <typename T>
 hipError_t forward(const MlpParams& p, hipStream_t stream) {
-    const MlpSpace w(p, sizeof(T), false);
-    return p.gelu ? gate<T, true>(p, w, false, stream) : gate<T, false>(p, w, false, stream);
+    const MlpSpace w(p, sizeof(T) == 2, false);
+    ProductParams q = gate_params<T>(p, w, padded<T>(p, w, stream));
+    q.c0 = p.out;
+    q.ldc = p.F;
+    return launch_product<T, Kind::kGate>(q, w.gate, stream);
+}
+
+template <typename T>
+hipError_t backward(const MlpParams& p, hipStream_t stream) {
+    const MlpSpace w(p, sizeof(T) == 2, true);
+    char* const ws = static_cast<char*>(p.ws);
+    float* const part = reinterpret_cast<float*>(ws + w.part);
+    const Padded o = padded<T>(p, w, stream);
+    ProductParams q = gate_params<T>(p, w, o);
+    q.c0 = ws + w.dgu;
+    q.ldc = 2 * w.hp;
+    q.hp = static_cast<int>(w.hp);
+    q.dout = p.dout;
+    hipError_t e = launch_product<T, Kind::kGateGrad>(q, w.gate, stream);
+    if (e != hipSuccess) return e;
+    if (p.dx != nullptr) {
+        ProductParams r{};
+        r.M = r.rows0 = r.split = p.M;
+        r.N = p.D;
+        r.K = p.F;
+        r.half = static_cast<int>(w.hp / kStageK<T>);
+        r.stages = 2 * r.half;
+        r.a = ws + w.dgu;
+        r.lda = 2 * w.hp;
+        r.b0 = o.wg;
+        r.b1 = o.wu;
+        r.ldb = r.wb = w.dp;
+        r.c0 = p.dx;
+        r.ldc = p.D;
+        e = launch_split<T, Kind::kInput>(r, w.input, part, stream);
+        if (e != hipSuccess) return e;
+    }
+    if (p.dwg != nullptr) {
+        ProductParams r{};
+        r.M = w.hp + p.F;  // dG's columns, a gap up to hp, dU's
+        r.rows0 = p.F;
+        r.split = w.hp;
+        r.N = p.D;
+        r.K = p.M;
+        r.stages = r.half = static_cast<int>(over(p.M, kStageK<T>));
+        r.a = ws + w.dgu;
+        r.lda = r.wa = 2 * w.hp;
+        r.b0 = r.b1 = o.x;
+        r.ldb = r.wb = w.dp;
+        r.ldc = p.D;
+        r.c0 = p.dwg;
+        r.c1 = p.dwu;
+        e = launch_split<T, Kind::kWeights>(r, w.weights, part, stream);
+    }
+    return e;
 }
 
 }  // namespace
 
 size_t mlp_fwd_workspace_bytes(const MlpParams& p, bool bf16) {
-    return MlpSpace(p, bf16 ? 2 : 4, false).all;
+    return MlpSpace(p, bf16, false).all;
 }
 
 size_t mlp_bwd_workspace_bytes(const MlpParams& p, bool bf16) {
-    return MlpSpace(p, bf16 ? 2 : 4, true).all;
+    return MlpSpace(p, bf16, true).all;
 }
 
 hipError_t launch_mlp_fwd(const MlpParams& p, bool bf16, hipStream_t stream) {
