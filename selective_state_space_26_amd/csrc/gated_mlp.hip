@@ -4,8 +4,8 @@
 //
 // The matrix cores bound it.  A block computes a tile of C with both operands staged in LDS, one
 // stage of 128 bytes of k ahead, loaded without a register between (global_load_lds).  A row of a
-// stage is 8 chunks of 16 bytes, chunk c of row r at place c ^ (r & 7): the 8 lanes that LDS serves
-// together read one chunk of 8 rows, which then lie in 8 different places.  In the fused product the
+// stage is 8 chunks of 16 bytes, chunk c of row r at place c ^ (r / 2 & 7): the 16 lanes that LDS
+// serves together read one chunk of 16 rows, which then cover all 64 banks.  In the fused product the
 // B rows of a wavefront are 32 rows of Wg and the same 32 of Wu, so that a lane holds G and U of the
 // same elements and the activation and the product need no exchange.
 // The MFMA's rows are C's columns, so that a lane holds consecutive columns of a row of C.  The
@@ -130,8 +130,8 @@ __device__ __forceinline__ int order32(int i) {
 
 // An operand of W rows (or columns of C's side) per stage in LDS, by chunks of 16 bytes.
 //
-// Consecutive k: [W][8 chunks], chunk c of row r at place c ^ (r & 7): the 8 lanes that LDS serves
-// together read one chunk of 8 rows, in 8 different places.  ORDER: rows in the order order32.
+// Consecutive k: [W][8 chunks], chunk c of row r at place c ^ (r / 2 & 7): two rows are as long as
+// the 64 banks, and the 16 lanes that LDS serves together read one chunk of 16 rows.  ORDER: rows in the order order32.
 //
 // By rows of k: [rows of k][W columns].  bf16 fragments are read with the transposing read, which
 // gives each lane of 16 the 4 values of its column from 4 rows of 16 columns; two such groups read
@@ -144,7 +144,7 @@ struct Operand {
     static constexpr int kChunks = BY_ROWS ? W / kPerChunk : 8;  // of a row in LDS
 
     __device__ __forceinline__ static int swizzle(int r) {
-        if constexpr (!BY_ROWS) return r & 7;
+        if constexpr (!BY_ROWS) return (r >> 1) & 7;
         if constexpr (sizeof(T) == 4) return ((r >> 2) & 1) << 3;
         return kChunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
     }
@@ -154,7 +154,7 @@ struct Operand {
         if constexpr (!BY_ROWS) {
             const int r = f * 32 + (lane & 31);
             return *reinterpret_cast<const u32x4*>(at + r * kStageBytes +
-                                                   (((2 * s + h) ^ (lane & 7)) * 16));
+                                                   (((2 * s + h) ^ swizzle(lane)) * 16));
         } else if constexpr (sizeof(T) == 4) {
             const int c = f * 32 + (ORDER ? order32(lane & 31) : lane & 31);
             u32x4 v;
