@@ -2,10 +2,13 @@
 //   dG = dout U act'(G), dU = dout act(G);  dx = dG Wg + dU Wu;  dWg = dG^T x, dWu = dU^T x
 // as MFMA products of rows with consecutive k: C[m][n] = sum_k A[m][k] B[n][k].
 //
-// The matrix cores bound it.  A block computes a tile of C with both operands staged in LDS, one
-// stage of 128 bytes of k ahead, loaded without a register between (global_load_lds).  A row of a
-// stage is 8 chunks of 16 bytes, chunk c of row r at place c ^ (r / 2 & 7): the 16 lanes that LDS
-// serves together read one chunk of 16 rows, which then cover all 64 banks.  In the fused product the
+// The matrix cores bound it.  A block computes a tile of C with both operands staged in LDS, two
+// stages of 128 bytes of k in turn, loaded without a register between (global_load_lds).  A step's
+// fragments are read from LDS during the MFMAs of the step before, across the stages' borders too:
+// a stage's place is loaded again as soon as its last fragments have been read, before they are
+// used.  A row of a stage is 8 chunks of 16 bytes, chunk c of row r at place c ^ (r / 2 & 7): the 16
+// lanes that LDS serves together read one chunk of 16 rows, which then cover all 64 banks.  The
+// result goes out through LDS too, in whole rows of the tile.  In the fused product the
 // B rows of a wavefront are 32 rows of Wg and the same 32 of Wu, so that a lane holds G and U of the
 // same elements and the activation and the product need no exchange.
 // The MFMA's rows are C's columns, so that a lane holds consecutive columns of a row of C.  The
@@ -28,6 +31,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStageBytes = 128;  // of k per stage
+constexpr int kRing = 2;          // stages in LDS
 constexpr int kSteps = kStageBytes / 32;
 
 template <typename T>
@@ -107,16 +111,6 @@ __device__ __forceinline__ bool tile_at(const ProductParams& p, int& m, int& n) 
     return true;
 }
 
-// 8 values into columns [col, col + 8) of a row of n columns.
-template <typename T>
-__device__ __forceinline__ void store8(T* row, int col, int n, const float (&v)[8]) {
-    const RawVec<T, 8> r = from_f32<T, 8>(v);
-    if (col + 8 <= n)
-        st_raw<T, 8>(row + MSEL_SPAN(col, 8, n), r);
-    else if (col < n)
-        st_part<T, 8>(row + col, r, n - col);
-}
-
 typedef __attribute__((address_space(1))) const void GlobalVoid;
 typedef __attribute__((address_space(3))) void LdsVoid;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -141,7 +135,7 @@ template <typename T, int W, bool BY_ROWS, bool ORDER>
 struct Operand {
     static constexpr int kBytes = W * kStageBytes;
     static constexpr int kPerChunk = 16 / static_cast<int>(sizeof(T));
-    static constexpr int kChunks = BY_ROWS ? W / kPerChunk : 8;  // of a row in LDS
+    static constexpr int kChunks = BY_ROWS ? W / kPerChunk : kStageBytes / 16;  // of a row in LDS
 
     __device__ __forceinline__ static int swizzle(int r) {
         if constexpr (!BY_ROWS) return (r >> 1) & 7;
@@ -188,6 +182,56 @@ struct Operand {
     }
 };
 
+// A tile of C on its way out: BM rows of W columns of type U in LDS, in chunks of 16 bytes, swizzled
+// so that 16 rows of one chunk (a wavefront writes them) and a row's chunks (it reads them) both
+// cover all banks.
+template <typename U, int W>
+struct OutTile {
+    static constexpr int kPerChunk = 16 / static_cast<int>(sizeof(U));
+    static constexpr int kChunks = W / kPerChunk;
+    __device__ __forceinline__ static int place(int r, int c) {
+        return (r * kChunks + (c ^ (kChunks == 8 ? (r >> 1) & 7 : r & 15))) * 16;
+    }
+    // 16 columns from `col` on of row r
+    __device__ __forceinline__ static void put(char* lds, int r, int col, const float (&v)[16]) {
+#pragma unroll
+        for (int q = 0; q < 16 / kPerChunk; ++q) {
+            float w[kPerChunk];
+#pragma unroll
+            for (int e = 0; e < kPerChunk; ++e) w[e] = v[q * kPerChunk + e];
+            const RawVec<U, kPerChunk> raw = from_f32<U, kPerChunk>(w);
+            __builtin_memcpy(lds + place(r, col / kPerChunk + q), &raw, 16);
+        }
+    }
+    __device__ __forceinline__ static void get(const char* lds, int r, int col, float (&v)[16]) {
+#pragma unroll
+        for (int q = 0; q < 16 / kPerChunk; ++q) {
+            RawVec<U, kPerChunk> raw;
+            __builtin_memcpy(&raw, lds + place(r, col / kPerChunk + q), 16);
+            float w[kPerChunk];
+            to_f32<U, kPerChunk>(raw, w);
+#pragma unroll
+            for (int e = 0; e < kPerChunk; ++e) v[q * kPerChunk + e] = w[e];
+        }
+    }
+};
+
+// Up to a vector's columns of a row of n: columns [col, col + VE).
+template <typename U, int VE>
+__device__ __forceinline__ void store_columns(U* row, int col, int n, const RawVec<U, VE>& r) {
+    if (col + VE <= n)
+        st_raw<U, VE>(row + MSEL_SPAN(col, VE, n), r);
+    else if (col < n)
+        st_part<U, VE>(row + col, r, n - col);
+}
+
+// All but the n loads issued last have landed, here and in the other wavefronts, and what this one
+// read from LDS has arrived.
+template <int N>
+__device__ __forceinline__ void barrier_after() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 // WM x WN wavefronts, each MI x 2 MFMA tiles of 32 x 32: a block computes WM MI 32 rows by
 // WN 64 columns (in the fused products WN 32 columns of both weights).
 template <typename T, int WM, int WN, int MI, Kind KIND>
@@ -200,6 +244,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     using OpB = Operand<T, BN, kRowsB, true>;
     constexpr int LA = OpA::kBytes / 16 / kThreads, LB = OpB::kBytes / 16 / kThreads;
     constexpr int kStage = OpA::kBytes + OpB::kBytes;
+    constexpr int CW = kDual ? BN / 2 : BN;  // columns of C
     static_assert(LA * kThreads * 16 == OpA::kBytes && LB * kThreads * 16 == OpB::kBytes,
                   "whole rounds");
     extern __shared__ __align__(16) char lds[];
@@ -277,101 +322,198 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-    const int first = blockIdx.z * p.per_split, last = min(p.stages, first + p.per_split);
-    load_stage(first, 0);
-    for (int k = first; k < last; ++k) {
-        const int buf = (k - first) & 1;
-        __syncthreads();  // the stage has landed, and the other buffer has been read
-        if (kRowsB) {
-            const int rows = rows_of(k);
-            if (rows < kStageK<T>) {  // uniform
-                const u32x4 zero = {0, 0, 0, 0};
-                char* at = lds + buf * kStage;
-                if (kRowsA)
-                    for (int i = rows * OpA::kChunks + tid; i < OpA::kBytes / 16; i += kThreads)
-                        *reinterpret_cast<u32x4*>(at + i * 16) = zero;
-                for (int i = rows * OpB::kChunks + tid; i < OpB::kBytes / 16; i += kThreads)
-                    *reinterpret_cast<u32x4*>(at + OpA::kBytes + i * 16) = zero;
-                __syncthreads();
-            }
+    // kGateGrad: dout's tile in the order in which the results go out
+    constexpr int VE = 16 / static_cast<int>(sizeof(T));
+    constexpr int kOut = BM * CW / VE / kThreads;
+    RawVec<T, VE> dout[KIND == Kind::kGateGrad ? kOut : 1];
+    if constexpr (KIND == Kind::kGateGrad) {
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) {
+            const int at = i * kThreads + tid, n = n0 + at % (CW / VE) * VE;
+            const int64_t m = min(m0 + at / (CW / VE), p.M - 1);
+            const T* row = static_cast<const T*>(p.dout) + MSEL_IDX(m, p.M) * p.N;
+            if (n + VE <= p.N)
+                dout[i] = ld_raw<T, VE>(row + MSEL_SPAN(n, VE, p.N));
+            else
+                dout[i] = ld_part<T, VE>(row + n, p.N - n);
         }
-        if (k + 1 < last) load_stage(k + 1, buf ^ 1);
-        const char* sa = lds + buf * kStage;
-        const char* sb = sa + OpA::kBytes;
+    }
+
+    const int first = blockIdx.z * p.per_split, last = min(p.stages, first + p.per_split);
+    // waits for stage k, which has `after` loads behind it; rows of k past the end become 0
+    const auto enter_stage = [&](int k, auto after) {
+        barrier_after<decltype(after)::value>();
+        if (!kRowsB || rows_of(k) == kStageK<T>) return;  // uniform
+        const int rows = rows_of(k);
+        const u32x4 zero = {0, 0, 0, 0};
+        char* at = lds + ((k - first) & 1) * kStage;
+        if (kRowsA)
+            for (int i = rows * OpA::kChunks + tid; i < OpA::kBytes / 16; i += kThreads)
+                *reinterpret_cast<u32x4*>(at + i * 16) = zero;
+        for (int i = rows * OpB::kChunks + tid; i < OpB::kBytes / 16; i += kThreads)
+            *reinterpret_cast<u32x4*>(at + OpA::kBytes + i * 16) = zero;
+        __syncthreads();
+    };
+    u32x4 fa[2][MI], fb[2][2];  // fragments of a step and of the next
+    const auto read_step = [&](int k, int s, int to) {
+        const char* sa = lds + ((k - first) & 1) * kStage;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) fa[to][i] = OpA::read(sa, wm * MI + i, s, lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) fb[to][j] = OpB::read(sa + OpA::kBytes, wn * 2 + j, s, lane);
+    };
+    load_stage(first, 0);
+    if (first + 1 < last) {
+        load_stage(first + 1, 1);
+        enter_stage(first, std::integral_constant<int, LA + LB>());
+    } else {
+        enter_stage(first, std::integral_constant<int, 0>());
+    }
+    read_step(first, 0, 0);
+    for (int k = first; k < last; ++k) {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            u32x4 fa[MI], fb[2];
-#pragma unroll
-            for (int i = 0; i < MI; ++i) fa[i] = OpA::read(sa, wm * MI + i, s, lane);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) fb[j] = OpB::read(sb, wn * 2 + j, s, lane);
+            const int cur = s & 1;
+            if (s + 1 < kSteps) {
+                read_step(k, s + 1, cur ^ 1);
+            } else if (k + 1 < last) {
+                enter_stage(k + 1, std::integral_constant<int, 0>());
+                if (k + 2 < last) load_stage(k + 2, (k - first) & 1);
+                read_step(k + 1, 0, cur ^ 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);  // the reads first, the MFMAs over their latency
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    mfma_step(static_cast<const T*>(nullptr), fb[j], fa[i], acc[i][j]);
+                    mfma_step(static_cast<const T*>(nullptr), fb[cur][j], fa[cur][i], acc[i][j]);
         }
     }
+    __syncthreads();  // the ring becomes the tile on its way out
 
-    // lane l holds 16 columns from 16 (l / 32) on of row l % 32
-    const int h = lane >> 5;
+    // lane l holds 16 columns from 16 (l / 32) on of row l % 32 of its fragments
+    const int h16 = (lane >> 5) * 16, r0 = wm * MI * 32 + (lane & 31);
+    const auto values = [](const f32x16& a, float (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int64_t m = m0 + (wm * MI + i) * 32 + (lane & 31);
-        if (m >= p.M) continue;
-        if (!kDual && m >= p.rows0 && m < p.split) continue;
+        for (int e = 0; e < 16; ++e) v[e] = a[e];
+    };
+    // rows of a tile of W columns of type U to dst(row of C, first column in the tile, chunk)
+    const auto send = [&](auto tile, auto dst) {
+        using Tile = decltype(tile);
+        __syncthreads();
+        for (int at = tid; at < BM * Tile::kChunks; at += kThreads) {
+            const int r = at / Tile::kChunks, c = at % Tile::kChunks;
+            if (m0 + r < p.M) dst(m0 + r, c * Tile::kPerChunk, lds + Tile::place(r, c));
+        }
+    };
+    if constexpr (kDual) {
+        using Tile = OutTile<T, CW>;
+        static_assert(BM * CW * sizeof(T) <= kRing * kStage, "the tile fits where the ring was");
+        const int col = wn * 32 + h16;
+        const auto to = [&](int shift, int cols) {
+            return [&, shift, cols](int64_t m, int c, const char* from) {
+                RawVec<T, VE> raw;
+                __builtin_memcpy(&raw, from, 16);
+                store_columns<T, VE>(static_cast<T*>(p.c0) + m * p.ldc + shift, n0 + c, cols, raw);
+            };
+        };
+        if constexpr (KIND == Kind::kGate) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {  // 8 columns each
-            if constexpr (!kDual) {
+            for (int i = 0; i < MI; ++i) {
+                float g[16], u[16];
+                values(acc[i][0], g);
+                values(acc[i][1], u);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) g[e] = act_of(g[e], p.gelu) * u[e];
+                Tile::put(lds, r0 + i * 32, col, g);
+            }
+            send(Tile(), to(0, p.N));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) {
+                const int at = i * kThreads + tid;
+                __builtin_memcpy(lds + Tile::place(at / Tile::kChunks, at % Tile::kChunks),
+                                 &dout[i], 16);
+            }
+            __syncthreads();
+            // dG over dout, a lane's own columns; dU waits where U was
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                float d[16], g[16], u[16];
+                Tile::get(lds, r0 + i * 32, col, d);
+                values(acc[i][0], g);
+                values(acc[i][1], u);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float v, slope;
+                    act_grad(g[e], p.gelu, v, slope);
+                    // columns behind the weights' last row are 0: the next products read them
+                    const bool in = n0 + col + e < p.N;
+                    g[e] = in ? d[e] * u[e] * slope : 0.0f;
+                    acc[i][1][e] = in ? d[e] * v : 0.0f;
+                }
+                Tile::put(lds, r0 + i * 32, col, g);
+            }
+            send(Tile(), to(0, p.hp));
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                float u[16];
+                values(acc[i][1], u);
+                Tile::put(lds, r0 + i * 32, col, u);
+            }
+            send(Tile(), to(p.hp, p.hp));
+        }
+    } else {
+        // fp32 in two halves: the first 32 of each wavefront's 64 columns, then the others
+        const auto halves = [&](auto row_of) {
+            using Tile = OutTile<float, BN / 2>;
+            static_assert(BM * BN / 2 * sizeof(float) <= kRing * kStage, "fits");
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (j > 0) __syncthreads();
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    float v[16];
+                    values(acc[i][j], v);
+                    Tile::put(lds, r0 + i * 32, wn * 32 + h16, v);
+                }
+                send(Tile(), [&](int64_t m, int c, const char* from) {
+                    float* row = row_of(m);
+                    RawVec<float, 4> raw;
+                    __builtin_memcpy(&raw, from, 16);
+                    const int n = n0 + (c >> 5) * 64 + j * 32 + (c & 31);
+                    if (row != nullptr) store_columns<float, 4>(row, n, p.N, raw);
+                });
+            }
+        };
+        const auto row_of = [&](int64_t m) -> T* {
+            return m < p.rows0    ? static_cast<T*>(p.c0) + m * p.ldc
+                   : m >= p.split ? static_cast<T*>(p.c1) + (m - p.split) * p.ldc
+                                  : nullptr;
+        };
+        if (p.part != nullptr) {
+            halves([&](int64_t m) { return p.part + (blockIdx.z * p.M + m) * p.N; });
+        } else if constexpr (sizeof(T) == 4) {
+            halves(row_of);
+        } else {
+            using Tile = OutTile<T, BN>;
+            static_assert(BM * BN * sizeof(T) <= kRing * kStage, "fits");
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int n = n0 + wn * 64 + j * 32 + 16 * h + 8 * q;
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = acc[i][j][8 * q + e];
-                    if (p.part != nullptr) {
-                        store8(p.part + (blockIdx.z * p.M + m) * p.N, n, p.N, v);
-                    } else {
-                        T* row = m < p.rows0 ? static_cast<T*>(p.c0) + m * p.ldc
-                                             : static_cast<T*>(p.c1) + (m - p.split) * p.ldc;
-                        store8(row, n, p.N, v);
-                    }
-                }
-            } else {
-                const int n = n0 + wn * 32 + 16 * h + 8 * q;
-                T* row = static_cast<T*>(p.c0) + m * p.ldc;
-                float g[8], u[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    g[e] = acc[i][0][8 * q + e];
-                    u[e] = acc[i][1][8 * q + e];
-                }
-                if constexpr (KIND == Kind::kGate) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) g[e] = act_of(g[e], p.gelu) * u[e];
-                    store8(row, n, p.N, g);
-                } else {
-                    const T* dout = static_cast<const T*>(p.dout) + m * p.N;
-                    float d[8] = {};
-                    if (n < p.N) {
-                        if (n + 8 <= p.N)
-                            to_f32<T, 8>(ld_raw<T, 8>(dout + MSEL_SPAN(n, 8, p.N)), d);
-                        else
-                            to_f32<T, 8>(ld_part<T, 8>(dout + n, p.N - n), d);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float v, slope;
-                        act_grad(g[e], p.gelu, v, slope);
-                        // columns behind the weights' last row are 0: the next products read them
-                        const bool in = n + e < p.N;
-                        g[e] = in ? d[e] * u[e] * slope : 0.0f;
-                        u[e] = in ? d[e] * v : 0.0f;
-                    }
-                    store8(row, n, p.hp, g);
-                    store8(row + p.hp, n, p.hp, u);
+                    float v[16];
+                    values(acc[i][j], v);
+                    Tile::put(lds, r0 + i * 32, wn * 64 + j * 32 + h16, v);
                 }
             }
+            send(Tile(), [&](int64_t m, int c, const char* from) {
+                T* row = row_of(m);
+                RawVec<T, VE> raw;
+                __builtin_memcpy(&raw, from, 16);
+                if (row != nullptr) store_columns<T, VE>(row, n0 + c, p.N, raw);
+            });
         }
     }
 }
@@ -476,7 +618,7 @@ ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf
 template <typename T, int WM, int WN, int MI, Kind KIND>
 hipError_t launch_tiles(ProductParams p, int splits, hipStream_t stream) {
     constexpr int BM = WM * MI * 32, BN = WN * 64;
-    constexpr int bytes = 2 * (BM + BN) * kStageBytes;
+    constexpr int bytes = kRing * (BM + BN) * kStageBytes;
     const int bn = dual(KIND) ? BN / 2 : BN;
     p.tm = static_cast<int>(over(p.M, BM));
     p.tn = static_cast<int>(over(KIND == Kind::kGateGrad ? p.hp : p.N, bn));
