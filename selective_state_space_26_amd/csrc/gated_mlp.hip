@@ -202,6 +202,7 @@ template <typename U, int W>
 struct OutTile {
     static constexpr int kPerChunk = 16 / static_cast<int>(sizeof(U));
     static constexpr int kChunks = W / kPerChunk;
+    static_assert(kChunks == 8 || kChunks % 16 == 0, "the swizzle stays inside a row");
     __device__ __forceinline__ static int place(int r, int c) {
         return (r * kChunks + (c ^ (kChunks == 8 ? (r >> 1) & 7 : r & 15))) * 16;
     }
@@ -688,29 +689,33 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, int splits
     }
 }
 
-// dst[r][c] = src[r][c] for c < cols, 0 up to ldd.
+// The operands' rows, padded with zeros to whole stages: dst[r][c] = src[r][c] for c < cols, 0 up to
+// ldd; one operand per blockIdx.y.
+struct PadParams {
+    const void* src[3];
+    void* dst[3];
+    int64_t rows[3];
+    int cols, ldd;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void pad_kernel(const T* src, int64_t rows, int64_t cols, T* dst,
-                                                  int64_t ldd) {
-    const int64_t n = rows * ldd;
+__global__ __launch_bounds__(256) void pad_kernel(PadParams p) {
+    constexpr int VE = 16 / static_cast<int>(sizeof(T));
+    const T* const src = static_cast<const T*>(p.src[blockIdx.y]);
+    T* const dst = static_cast<T*>(p.dst[blockIdx.y]);
+    const int per = p.ldd / VE;
+    const int64_t n = p.rows[blockIdx.y] * per;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = i / ldd, c = i - r * ldd;
-        const float v = c < cols ? Elem<T>::load1(src + MSEL_IDX(r * cols + c, rows * cols)) : 0.0f;
-        Elem<T>::store1(dst + MSEL_IDX(i, n), v);
+        const int64_t r = i / per;
+        const int c = static_cast<int>(i - r * per) * VE;
+        const T* row = src + MSEL_IDX(r, p.rows[blockIdx.y]) * p.cols;
+        const RawVec<T, VE> v = c + VE <= p.cols ? ld_raw<T, VE>(row + MSEL_SPAN(c, VE, p.cols))
+                                                 : ld_part<T, VE>(row + c, p.cols - c);
+        st_raw<T, VE>(dst + MSEL_IDX(i, n) * VE, v);
     }
 }
 
 constexpr unsigned kMaxBlocks = 1u << 20;
-
-template <typename T>
-void pad(const void* src, int64_t rows, int64_t cols, void* dst, int64_t ldd, hipStream_t stream) {
-    const int64_t blocks = (rows * ldd + 1023) / 1024;
-    hipLaunchKernelGGL(pad_kernel<T>,
-                       dim3(static_cast<unsigned>(std::min<int64_t>(blocks, kMaxBlocks))),
-                       dim3(256), 0, stream, static_cast<const T*>(src), rows, cols,
-                       static_cast<T*>(dst), ldd);
-}
 
 // ---- plans -------------------------------------------------------------------------------------
 
@@ -722,24 +727,29 @@ struct ProductPlan {
     int splits;
 };
 
-// The cheapest by a model in cycles: the rounds of blocks that the chip takes, each with its
-// stages' MFMA time at the share of the peak that such tiles reach and a fixed part, and for split
-// stages the parts' way through the last-level cache.
+// The cheapest by a model in cycles: the blocks of a CU take turns on its matrix cores, at the share
+// of the peak that such tiles reach (256 x 256: 2.2 us a stage, 128 x 128: 0.84, 64 x 128: 0.42), but
+// a stage takes no less than the way of its loads, which the blocks that a CU holds share; then a
+// fixed part per block, and for split stages the parts' way through the last-level cache.  16384 x
+// 768 by 4096: 256 x 256 without a split 140 us, 128 x 128 162; 1024 rows: 8 parts 20 us, one 60.
 ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf16) {
-    constexpr int rows_of[] = {256, 128, 64}, cols_of[] = {256, 128, 128};
-    constexpr double share16[] = {0.8, 0.52, 0.5}, share32[] = {0.95, 0.9, 0.85};
+    constexpr int rows_of[] = {256, 128, 64}, cols_of[] = {256, 128, 128}, held[] = {1, 2, 3};
+    constexpr double share16[] = {0.8, 0.52, 0.5}, share32[] = {0.74, 0.74, 0.7};
     constexpr int kCus = 256;
+    constexpr double kLoads = 2000.0;
     ProductPlan best{1, 1};
     double least = 0.0;
     for (int t = 0; t < 3; ++t) {
         const int64_t tiles = over(M, rows_of[t]) * over(cols, cols_of[t]);
-        const double stage = rows_of[t] * cols_of[t] * (bf16 ? 64 / 2048.0 / share16[t]
-                                                             : 32 / 128.0 / share32[t]);
+        const double area = rows_of[t] * cols_of[t];
+        const double stage = area * (bf16 ? 64 / 2048.0 / share16[t] : 32 / 128.0 / share32[t]);
         for (int s = 1; s <= (dual(kind) ? 1 : 16) && (s == 1 || stages / s >= 4); ++s) {
-            // blocks that a CU holds together share its matrix cores: they take turns here
-            const double per = over(stages, s) * stage + 1000.0 + rows_of[t] * cols_of[t] / 12.0;
-            double cost = static_cast<double>(over(tiles * s, kCus)) * per;
-            if (s > 1) cost += 6000.0 + static_cast<double>(s) * M * cols * 8 / 3000.0;
+            const int64_t turns = over(tiles * s, kCus), full = turns / held[t];
+            const int rest = static_cast<int>(turns % held[t]);
+            const double a_stage = full * std::max(held[t] * stage, kLoads) +
+                                   (rest > 0 ? std::max(rest * stage, kLoads) : 0.0);
+            double cost = over(stages, s) * a_stage + turns * (1000.0 + area / 12.0);
+            if (s > 1) cost += 4000.0 + static_cast<double>(s) * M * cols * 8 / 6000.0;
             if (least == 0.0 || cost < least) {
                 least = cost;
                 best = {t, s};
@@ -837,9 +847,12 @@ template <typename T>
 Padded padded(const MlpParams& p, const MlpSpace& w, hipStream_t stream) {
     if (w.dp == p.D) return {p.x, p.wg, p.wu};
     char* const ws = static_cast<char*>(p.ws);
-    pad<T>(p.x, p.M, p.D, ws + w.x, w.dp, stream);
-    pad<T>(p.wg, p.F, p.D, ws + w.wg, w.dp, stream);
-    pad<T>(p.wu, p.F, p.D, ws + w.wu, w.dp, stream);
+    const PadParams q{{p.x, p.wg, p.wu}, {ws + w.x, ws + w.wg, ws + w.wu}, {p.M, p.F, p.F}, p.D,
+                      static_cast<int>(w.dp)};
+    const int64_t blocks = over(std::max<int64_t>(p.M, p.F) * w.dp * sizeof(T), 256 * 16);
+    hipLaunchKernelGGL(pad_kernel<T>,
+                       dim3(static_cast<unsigned>(std::min<int64_t>(blocks, kMaxBlocks)), 3),
+                       dim3(256), 0, stream, q);
     return {ws + w.x, ws + w.wg, ws + w.wu};
 }
 
