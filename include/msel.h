@@ -791,7 +791,8 @@ msel_status msel_validate_logprob_bwd(const msel_logprob_args *args,
                                       const msel_logprob_grads *grads);
 /* Bytes of workspace msel_logprob_fwd needs: 0 unless few rows are shared by several blocks. */
 size_t msel_logprob_fwd_workspace_bytes(const msel_logprob_args *args);
-/* Both deterministic; the workspace is 256-byte aligned. */
+/* Both deterministic (for rows at the same place in their lines of memory: sums start with a line);
+ * the workspace is 256-byte aligned. */
 msel_status msel_logprob_fwd(const msel_logprob_args *args, void *workspace,
                              size_t workspace_bytes, hipStream_t stream);
 msel_status msel_logprob_bwd(const msel_logprob_args *args, const msel_logprob_grads *grads,

@@ -29,7 +29,6 @@ namespace {
 
 constexpr float kLowest = -3.402823466e38f;
 constexpr int kThreads = 256;
-constexpr int kNarrowVecs = 4;      // vectors per lane of a row in registers
 constexpr int kCandidates = 1024;
 constexpr unsigned kMaxBlocks = 1u << 22;  // a grid has fewer than 2^32 threads
 // beyond it an fp32 lse has fewer than 13 bits behind the point: the backward sums the row again
@@ -175,12 +174,12 @@ __device__ __forceinline__ void write_top(const LogprobParams& p, int64_t r, int
     p.top_logprobs[at] = o.logprob(value_of(k), p.scale);
 }
 
-// ---- narrow rows: TEAM lanes hold a row in registers -------------------------------------------
+// ---- narrow rows: TEAM lanes hold a row in registers, N vectors each ----------------------------
 
-template <typename T, int TEAM>
+template <typename T, int TEAM, int NV>
 struct NarrowRow {
     static constexpr int VE = 16 / static_cast<int>(sizeof(T));
-    static constexpr int N = kNarrowVecs;
+    static constexpr int N = NV;
     float x[N * VE];  // columns past the end are -inf
     __device__ __forceinline__ static int col(int l, int k) {
         return ((k / VE) * TEAM + l) * VE + k % VE;
@@ -216,9 +215,9 @@ struct NarrowRow {
     }
 };
 
-template <typename T, int TEAM>
+template <typename T, int TEAM, int NV>
 __global__ __launch_bounds__(kThreads) void narrow_fwd_kernel(LogprobParams p) {
-    using Row = NarrowRow<T, TEAM>;
+    using Row = NarrowRow<T, TEAM, NV>;
     const int l = threadIdx.x % TEAM;
     const float k2 = p.scale * kLog2e;
     constexpr int kTeams = kThreads / TEAM;
@@ -277,9 +276,9 @@ struct RowGrad {
     }
 };
 
-template <typename T, int TEAM>
+template <typename T, int TEAM, int NV>
 __global__ __launch_bounds__(kThreads) void narrow_bwd_kernel(LogprobParams p) {
-    using Row = NarrowRow<T, TEAM>;
+    using Row = NarrowRow<T, TEAM, NV>;
     constexpr int VE = Row::VE;
     constexpr int kTeams = kThreads / TEAM;
     const int l = threadIdx.x % TEAM;
@@ -320,13 +319,45 @@ __global__ __launch_bounds__(kThreads) void narrow_bwd_kernel(LogprobParams p) {
 
 constexpr int kUnroll = 4;
 
-// Calls each(x values of a vector, first column, count) for the vectors of columns [c0, c1) that
-// are this thread's, kUnroll of them loaded at once.
+// Columns before c0 of the line of 128 bytes that c0 lies in: the vectors start with it, since a
+// wavefront's vectors across the lines of an odd row take one line more each (16384 rows of 50257
+// in bf16: 352 us forward, 286 with this).
+template <typename T>
+__device__ __forceinline__ int before_line(const T* row, int c0) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(row + c0) & 127) / sizeof(T));
+}
+
+// The values of a vector's columns in [c0, c1), -inf in place of others.
+template <typename T, int VE>
+__device__ __forceinline__ RawVec<T, VE> ld_between(const T* row, int c, int c0, int c1) {
+    if (c >= c0 && c + VE <= c1) return ld_raw<T, VE>(row + MSEL_SPAN(c, VE, c1));
+    float v[VE];
+#pragma unroll
+    for (int k = 0; k < VE; ++k)
+        v[k] = c + k >= c0 && c + k < c1 ? Elem<T>::load1(row + c + k) : -INFINITY;
+    return from_f32<T, VE>(v);
+}
+
+// Calls each(x values of some vectors, first column, columns from a vector to the next, number of
+// vectors) for the vectors of columns [c0, c1) that are this thread's, kUnroll of them loaded at
+// once.  Columns outside are -inf.
 template <typename T, typename Fn>
 __device__ __forceinline__ void each_vector(const T* row, int c0, int c1, Fn each) {
     constexpr int VE = 16 / static_cast<int>(sizeof(T));
     constexpr int kRound = kThreads * VE;
-    int c = c0 + static_cast<int>(threadIdx.x) * VE;
+    int c = c0 - before_line(row, c0) + static_cast<int>(threadIdx.x) * VE;
+    const auto one = [&] {
+        float v[VE];
+        to_f32<T, VE>(ld_between<T, VE>(row, c, c0, c1), v);
+        each(v, c, kRound, std::integral_constant<int, 1>());
+        c += kRound;
+    };
+    if (c < c0) {
+        if (c + VE > c0)
+            one();
+        else
+            c += kRound;
+    }
     for (; c + (kUnroll - 1) * kRound + VE <= c1; c += kUnroll * kRound) {
         RawVec<T, VE> raw[kUnroll];
 #pragma unroll
@@ -342,18 +373,27 @@ __device__ __forceinline__ void each_vector(const T* row, int c0, int c1, Fn eac
         }
         each(v, c, kRound, std::integral_constant<int, kUnroll>());
     }
-    for (; c < c1; c += kRound) {
-        float v[VE];
+    while (c < c1) one();
+}
+
+// The terms of some values added to sums that may have to be moved for them.
+template <bool ENTROPY, typename V>
+__device__ __forceinline__ void add_vector(Sums& t, const V& v, float k2) {
+    constexpr int n = sizeof(v) / sizeof(v[0]);
+    float m = v[0];
 #pragma unroll
-        for (int k = 0; k < VE; ++k) v[k] = -INFINITY;
-        if (c + VE <= c1) {
-            to_f32<T, VE>(ld_raw<T, VE>(row + MSEL_SPAN(c, VE, c1)), v);
-        } else {
+    for (int k = 1; k < n; ++k) m = fmaxf(m, v[k]);
+    if (m > t.max) {
+        rebase(t, fmaxf(m, kLowest), k2);
+        t.max = m;
+    }
+    const float at = t.m();
 #pragma unroll
-            for (int k = 0; k < VE; ++k)
-                if (c + k < c1) v[k] = Elem<T>::load1(row + c + k);
-        }
-        each(v, c, kRound, std::integral_constant<int, 1>());
+    for (int k = 0; k < n; ++k) {
+        if constexpr (ENTROPY)
+            add_term(v[k], at, k2, t.s, t.w);
+        else
+            t.s += exp2_hw((v[k] - at) * k2);
     }
 }
 
@@ -361,24 +401,7 @@ __device__ __forceinline__ void each_vector(const T* row, int c0, int c1, Fn eac
 template <typename T, bool ENTROPY>
 __device__ __forceinline__ Sums thread_sums(const T* row, int c0, int c1, float k2) {
     Sums t{-INFINITY, 0.0f, 0.0f};
-    each_vector<T>(row, c0, c1, [&](const auto& v, int, int, auto) {
-        constexpr int n = sizeof(v) / sizeof(v[0]);
-        float m = v[0];
-#pragma unroll
-        for (int k = 1; k < n; ++k) m = fmaxf(m, v[k]);
-        if (m > t.max) {
-            rebase(t, fmaxf(m, kLowest), k2);
-            t.max = m;
-        }
-        const float at = t.m();
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-            if constexpr (ENTROPY)
-                add_term(v[k], at, k2, t.s, t.w);
-            else
-                t.s += exp2_hw((v[k] - at) * k2);
-        }
-    });
+    each_vector<T>(row, c0, c1, [&](const auto& v, int, int, auto) { add_vector<ENTROPY>(t, v, k2); });
     return t;
 }
 
@@ -412,10 +435,10 @@ struct TopList {
     int count;
 };
 
-// The `top` largest keys of columns [c0, c1), handed to put(rank, key); c1 - c0 >= top.  mx: the
-// largest value among this thread's columns.
-template <typename T, typename Put>
-__device__ __forceinline__ void block_top(const T* row, int c0, int c1, int top, float mx,
+// The `top` largest keys of columns [c0, c1), handed to put(rank, key); c1 - c0 >= top.  each: calls
+// its argument for this thread's vectors, as each_vector does.  mx: the largest value among them.
+template <int VE, typename Each, typename Put>
+__device__ __forceinline__ void block_top(Each each, int c0, int c1, int top, float mx,
                                           TopList& list, Put put) {
     const int wave = threadIdx.x >> 6;
     const float kth = kth_of_lanes(mx, top);
@@ -425,8 +448,7 @@ __device__ __forceinline__ void block_top(const T* row, int c0, int c1, int top,
     float bound = list.bound[0];
 #pragma unroll
     for (int i = 1; i < kThreads / 64; ++i) bound = fmaxf(bound, list.bound[i]);
-    each_vector<T>(row, c0, c1, [&](const auto& v, int c, int round, auto) {
-        constexpr int VE = 16 / static_cast<int>(sizeof(T));
+    each([&](const auto& v, int c, int round, auto) {
         constexpr int n = sizeof(v) / sizeof(v[0]);
         bool any = false;
 #pragma unroll
@@ -435,7 +457,7 @@ __device__ __forceinline__ void block_top(const T* row, int c0, int c1, int top,
 #pragma unroll
         for (int k = 0; k < n; ++k) {
             const int col = c + (k / VE) * round + k % VE;
-            if (v[k] < bound || col >= c1) continue;
+            if (v[k] < bound || col < c0 || col >= c1) continue;
             const int at = atomicAdd(&list.count, 1);
             if (at < kCandidates) list.keys[MSEL_IDX(at, kCandidates)] = key_of(v[k], col);
         }
@@ -446,6 +468,7 @@ __device__ __forceinline__ void block_top(const T* row, int c0, int c1, int top,
         for (int i = threadIdx.x; i < n; i += kThreads) {
             const Key mine = list.keys[i];
             int rank = 0;
+#pragma unroll 8
             for (int j = 0; j < n; ++j) rank += list.keys[j] > mine;
             if (rank < top) put(rank, mine);
         }
@@ -454,14 +477,13 @@ __device__ __forceinline__ void block_top(const T* row, int c0, int c1, int top,
     Key below = ~Key(0);
     for (int k = 0; k < top; ++k) {
         Key best = 0;
-        each_vector<T>(row, c0, c1, [&](const auto& v, int c, int round, auto) {
-            constexpr int VE = 16 / static_cast<int>(sizeof(T));
+        each([&](const auto& v, int c, int round, auto) {
             constexpr int m = sizeof(v) / sizeof(v[0]);
 #pragma unroll
             for (int j = 0; j < m; ++j) {
                 const int col = c + (j / VE) * round + j % VE;
                 const Key q = key_of(v[j], col);
-                if (col < c1 && q < below && q > best) best = q;
+                if (col >= c0 && col < c1 && q < below && q > best) best = q;
             }
         });
         best = team_max_key<64>(best);
@@ -480,6 +502,31 @@ __host__ __device__ inline size_t sums_bytes(int64_t rows, int slices) {
     return (static_cast<size_t>(rows) * slices * sizeof(Sums) + 255) / 256 * 256;
 }
 
+// What a block has of a (row, slice): to the outputs, or to the slice's part of the workspace.
+template <typename T, bool TOP, typename Each>
+__device__ __forceinline__ void finish(const LogprobParams& p, const T* row, int64_t u, int64_t r,
+                                       int c0, int c1, float mx, const Sums& all, TopList* list,
+                                       Each each) {
+    constexpr int VE = 16 / static_cast<int>(sizeof(T));
+    [[maybe_unused]] const int64_t units = p.rows * p.slices;
+    if (p.slices > 1) {
+        if (threadIdx.x == 0) static_cast<Sums*>(p.ws)[MSEL_IDX(u, units)] = all;
+        if constexpr (TOP) {
+            Key* keys = reinterpret_cast<Key*>(static_cast<char*>(p.ws) +
+                                               sums_bytes(p.rows, p.slices));
+            block_top<VE>(each, c0, c1, p.top, mx, *list, [&](int rank, Key k) {
+                keys[MSEL_IDX(u * p.top + rank, units * p.top)] = k;
+            });
+        }
+    } else {
+        const RowOut o(all, p.scale);
+        if (threadIdx.x == 0) write_row<T>(p, row, r, o);
+        if constexpr (TOP)
+            block_top<VE>(each, c0, c1, p.top, mx, *list,
+                          [&](int rank, Key k) { write_top(p, r, rank, k, o); });
+    }
+}
+
 template <typename T, bool ENTROPY, bool TOP>
 __global__ __launch_bounds__(kThreads) void wide_fwd_kernel(LogprobParams p) {
     __shared__ Sums part[kThreads / 64];
@@ -493,27 +540,58 @@ __global__ __launch_bounds__(kThreads) void wide_fwd_kernel(LogprobParams p) {
         const int c0 = q * p.slice, c1 = min(p.V, c0 + p.slice);
         const Sums mine = thread_sums<T, ENTROPY>(row, c0, c1, k2);
         const Sums all = block_join(mine, k2, part);
-        if (p.slices > 1) {
-            if (threadIdx.x == 0) static_cast<Sums*>(p.ws)[MSEL_IDX(u, units)] = all;
-            if constexpr (TOP) {
-                Key* keys = reinterpret_cast<Key*>(static_cast<char*>(p.ws) +
-                                                   sums_bytes(p.rows, p.slices));
-                block_top<T>(row, c0, c1, p.top, mine.max, list, [&](int rank, Key k) {
-                    keys[MSEL_IDX(u * p.top + rank, units * p.top)] = k;
-                });
-            }
-        } else {
-            const RowOut o(all, p.scale);
-            if (threadIdx.x == 0) write_row<T>(p, row, r, o);
-            if constexpr (TOP)
-                block_top<T>(row, c0, c1, p.top, mine.max, list,
-                             [&](int rank, Key k) { write_top(p, r, rank, k, o); });
-        }
+        finish<T, TOP>(p, row, u, r, c0, c1, mine.max, all, reinterpret_cast<TopList*>(&list),
+                       [&](auto fn) { each_vector<T>(row, c0, c1, fn); });
         __syncthreads();  // the list is the next row's too
     }
 }
 
-// The slices of a row joined, a wavefront per row (four per block).  Up to kCandidates keys.
+// Slices of up to kHeld columns stay in registers: loaded at once, and read once (64 rows of 50257
+// in fp32 with 20 likeliest tokens: 17 us in two readings).
+constexpr int kHeldCols = 8192, kHeld = kHeldCols - 64;  // 64: what may lie before a line of fp32, bf16
+
+template <typename T, bool TOP>
+__global__ __launch_bounds__(kThreads) void held_fwd_kernel(LogprobParams p) {
+    constexpr int VE = 16 / static_cast<int>(sizeof(T));
+    constexpr int kRound = kThreads * VE, N = kHeldCols / kRound;
+    __shared__ Sums part[kThreads / 64];
+    __shared__ typename std::conditional<TOP, TopList, char>::type list;
+    const float k2 = p.scale * kLog2e;
+    const int64_t units = p.rows * p.slices;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t r = p.slices == 1 ? u : u / p.slices;
+        const int q = static_cast<int>(u - r * p.slices);
+        const T* row = static_cast<const T*>(p.logits) + MSEL_IDX(r, p.rows) * p.stride;
+        const int c0 = q * p.slice, c1 = min(p.V, c0 + p.slice);
+        const int c = c0 - before_line(row, c0) + static_cast<int>(threadIdx.x) * VE;
+        RawVec<T, VE> raw[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) raw[i] = ld_between<T, VE>(row, c + i * kRound, c0, c1);
+        const auto each = [&](auto fn) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float v[VE];
+                to_f32<T, VE>(raw[i], v);
+                if (c + i * kRound < c1) fn(v, c + i * kRound, kRound, std::integral_constant<int, 1>());
+            }
+        };
+        Sums mine{-INFINITY, 0.0f, 0.0f};
+        each([&](const auto& v, int, int, auto) {
+#pragma unroll
+            for (int k = 0; k < VE; ++k) mine.max = fmaxf(mine.max, v[k]);
+        });
+        const float at = mine.m();
+        each([&](const auto& v, int, int, auto) {
+#pragma unroll
+            for (int k = 0; k < VE; ++k) add_term(v[k], at, k2, mine.s, mine.w);
+        });
+        const Sums all = block_join(mine, k2, part);
+        finish<T, TOP>(p, row, u, r, c0, c1, mine.max, all, reinterpret_cast<TopList*>(&list), each);
+        __syncthreads();
+    }
+}
+
+// The slices of a row joined, a block per row.  Up to kCandidates keys.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void join_kernel(LogprobParams p) {
     const float k2 = p.scale * kLog2e;
@@ -523,19 +601,26 @@ __global__ __launch_bounds__(kThreads) void join_kernel(LogprobParams p) {
     __shared__ Key held[kCandidates];
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const int n = p.slices * p.top;
-        for (int i = threadIdx.x; i < n; i += kThreads)
-            held[MSEL_IDX(i, kCandidates)] = keys[MSEL_IDX(r * n + i, p.rows * n)];
         Sums t{-INFINITY, 0.0f, 0.0f};
         if (lane_id() < p.slices) t = parts[MSEL_IDX(r * p.slices + lane_id(), p.rows * p.slices)];
+        Key mine[kCandidates / kThreads];
+#pragma unroll
+        for (int i = 0; i < kCandidates / kThreads; ++i) {
+            const int at = i * kThreads + static_cast<int>(threadIdx.x);
+            mine[i] = at < n ? keys[MSEL_IDX(r * n + at, p.rows * n)] : Key(0);
+            held[at] = mine[i];
+        }
         const RowOut o(wave_join(t, k2), p.scale);
-        if (threadIdx.x == 0)
+        if (threadIdx.x == kThreads - 1)
             write_row<T>(p, static_cast<const T*>(p.logits) + MSEL_IDX(r, p.rows) * p.stride, r, o);
         __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const Key mine = held[i];
+#pragma unroll
+        for (int i = 0; i < kCandidates / kThreads; ++i) {
+            if (i * kThreads + static_cast<int>(threadIdx.x) >= n) break;
             int rank = 0;
-            for (int j = 0; j < n; ++j) rank += held[j] > mine;
-            if (rank < p.top) write_top(p, r, rank, mine, o);
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) rank += held[j] > mine[i];
+            if (rank < p.top) write_top(p, r, rank, mine[i], o);
         }
         __syncthreads();
     }
@@ -574,11 +659,13 @@ __global__ __launch_bounds__(kThreads) void wide_bwd_kernel(LogprobParams p) {
 #pragma unroll
                     for (int k = 0; k < VE; ++k) d[k] = 0.0f;
                 }
-                const RawVec<T, VE> w = from_f32<T, VE>(d);
-                if (col + VE <= c1)
-                    st_raw<T, VE, PAST>(out + MSEL_SPAN(col, VE, c1), w);
-                else
-                    st_part<T, VE>(out + col, w, c1 - col);
+                if (col >= c0 && col + VE <= c1) {
+                    st_raw<T, VE, PAST>(out + MSEL_SPAN(col, VE, c1), from_f32<T, VE>(d));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < VE; ++k)
+                        if (col + k >= c0 && col + k < c1) Elem<T>::store1(out + col + k, d[k]);
+                }
             }
         });
     }
@@ -586,19 +673,24 @@ __global__ __launch_bounds__(kThreads) void wide_bwd_kernel(LogprobParams p) {
 
 // ---- plans ---------------------------------------------------------------------------------------
 
-int team_of(int V, bool bf16) {
+// Lanes and vectors per lane of a narrow row (0 lanes: a wide one).
+struct Narrow {
+    int team, vecs;
+};
+Narrow narrow_of(int V, bool bf16) {
     const int ve = bf16 ? 8 : 4;
-    for (int team : {4, 16, 64})
-        if (V <= team * ve * kNarrowVecs) return team;
-    return 0;
+    for (const Narrow n : {Narrow{4, 1}, Narrow{4, 2}, Narrow{4, 4}, Narrow{16, 2}, Narrow{16, 4},
+                           Narrow{64, 2}, Narrow{64, 4}})
+        if (V <= n.team * n.vecs * ve) return n;
+    return {0, 0};
 }
 
 // Slices of a row: enough blocks for the chip, of about 4096 columns at least, no more than a
-// wavefront joins and than the joined keys' list holds.  With likeliest tokens the last slice has
-// V / n - 64 (n - 1) > 1700 columns or more for up to n = 16, so more than kMaxTop.
+// wavefront joins and than the joined keys' list holds.  The last slice has V / n - 64 (n - 1)
+// columns or more, which for up to n = 48 is above 1000, so more than kMaxTop.
 void slice_rows(int64_t rows, int V, int top, int64_t blocks, int& slices, int& slice) {
     int64_t n = std::min<int64_t>((blocks + rows - 1) / rows, (V + 4095) / 4096);
-    n = std::min<int64_t>(n, top > 0 ? kCandidates / kMaxTop : 64);
+    n = std::min<int64_t>(n, top > 0 ? std::min(48, kCandidates / top) : 64);
     slice = static_cast<int>((V + n - 1) / n);
     slice = (slice + 63) / 64 * 64;
     slices = (V + slice - 1) / slice;
@@ -609,26 +701,47 @@ dim3 grid_for(int64_t units) {
     return dim3(static_cast<unsigned>(std::min<int64_t>(units, kMaxBlocks)));
 }
 
+template <typename T, int TEAM, int NV>
+void launch_narrow(const LogprobParams& p, bool bwd, hipStream_t stream) {
+    const dim3 grid = grid_for((p.rows + kThreads / TEAM - 1) / (kThreads / TEAM));
+    if (bwd)
+        hipLaunchKernelGGL((narrow_bwd_kernel<T, TEAM, NV>), grid, dim3(kThreads), 0, stream, p);
+    else
+        hipLaunchKernelGGL((narrow_fwd_kernel<T, TEAM, NV>), grid, dim3(kThreads), 0, stream, p);
+}
+
+template <typename T>
+hipError_t launch_narrow(const LogprobParams& p, const Narrow& n, bool bwd, hipStream_t stream) {
+    if (n.team == 4 && n.vecs == 1)
+        launch_narrow<T, 4, 1>(p, bwd, stream);
+    else if (n.team == 4 && n.vecs == 2)
+        launch_narrow<T, 4, 2>(p, bwd, stream);
+    else if (n.team == 4)
+        launch_narrow<T, 4, 4>(p, bwd, stream);
+    else if (n.team == 16 && n.vecs == 2)
+        launch_narrow<T, 16, 2>(p, bwd, stream);
+    else if (n.team == 16)
+        launch_narrow<T, 16, 4>(p, bwd, stream);
+    else if (n.vecs == 2)
+        launch_narrow<T, 64, 2>(p, bwd, stream);
+    else
+        launch_narrow<T, 64, 4>(p, bwd, stream);
+    return hipGetLastError();
+}
+
 template <typename T>
 hipError_t forward(LogprobParams p, hipStream_t stream) {
     const dim3 block(kThreads);
-    const int team = team_of(p.V, sizeof(T) == 2);
-    if (team != 0) {
-        const dim3 grid = grid_for((p.rows + kThreads / team - 1) / (kThreads / team));
-        if (team == 4)
-            hipLaunchKernelGGL((narrow_fwd_kernel<T, 4>), grid, block, 0, stream, p);
-        else if (team == 16)
-            hipLaunchKernelGGL((narrow_fwd_kernel<T, 16>), grid, block, 0, stream, p);
-        else
-            hipLaunchKernelGGL((narrow_fwd_kernel<T, 64>), grid, block, 0, stream, p);
-        return hipGetLastError();
-    }
+    const Narrow narrow = narrow_of(p.V, sizeof(T) == 2);
+    if (narrow.team != 0) return launch_narrow<T>(p, narrow, false, stream);
     slice_rows(p.rows, p.V, p.top, kFwdBlocks, p.slices, p.slice);
     const dim3 grid = grid_for(p.rows * p.slices);
-    if (p.top > 0 && p.entropy != nullptr)
-        hipLaunchKernelGGL((wide_fwd_kernel<T, true, true>), grid, block, 0, stream, p);
+    if (p.slice <= kHeld && p.top > 0)
+        hipLaunchKernelGGL((held_fwd_kernel<T, true>), grid, block, 0, stream, p);
+    else if (p.slice <= kHeld)
+        hipLaunchKernelGGL((held_fwd_kernel<T, false>), grid, block, 0, stream, p);
     else if (p.top > 0)
-        hipLaunchKernelGGL((wide_fwd_kernel<T, false, true>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((wide_fwd_kernel<T, true, true>), grid, block, 0, stream, p);
     else if (p.entropy != nullptr)
         hipLaunchKernelGGL((wide_fwd_kernel<T, true, false>), grid, block, 0, stream, p);
     else
@@ -641,17 +754,8 @@ hipError_t forward(LogprobParams p, hipStream_t stream) {
 template <typename T>
 hipError_t backward(LogprobParams p, hipStream_t stream) {
     const dim3 block(kThreads);
-    const int team = team_of(p.V, sizeof(T) == 2);
-    if (team != 0) {
-        const dim3 grid = grid_for((p.rows + kThreads / team - 1) / (kThreads / team));
-        if (team == 4)
-            hipLaunchKernelGGL((narrow_bwd_kernel<T, 4>), grid, block, 0, stream, p);
-        else if (team == 16)
-            hipLaunchKernelGGL((narrow_bwd_kernel<T, 16>), grid, block, 0, stream, p);
-        else
-            hipLaunchKernelGGL((narrow_bwd_kernel<T, 64>), grid, block, 0, stream, p);
-        return hipGetLastError();
-    }
+    const Narrow narrow = narrow_of(p.V, sizeof(T) == 2);
+    if (narrow.team != 0) return launch_narrow<T>(p, narrow, true, stream);
     p.slices = 1;
     p.slice = p.V;
     if (p.dlogits != p.logits) slice_rows(p.rows, p.V, 0, kBwdBlocks, p.slices, p.slice);
@@ -666,7 +770,7 @@ hipError_t backward(LogprobParams p, hipStream_t stream) {
 }  // namespace
 
 size_t logprob_workspace_bytes(int64_t rows, int V, int top, bool bf16) {
-    if (team_of(V, bf16) != 0) return 0;
+    if (narrow_of(V, bf16).team != 0) return 0;
     int slices = 1, slice = 0;
     slice_rows(rows, V, top, kFwdBlocks, slices, slice);
     if (slices == 1) return 0;

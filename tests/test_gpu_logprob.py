@@ -179,8 +179,10 @@ def test_large_logits(vocab):
 @pytest.mark.parametrize("vocab,width,start", [(50, 64, 0), (1000, 1030, 3), (5000, 5004, 1)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_strided_rows(vocab, width, start, dtype):
-    """The first columns of a padded vocabulary: as the copied rows, and nothing is written
-    beside them."""
+    """The first columns of a padded vocabulary, and nothing is written beside them.  A row's vectors
+    start with its line of memory, so rows at other addresses are summed in another order: both are
+    within the bounds of the sums, which hold for any order.  The ids, and the gradient for the same
+    sums, are equal."""
     log(f"logprob strided {vocab} {dtype}")
     wide = normal((2, 5, width), dtype, 1, 3.0)
     x = wide[..., start:start + vocab]
@@ -189,15 +191,16 @@ def test_strided_rows(vocab, width, start, dtype):
     c = x.contiguous()
     a = msel.msel_logprob_fwd(x, ids, top=4, want_entropy=True)
     b = msel.msel_logprob_fwd(c, ids, top=4, want_entropy=True)
-    for k in a:
-        assert torch.equal(a[k], b[k]), k
+    ref = block.logprob_fwd(values(c), ids.cpu().numpy(), 1.0, 4)
+    _check(a, ref, 4)
+    _check(b, ref, 4)
     assert a["top_ids"].shape == (2, 5, 4)
     ref = msel.msel_logprob_bwd(c, ids, b["lse"], dlp)
-    d = msel.msel_logprob_bwd(x, ids, a["lse"], dlp)
+    d = msel.msel_logprob_bwd(x, ids, b["lse"], dlp)
     assert d.is_contiguous() and torch.equal(d, ref)
     keep = wide.clone()
     at = keep[..., start:start + vocab]
-    msel.msel_logprob_bwd(at, ids, a["lse"], dlp, dlogits=at)
+    msel.msel_logprob_bwd(at, ids, b["lse"], dlp, dlogits=at)
     assert torch.equal(at, ref)
     at.copy_(x)
     assert torch.equal(keep, wide)
