@@ -10,9 +10,9 @@
 // HBM bounds it: one read forward, one read and one write backward, against about 12 and 14 VALU
 // slots per element, 4 of them the exp.
 //
-// The likeliest tokens, by value and then by index: the k-th largest of a wavefront's lane maxima
-// is a bound that at least k elements of the row reach, so the row's second reading (from the
-// caches) keeps only the elements at or above the largest such bound, some 4 k of them, and each
+// The likeliest tokens, by value and then by index: about the k-th largest of a wavefront's lane
+// maxima is a bound that at least k elements of the row reach, so the row's second reading (from the
+// caches, or registers) keeps only the elements at or above the largest such bound, some 4 k of them, and each
 // kept element's rank is counted.  Rows with more ties than the list holds are searched once per
 // token.
 #include <hip/hip_runtime.h>
@@ -417,15 +417,17 @@ __device__ __forceinline__ Sums block_join(const Sums& mine, float k2, Sums* par
     return t;
 }
 
-// The k-th largest of the wavefront's lane values.
+// A value that at least k lanes of the wavefront reach: the k-th largest, cut to its sign, exponent
+// and 7 bits (below -inf, where that is the k-th largest, it is a NaN that every value passes).
 __device__ __forceinline__ float kth_of_lanes(float v, int k) {
-    int rank = 0;
-    for (int i = 0; i < 64; ++i) {
-        const float o = readlane(v, i);
-        rank += o > v || (o == v && i < lane_id());
+    const uint32_t u = static_cast<uint32_t>(key_of(v, 0) >> 32);
+    uint32_t t = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t c = t | (1u << bit);
+        if (__popcll(__ballot(u >= c)) >= k) t = c;
     }
-    const unsigned long long at = __ballot(rank == k - 1);
-    return readlane(v, at == 0 ? 63 : __ffsll(static_cast<unsigned long long>(at)) - 1);
+    return __uint_as_float(t ^ (t >> 31 ? 0x80000000u : 0xffffffffu));
 }
 
 struct TopList {

@@ -37,19 +37,24 @@ struct Gates {
     float m2;  // 1 - a^2
 };
 
-// 1 - a^2 = 1 - e^-q, q = -2 lam r: near q = 0 the difference would cancel, so up to 0.4 it is the
-// series q (1 - q/2 (1 - q/3 (...))), whose first missing term is q^8 / 9! < 2e-9 of it.
-__device__ __forceinline__ Gates gates_of(float ga, float gx, float lam) {
+// lam2: lam log2 e, so that a = 2^l, l = lam2 r.  1 - a^2 = 1 - e^-q, q = -2 ln 2 l: near q = 0 the
+// difference would cancel, so up to q = 0.3 it is the series q - q^2 / 2! + ... - q^6 / 6! in powers
+// of l, whose first missing term is q^6 / 7! < 1.5e-7 of it; from there on the difference loses at
+// most 2 bits.
+__device__ __forceinline__ Gates gates_of(float ga, float gx, float lam2) {
     Gates s;
     s.r = sigmoid_f(ga);
     s.i = sigmoid_f(gx);
-    const float la = lam * s.r;
-    s.a = exp2_hw(la * kLog2e);
-    const float q = -2.0f * la;
-    float p = fmaf(q, -1.0f / 8.0f, 1.0f);
-#pragma unroll
-    for (int k = 7; k >= 2; --k) p = fmaf(q * p, -1.0f / static_cast<float>(k), 1.0f);
-    s.m2 = q < 0.4f ? q * p : fmaf(-s.a, s.a, 1.0f);
+    const float l = lam2 * s.r;
+    s.a = exp2_hw(l);
+    constexpr float c = -2.0f * kLn2;  // q = c l
+    float p = -c * c * c * c * c * c / 720.0f;
+    p = fmaf(p, l, c * c * c * c * c / 120.0f);
+    p = fmaf(p, l, -c * c * c * c / 24.0f);
+    p = fmaf(p, l, c * c * c / 6.0f);
+    p = fmaf(p, l, -c * c / 2.0f);
+    p = fmaf(p, l, c);
+    s.m2 = l > 0.3f / c ? p * l : fmaf(-s.a, s.a, 1.0f);
     return s;
 }
 
@@ -59,11 +64,11 @@ __device__ __forceinline__ RawVec<T, kStep> ld_row(const T* row, int t0, int L) 
     return ld_part<T, kStep>(row + t0, L - t0);
 }
 
-template <typename T>
+template <typename T, bool PAST>
 __device__ __forceinline__ void st_row(T* row, int t0, int L, const float (&v)[kStep]) {
     const RawVec<T, kStep> r = from_f32<T, kStep>(v);
     if (t0 + kStep <= L)
-        st_raw<T, kStep>(row + MSEL_SPAN(t0, kStep, L), r);
+        st_raw<T, kStep, PAST>(row + MSEL_SPAN(t0, kStep, L), r);
     else if (t0 < L)
         st_part<T, kStep>(row + t0, r, L - t0);
 }
@@ -157,20 +162,28 @@ __device__ __forceinline__ float enter_backward(float P, float S, float& e) {
     }
 }
 
-// a_t and the input's share b_t of kStep steps from t0; steps past the end are the identity.
+// a_t and the input's share b_t of kStep steps, the first `valid` of them real and the others the
+// identity; whole: all of them are (uniform).
 template <typename T>
 __device__ __forceinline__ void steps_of(const RawVec<T, kStep>& rx, const RawVec<T, kStep>& ra,
-                                         const RawVec<T, kStep>& ri, float lam, int valid,
-                                         float (&a)[kStep], float (&b)[kStep]) {
+                                         const RawVec<T, kStep>& ri, float lam2, bool whole,
+                                         int valid, float (&a)[kStep], float (&b)[kStep]) {
     float x[kStep], ga[kStep], gx[kStep];
     to_f32<T, kStep>(rx, x);
     to_f32<T, kStep>(ra, ga);
     to_f32<T, kStep>(ri, gx);
 #pragma unroll
     for (int k = 0; k < kStep; ++k) {
-        const Gates s = gates_of(ga[k], gx[k], lam);
-        a[k] = k < valid ? s.a : 1.0f;
-        b[k] = k < valid ? __builtin_amdgcn_sqrtf(s.m2) * s.i * x[k] : 0.0f;
+        const Gates s = gates_of(ga[k], gx[k], lam2);
+        a[k] = s.a;
+        b[k] = __builtin_amdgcn_sqrtf(s.m2) * s.i * x[k];
+    }
+    if (!whole) {
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+            a[k] = k < valid ? a[k] : 1.0f;
+            b[k] = k < valid ? b[k] : 0.0f;
+        }
     }
 }
 
@@ -194,7 +207,7 @@ __global__ __launch_bounds__(256) void lru_step_kernel(LruParams p) {
         const int64_t at = MSEL_IDX(row, rows);
         const Gates s = gates_of(Elem<T>::load1(static_cast<const T*>(p.ga) + at),
                                  Elem<T>::load1(static_cast<const T*>(p.gx) + at),
-                                 p.lam[MSEL_IDX(static_cast<int>(row % p.D), p.D)]);
+                                 p.lam[MSEL_IDX(static_cast<int>(row % p.D), p.D)] * kLog2e);
         const float h0 = p.h0 != nullptr ? p.h0[at] : 0.0f;
         const float x = Elem<T>::load1(static_cast<const T*>(p.x) + at);
         const float h = fmaf(s.a, h0, __builtin_amdgcn_sqrtf(s.m2) * s.i * x);
@@ -231,7 +244,7 @@ __global__ __launch_bounds__(256) void lru_summary_kernel(LruParams p) {
          u += static_cast<int64_t>(gridDim.x) * 4) {
         const int64_t row = u / p.nseg;
         const int seg = static_cast<int>(u - row * p.nseg);
-        const float lam = p.lam[MSEL_IDX(static_cast<int>(row % p.D), p.D)];
+        const float lam2 = p.lam[MSEL_IDX(static_cast<int>(row % p.D), p.D)] * kLog2e;
         const int64_t base = MSEL_IDX(row, rows) * p.L;
         const T* ga = static_cast<const T*>(p.ga) + base;
         const T* gx = static_cast<const T*>(p.gx) + base;
@@ -256,7 +269,7 @@ __global__ __launch_bounds__(256) void lru_summary_kernel(LruParams p) {
             float P, S;
             if constexpr (DIR > 0) {
                 float a[kStep], b[kStep];
-                steps_of<T>(rx, ra, ri, lam, p.L - t, a, b);
+                steps_of<T>(rx, ra, ri, lam2, t - l8 + kTile <= p.L, p.L - t, a, b);
                 compose(a, b, P, S);
                 scan_fwd_fused(P, S);
                 P = readlane(P, 63);
@@ -269,7 +282,7 @@ __global__ __launch_bounds__(256) void lru_summary_kernel(LruParams p) {
                 S = 0.0f;
 #pragma unroll
                 for (int j = kStep - 1; j >= 0; --j) {
-                    const float a = j < p.L - t ? exp2_hw(lam * kLog2e * sigmoid_f(g[j])) : 1.0f;
+                    const float a = j < p.L - t ? exp2_hw(lam2 * sigmoid_f(g[j])) : 1.0f;
                     P *= a;
                     S = a * (d[j] + S);
                 }
@@ -291,14 +304,15 @@ __global__ __launch_bounds__(256) void lru_summary_kernel(LruParams p) {
     }
 }
 
-// The forward.  A team of 1, 16 or 64 lanes, or of four wavefronts (256), per row, or a wavefront
-// per segment of a row when there are several (their pairs known).  out may be null (states only).
-template <typename T, int TEAM>
-__global__ __launch_bounds__(256) void lru_fwd_kernel(LruParams p) {
-    constexpr bool kBlock = TEAM == 256;
+// The forward.  A team of 1, 16 or 64 lanes, or of several wavefronts, per row, or a wavefront per
+// segment of a row when there are several (their pairs known).  out may be null (states only).
+// PAST: out is stored past the caches.
+template <typename T, int TEAM, bool PAST>
+__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void lru_fwd_kernel(LruParams p) {
+    constexpr bool kBlock = TEAM > 64;
     constexpr int kLanes = kBlock ? 64 : TEAM;  // of one scan
-    constexpr int kTeams = 256 / TEAM;
-    __shared__ float2 total[2][4];
+    constexpr int kTeams = kBlock ? 1 : 256 / TEAM, kWaves = kBlock ? TEAM / 64 : 1;
+    __shared__ float2 total[2][kWaves];
     const int64_t rows = static_cast<int64_t>(p.B) * p.D;
     const int nseg = TEAM == 64 ? p.nseg : 1;
     const int64_t units = rows * nseg;
@@ -315,7 +329,7 @@ __global__ __launch_bounds__(256) void lru_fwd_kernel(LruParams p) {
         const int64_t u = live ? mine : units - 1;  // lanes without a row repeat the last one
         const int64_t row = nseg == 1 ? u : u / nseg;
         const int seg = static_cast<int>(u - row * nseg);
-        const float lam = p.lam[MSEL_IDX(static_cast<int>(row % p.D), p.D)];
+        const float lam2 = p.lam[MSEL_IDX(static_cast<int>(row % p.D), p.D)] * kLog2e;
         const int64_t base = MSEL_IDX(row, rows) * p.L;
         const T* x = static_cast<const T*>(p.x) + base;
         const T* ga = static_cast<const T*>(p.ga) + base;
@@ -340,7 +354,7 @@ __global__ __launch_bounds__(256) void lru_fwd_kernel(LruParams p) {
                 ni = ld_row(gx, t + tile, p.L);
             }
             float a[kStep], b[kStep], P, S;
-            steps_of<T>(rx, ra, ri, lam, p.L - t, a, b);
+            steps_of<T>(rx, ra, ri, lam2, t0 + tile <= p.L, p.L - t, a, b);
             compose(a, b, P, S);
             float in, entered = h;  // what enters the wavefront
             if constexpr (kBlock) {
@@ -349,7 +363,7 @@ __global__ __launch_bounds__(256) void lru_fwd_kernel(LruParams p) {
                 __syncthreads();  // the other buffer is written before the next one
                 float before = h;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
+                for (int w = 0; w < kWaves; ++w) {
                     if (w == wave) before = h;
                     h = fmaf(total[turn][w].x, h, total[turn][w].y);
                 }
@@ -366,7 +380,7 @@ __global__ __launch_bounds__(256) void lru_fwd_kernel(LruParams p) {
                 float v[kStep];
 #pragma unroll
                 for (int k = 0; k < kStep; ++k) v[k] = in = fmaf(a[k], in, b[k]);
-                if (live) st_row(out, t, p.L, v);
+                if (live) st_row<T, PAST>(out, t, p.L, v);
             }
         }
         if (p.final_state != nullptr && t_hi == p.L && live && threadIdx.x % TEAM == 0)
@@ -376,13 +390,13 @@ __global__ __launch_bounds__(256) void lru_fwd_kernel(LruParams p) {
 }
 
 // The backward, teams as in the forward.  dlam's parts: one per row (and segment).
-template <typename T, int TEAM>
-__global__ __launch_bounds__(256) void lru_bwd_kernel(LruParams p) {
-    constexpr bool kBlock = TEAM == 256;
+template <typename T, int TEAM, bool PAST>
+__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void lru_bwd_kernel(LruParams p) {
+    constexpr bool kBlock = TEAM > 64;
     constexpr int kLanes = kBlock ? 64 : TEAM;
-    constexpr int kTeams = 256 / TEAM;
-    __shared__ float2 total[2][4];
-    __shared__ float sums[4];
+    constexpr int kTeams = kBlock ? 1 : 256 / TEAM, kWaves = kBlock ? TEAM / 64 : 1;
+    __shared__ float2 total[2][kWaves];
+    __shared__ float sums[kWaves];
     const int64_t rows = static_cast<int64_t>(p.B) * p.D;
     const int nseg = TEAM == 64 ? p.nseg : 1;
     const int64_t units = rows * nseg;
@@ -398,7 +412,7 @@ __global__ __launch_bounds__(256) void lru_bwd_kernel(LruParams p) {
         const int64_t row = nseg == 1 ? u : u / nseg;
         const int seg = static_cast<int>(u - row * nseg);
         const int d = static_cast<int>(row % p.D);
-        const float lam = p.lam[MSEL_IDX(d, p.D)];
+        const float lam = p.lam[MSEL_IDX(d, p.D)], lam2 = lam * kLog2e;
         const int64_t base = MSEL_IDX(row, rows) * p.L;
         const T* x = static_cast<const T*>(p.x) + base;
         const T* ga = static_cast<const T*>(p.ga) + base;
@@ -435,17 +449,25 @@ __global__ __launch_bounds__(256) void lru_bwd_kernel(LruParams p) {
             to_f32<T, kStep>(ra, va);
             to_f32<T, kStep>(ri, vi);
             to_f32<T, kStep>(rd, ds);
-            float a[kStep], rr[kStep], ii[kStep], m2[kStep], b[kStep];
+            float a[kStep], rr[kStep], ii[kStep], ms[kStep], b[kStep];
 #pragma unroll
             for (int k = 0; k < kStep; ++k) {
-                const Gates s = gates_of(va[k], vi[k], lam);
-                const bool valid = k < p.L - t;
-                a[k] = valid ? s.a : 1.0f;
+                const Gates s = gates_of(va[k], vi[k], lam2);
+                a[k] = s.a;
                 rr[k] = s.r;
                 ii[k] = s.i;
-                m2[k] = s.m2;
-                b[k] = valid ? __builtin_amdgcn_sqrtf(s.m2) * s.i * xs[k] : 0.0f;
-                ds[k] = valid ? ds[k] : 0.0f;
+                ms[k] = __builtin_amdgcn_sqrtf(s.m2);
+                b[k] = ms[k] * s.i * xs[k];
+            }
+            if (t0 + tile > p.L) {  // steps past the end: the identity, and nothing to dlam
+#pragma unroll
+                for (int k = 0; k < kStep; ++k) {
+                    const bool valid = k < p.L - t;
+                    a[k] = valid ? a[k] : 1.0f;
+                    b[k] = valid ? b[k] : 0.0f;
+                    ds[k] = valid ? ds[k] : 0.0f;
+                    rr[k] = valid ? rr[k] : 0.0f;
+                }
             }
             float P, S;
             compose(a, b, P, S);
@@ -464,7 +486,7 @@ __global__ __launch_bounds__(256) void lru_bwd_kernel(LruParams p) {
                 __syncthreads();
                 float behind = e;
 #pragma unroll
-                for (int w = 3; w >= 0; --w) {
+                for (int w = kWaves - 1; w >= 0; --w) {
                     if (w == wave) behind = e;
                     e = fmaf(total[turn][w].x, e, total[turn][w].y);
                 }
@@ -481,7 +503,7 @@ __global__ __launch_bounds__(256) void lru_bwd_kernel(LruParams p) {
             float dx[kStep], dga[kStep], dgx[kStep];
 #pragma unroll
             for (int k = 0; k < kStep; ++k) {
-                const float m = __builtin_amdgcn_sqrtf(m2[k]);
+                const float m = ms[k];
                 const float ix = ii[k] * xs[k];
                 // where m = 0 the square root has no slope: its part is 0
                 const float by_m = m > 0.0f ? ix * a[k] * a[k] * rcp_hw(m) : m;
@@ -492,12 +514,12 @@ __global__ __launch_bounds__(256) void lru_bwd_kernel(LruParams p) {
                 dgx[k] = gm * ix * (1.0f - ii[k]);
                 const float qr = q * rr[k];
                 dga[k] = qr * lam * (1.0f - rr[k]);
-                dlam += k < p.L - t ? qr : 0.0f;
+                dlam += t0 + tile <= p.L || k < p.L - t ? qr : 0.0f;
             }
             if (live) {
-                st_row(static_cast<T*>(p.dx) + base, t, p.L, dx);
-                st_row(static_cast<T*>(p.dga) + base, t, p.L, dga);
-                st_row(static_cast<T*>(p.dgx) + base, t, p.L, dgx);
+                st_row<T, PAST>(static_cast<T*>(p.dx) + base, t, p.L, dx);
+                st_row<T, PAST>(static_cast<T*>(p.dga) + base, t, p.L, dga);
+                st_row<T, PAST>(static_cast<T*>(p.dgx) + base, t, p.L, dgx);
             }
         }
         if (p.dh0 != nullptr && t_lo == 0 && live && threadIdx.x % TEAM == 0)
@@ -512,7 +534,9 @@ __global__ __launch_bounds__(256) void lru_bwd_kernel(LruParams p) {
             if constexpr (kBlock) {
                 if (lane_id() == 0) sums[wave] = dlam;
                 __syncthreads();
-                dlam = sums[0] + sums[1] + sums[2] + sums[3];
+                dlam = sums[0];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) dlam += sums[w];
             }
             if (live && threadIdx.x % TEAM == 0) {
                 const int64_t part = (row / p.D * nseg + seg) * p.D + d;
@@ -539,6 +563,8 @@ LruPlan lru_plan(int64_t rows, int L) {
         q.team = 64;
     } else if (rows >= 512) {
         q.team = 256;
+    } else if (rows >= 128) {
+        q.team = 1024;  // 512 in the backward
     } else {
         q.team = 64;
         const int64_t want = std::min<int64_t>(kMaxSegments, (4096 + rows - 1) / rows);
@@ -556,6 +582,26 @@ dim3 grid_for(int64_t units, int per_block) {
     return dim3(static_cast<unsigned>(std::min<int64_t>(blocks, kMaxBlocks)));
 }
 
+template <typename T, int TEAM>
+void launch_fwd(const LruParams& p, bool past, int64_t units, hipStream_t stream) {
+    constexpr int threads = TEAM > 256 ? TEAM : 256;
+    const dim3 grid = grid_for(units, threads / TEAM), block(threads);
+    if (past)
+        hipLaunchKernelGGL((lru_fwd_kernel<T, TEAM, true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((lru_fwd_kernel<T, TEAM, false>), grid, block, 0, stream, p);
+}
+
+template <typename T, int TEAM>
+void launch_bwd(const LruParams& p, bool past, int64_t units, hipStream_t stream) {
+    constexpr int threads = TEAM > 256 ? TEAM : 256;
+    const dim3 grid = grid_for(units, threads / TEAM), block(threads);
+    if (past)
+        hipLaunchKernelGGL((lru_bwd_kernel<T, TEAM, true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((lru_bwd_kernel<T, TEAM, false>), grid, block, 0, stream, p);
+}
+
 template <typename T>
 hipError_t forward(LruParams p, hipStream_t stream) {
     const int64_t rows = static_cast<int64_t>(p.B) * p.D;
@@ -566,15 +612,16 @@ hipError_t forward(LruParams p, hipStream_t stream) {
     const LruPlan q = lru_plan(rows, p.L);
     p.nseg = q.nseg;
     p.seg_tiles = q.seg_tiles;
-    const dim3 grid = grid_for(rows * q.nseg, 256 / q.team), block(256);
+    const int64_t units = rows * q.nseg;
     if (q.nseg > 1)
-        hipLaunchKernelGGL((lru_summary_kernel<T, 1>), grid_for(rows * q.nseg, 4), block, 0, stream,
-                           p);
+        hipLaunchKernelGGL((lru_summary_kernel<T, 1>), grid_for(units, 4), dim3(256), 0, stream, p);
+    const bool past = past_cache(rows * p.L * static_cast<int64_t>(sizeof(T)));
     switch (q.team) {
-        case 1: hipLaunchKernelGGL((lru_fwd_kernel<T, 1>), grid, block, 0, stream, p); break;
-        case 16: hipLaunchKernelGGL((lru_fwd_kernel<T, 16>), grid, block, 0, stream, p); break;
-        case 64: hipLaunchKernelGGL((lru_fwd_kernel<T, 64>), grid, block, 0, stream, p); break;
-        default: hipLaunchKernelGGL((lru_fwd_kernel<T, 256>), grid, block, 0, stream, p); break;
+        case 1: launch_fwd<T, 1>(p, past, units, stream); break;
+        case 16: launch_fwd<T, 16>(p, past, units, stream); break;
+        case 64: launch_fwd<T, 64>(p, past, units, stream); break;
+        case 256: launch_fwd<T, 256>(p, past, units, stream); break;
+        default: launch_fwd<T, 1024>(p, past, units, stream); break;
     }
     return hipGetLastError();
 }
@@ -585,15 +632,17 @@ hipError_t backward(LruParams p, hipStream_t stream) {
     const LruPlan q = lru_plan(rows, p.L);
     p.nseg = q.nseg;
     p.seg_tiles = q.seg_tiles;
-    const dim3 grid = grid_for(rows * q.nseg, 256 / q.team), block(256);
+    const int64_t units = rows * q.nseg;
     if (q.nseg > 1)
-        hipLaunchKernelGGL((lru_summary_kernel<T, -1>), grid_for(rows * q.nseg, 4), block, 0,
-                           stream, p);
+        hipLaunchKernelGGL((lru_summary_kernel<T, -1>), grid_for(units, 4), dim3(256), 0, stream,
+                           p);
+    const bool past = past_cache(3 * rows * p.L * static_cast<int64_t>(sizeof(T)));
     switch (q.team) {
-        case 1: hipLaunchKernelGGL((lru_bwd_kernel<T, 1>), grid, block, 0, stream, p); break;
-        case 16: hipLaunchKernelGGL((lru_bwd_kernel<T, 16>), grid, block, 0, stream, p); break;
-        case 64: hipLaunchKernelGGL((lru_bwd_kernel<T, 64>), grid, block, 0, stream, p); break;
-        default: hipLaunchKernelGGL((lru_bwd_kernel<T, 256>), grid, block, 0, stream, p); break;
+        case 1: launch_bwd<T, 1>(p, past, units, stream); break;
+        case 16: launch_bwd<T, 16>(p, past, units, stream); break;
+        case 64: launch_bwd<T, 64>(p, past, units, stream); break;
+        case 256: launch_bwd<T, 256>(p, past, units, stream); break;
+        default: launch_bwd<T, 512>(p, past, units, stream); break;
     }
     const hipError_t s = hipGetLastError();
     if (s != hipSuccess || p.dlam_part == nullptr) return s;
