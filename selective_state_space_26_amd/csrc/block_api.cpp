@@ -77,10 +77,6 @@ msel_status check_lru(const msel_lru_args* a) {
     return MSEL_OK;
 }
 
-msel::LruPlan plan_of(const msel_lru_args* a) {
-    return msel::lru_plan(static_cast<int64_t>(a->batch) * a->dim, a->seqlen);
-}
-
 // The parts of a workspace, in the order in which they lie.
 struct LruSpace {
     size_t pairs = 0, chunks = 0, dlam = 0;  // bytes
@@ -88,9 +84,10 @@ struct LruSpace {
 };
 
 LruSpace lru_space(const msel_lru_args* a, bool bwd) {
-    const msel::LruPlan q = plan_of(a);
     const size_t rows = static_cast<size_t>(a->batch) * static_cast<size_t>(a->dim);
+    const msel::LruPlan q = msel::lru_plan(static_cast<int64_t>(rows), a->seqlen, bwd);
     LruSpace w;
+    // both directions cut the same rows into the same segments
     if (q.nseg > 1) w.pairs = rows * static_cast<size_t>(q.nseg + 1) * sizeof(float2);
     if (!bwd) return w;
     // rows of up to a chunk start from h0

@@ -30,7 +30,7 @@ struct LruParams {
     void* dga;
     void* dgx;
     float* dh0;
-    float* dlam_part;    // [B * nseg, D], or null
+    float* dlam_part;    // [B * nseg, D], or null (dlam itself where that is one part)
     float* dlam;
     int nseg, seg_tiles; // set by the launchers
 };
@@ -38,7 +38,7 @@ struct LruParams {
 struct LruPlan {
     int team, tiles, nseg, seg_tiles;
 };
-LruPlan lru_plan(int64_t rows, int L);
+LruPlan lru_plan(int64_t rows, int L, bool bwd);
 hipError_t launch_lru_fwd(const LruParams& p, bool bf16, hipStream_t stream);
 hipError_t launch_lru_bwd(const LruParams& p, bool bf16, hipStream_t stream);
 

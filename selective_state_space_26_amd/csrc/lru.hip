@@ -549,22 +549,33 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void lru_bwd_kernel(LruPar
 
 }  // namespace
 
-// Teams: a lane for a row of up to 8 steps, 16 lanes up to 128, then wavefronts.
-LruPlan lru_plan(int64_t rows, int L) {
+// Teams: a lane for a row of up to 8 steps, 16 lanes up to 128, then wavefronts.  A wavefront a row
+// where there are rows enough; four, whose loads are one stretch of 4 KB, where many rows fill their
+// tiles of 2048 steps (12288 x 2048 bf16, forward and backward: 107 us, 110 with one) or where fewer
+// rows than that leave wavefronts wanting (1536 x 16384: 109, 130); sixteen (eight in the backward,
+// for its registers) for very long rows (5120 x 65536 forward: 481, 541 with one or four) and for few
+// (200 x 30011 fp32: 59, 63 with four, 78 in segments).  Below 128 rows those are cut into segments
+// that are composed first (64 x 65536: 44 us, 63 with sixteen).
+LruPlan lru_plan(int64_t rows, int L, bool bwd) {
     LruPlan q{};
     q.tiles = (L + kTile - 1) / kTile;
     q.seg_tiles = q.tiles;
     q.nseg = 1;
+    const int most = bwd ? 512 : 1024;
     if (L <= kStep) {
         q.team = 1;
     } else if (L <= 16 * kStep) {
         q.team = 16;
-    } else if (q.tiles == 1 || rows >= 4096) {
+    } else if (q.tiles == 1) {
         q.team = 64;
-    } else if (rows >= 512) {
-        q.team = 256;
+    } else if (rows >= 2048) {
+        const bool full = (L + 4 * kTile - 1) / (4 * kTile) * static_cast<int64_t>(4 * kTile) <=
+                          L + L / 20;
+        q.team = L >= 64 * kTile && (!bwd || rows >= 4096) ? most
+                 : rows >= 8192 && full                      ? 256
+                                                             : 64;
     } else if (rows >= 128) {
-        q.team = 1024;  // 512 in the backward
+        q.team = L >= 64 * kTile || (rows < 512 && L > 8 * kTile) ? most : 256;
     } else {
         q.team = 64;
         const int64_t want = std::min<int64_t>(kMaxSegments, (4096 + rows - 1) / rows);
@@ -609,7 +620,7 @@ hipError_t forward(LruParams p, hipStream_t stream) {
         hipLaunchKernelGGL(lru_step_kernel<T>, grid_for(rows, 256), dim3(256), 0, stream, p);
         return hipGetLastError();
     }
-    const LruPlan q = lru_plan(rows, p.L);
+    const LruPlan q = lru_plan(rows, p.L, false);
     p.nseg = q.nseg;
     p.seg_tiles = q.seg_tiles;
     const int64_t units = rows * q.nseg;
@@ -629,10 +640,12 @@ hipError_t forward(LruParams p, hipStream_t stream) {
 template <typename T>
 hipError_t backward(LruParams p, hipStream_t stream) {
     const int64_t rows = static_cast<int64_t>(p.B) * p.D;
-    const LruPlan q = lru_plan(rows, p.L);
+    const LruPlan q = lru_plan(rows, p.L, true);
     p.nseg = q.nseg;
     p.seg_tiles = q.seg_tiles;
     const int64_t units = rows * q.nseg;
+    const int64_t parts = static_cast<int64_t>(p.B) * q.nseg;
+    if (parts == 1) p.dlam_part = p.dlam;  // the one part is the sum
     if (q.nseg > 1)
         hipLaunchKernelGGL((lru_summary_kernel<T, -1>), grid_for(units, 4), dim3(256), 0, stream,
                            p);
@@ -645,8 +658,8 @@ hipError_t backward(LruParams p, hipStream_t stream) {
         default: launch_bwd<T, 512>(p, past, units, stream); break;
     }
     const hipError_t s = hipGetLastError();
-    if (s != hipSuccess || p.dlam_part == nullptr) return s;
-    return launch_column_sums(p.dlam_part, static_cast<int64_t>(p.B) * q.nseg, p.D, p.dlam, stream);
+    if (s != hipSuccess || p.dlam == nullptr || parts == 1) return s;
+    return launch_column_sums(p.dlam_part, parts, p.D, p.dlam, stream);
 }
 
 }  // namespace

@@ -11,6 +11,7 @@ Layouts, as in include/msel.h:
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -28,6 +29,14 @@ def _call(fn, dev, *args):
         with torch.cuda.device(dev):
             code = call(*args, _handle(dev))
     _lib.check(fn, code)
+
+
+@functools.lru_cache(maxsize=1024)
+def _need_bytes(fn, bsz, dim, L, code, chunks):
+    """Bytes of workspace for these sizes; chunks: the backward is given the chunk states."""
+    a = _lib.LruArgs(_lib.ABI_VERSION, bsz, dim, L, code, 0)
+    a.chunk_states = 4 if chunks else None
+    return getattr(_lib.load(), fn)(ctypes.byref(a))
 
 
 def _args(x, gate_a, gate_x, lam, h0):
@@ -73,7 +82,7 @@ def msel_lru_fwd(x, gate_a, gate_x, lam, h0=None, return_final_state=True,
     elif return_chunk_states:
         chunk_states = torch.empty((bsz, dim, num_chunks(L)), device=dev, dtype=torch.float32)
     a.out, a.final_state, a.chunk_states = out.data_ptr(), _at(final_state), _at(chunk_states)
-    need = _lib.load().msel_lru_fwd_workspace_bytes(ctypes.byref(a))
+    need = _need_bytes("msel_lru_fwd_workspace_bytes", bsz, dim, L, a.dtype, False)
     workspace, size = _workspace(workspace, need, dev)
     _call("msel_lru_fwd", dev, ctypes.byref(a), _at(workspace), size)
     return out, final_state, chunk_states
@@ -97,7 +106,8 @@ def msel_lru_bwd(x, gate_a, gate_x, lam, dout, h0=None, dfinal_state=None, chunk
     dh0 = torch.empty((bsz, dim), device=dev, dtype=torch.float32) if want_dh0 else None
     g = _lib.LruGrads(dout.data_ptr(), _at(dfinal_state), dx.data_ptr(), dga.data_ptr(),
                       dgx.data_ptr(), _at(dlam), _at(dh0))
-    need = _lib.load().msel_lru_bwd_workspace_bytes(ctypes.byref(a))
+    need = _need_bytes("msel_lru_bwd_workspace_bytes", bsz, dim, L, a.dtype,
+                       chunk_states is not None)
     workspace, size = _workspace(workspace, need, dev)
     _call("msel_lru_bwd", dev, ctypes.byref(a), ctypes.byref(g), _at(workspace), size)
     return {"dx": dx, "dgate_a": dga, "dgate_x": dgx, "dlam": dlam, "dh0": dh0}
