@@ -559,31 +559,32 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     }
 }
 
-// Few tokens: a block for 16 columns of both weights, whose rows go from memory into the MFMA's
-// registers, each read once for up to 16 NT tokens; its wavefronts take the chunks of k in turn
-// and their sums are added in LDS.  HBM bounds it: 8 tokens of 2048 -> 5632 read 46 MB.
+// Few tokens: a block for 8 columns of both weights, whose 16 rows go from memory into the MFMA's
+// registers, each read once for up to 16 NT tokens; its wavefronts take the chunks of k in turn and
+// their sums are added in LDS.  HBM bounds it: 8 tokens of 2048 -> 5632 read 46 MB.  (16 columns a
+// block, the weights in MFMAs of their own: 352 blocks for 256 CUs there, 12.9 us.)
 template <typename T, int NT>
 __global__ __launch_bounds__(256) void skinny_kernel(ProductParams p) {
-    constexpr int kWaves = 4;
+    constexpr int kWaves = 4, kCols = 8;
     constexpr int VE = 16 / static_cast<int>(sizeof(T));
     constexpr int kChunk = 8 * VE;  // of k per wavefront: two vectors a lane, 128 bytes of a row
-    constexpr int kAhead = 2;       // chunks on their way together
+    constexpr int kAhead = 4;       // chunks on their way together
     typedef float f32x4_t __attribute__((ext_vector_type(4)));
-    __shared__ f32x4_t sums[kWaves][NT][2][64];
+    __shared__ float sums[kWaves][NT][16][16];
     const int lane = lane_id(), wave = threadIdx.x >> 6;
-    const int n0 = static_cast<int>(xcd_order(blockIdx.x, gridDim.x)) * 16;
+    const int n0 = static_cast<int>(xcd_order(blockIdx.x, gridDim.x)) * kCols;
     const int K = static_cast<int>(p.K);
-    // rows past the end repeat the last one; their results are not stored
-    const int64_t n = MSEL_IDX(min(n0 + (lane & 15), p.N - 1), p.N);
-    const T* const g = static_cast<const T*>(p.b0) + n * p.ldb;
-    const T* const u = static_cast<const T*>(p.b1) + n * p.ldb;
+    // rows 0..7 of the MFMA are Wg's, 8..15 Wu's; rows past the end repeat the last one, and their
+    // results are not stored
+    const int64_t n = MSEL_IDX(min(n0 + (lane & 7), p.N - 1), p.N);
+    const T* const w = static_cast<const T*>((lane & 8) ? p.b1 : p.b0) + n * p.ldb;
     const T* x[NT];
-    f32x4_t acc[NT][2];
+    f32x4_t acc[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int64_t m = MSEL_IDX(min<int64_t>(t * 16 + (lane & 15), p.M - 1), p.M);
         x[t] = static_cast<const T*>(p.a) + m * p.lda;
-        acc[t][0] = acc[t][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
     const auto load = [&](const T* row, int k) {  // columns past the end are 0
         if (k + VE <= K) return ld_raw<T, VE>(row + MSEL_SPAN(k, VE, K));
@@ -603,14 +604,13 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductParams p) {
     // lane l: row l % 16, 2 vectors from 2 VE (l / 16) on of a chunk
     const int at = (lane >> 4) * 2 * VE;
     for (int k0 = wave * kChunk; k0 < K; k0 += kAhead * kWaves * kChunk) {
-        RawVec<T, VE> vg[kAhead][2], vu[kAhead][2], vx[kAhead][2][NT];
+        RawVec<T, VE> vw[kAhead][2], vx[kAhead][2][NT];
 #pragma unroll
         for (int c = 0; c < kAhead; ++c) {
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 const int k = k0 + c * kWaves * kChunk + at + v * VE;
-                vg[c][v] = load(g, k);
-                vu[c][v] = load(u, k);
+                vw[c][v] = load(w, k);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) vx[c][v][t] = load(x[t], k);
             }
@@ -620,35 +620,26 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductParams p) {
 #pragma unroll
             for (int v = 0; v < 2; ++v)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    product(vg[c][v], vx[c][v][t], acc[t][0]);
-                    product(vu[c][v], vx[c][v][t], acc[t][1]);
-                }
+                for (int t = 0; t < NT; ++t) product(vw[c][v], vx[c][v][t], acc[t]);
     }
+    // lane l holds token l % 16 and rows 4 (l / 16) + 0..3
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        sums[wave][t][0][lane] = acc[t][0];
-        sums[wave][t][1][lane] = acc[t][1];
-    }
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[wave][t][4 * (lane >> 4) + e][lane & 15] = acc[t][e];
     __syncthreads();
-    // lane l holds token l % 16 and 4 columns from 4 (l / 16) on
-    for (int t = wave; t < NT; t += kWaves) {
-        f32x4_t a = sums[0][t][0][lane], b = sums[0][t][1][lane];
+    for (int i = threadIdx.x; i < NT * 16 * kCols; i += 256) {
+        const int m = i / kCols, c = i % kCols;
+        float g = 0.0f, u = 0.0f;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) {
-            a += sums[w][t][0][lane];
-            b += sums[w][t][1][lane];
+        for (int v = 0; v < kWaves; ++v) {
+            g += sums[v][m >> 4][c][m & 15];
+            u += sums[v][m >> 4][8 + c][m & 15];
         }
-        const int64_t m = t * 16 + (lane & 15);
-        const int col = n0 + 4 * (lane >> 4);
-        if (m < p.M) {
+        if (m < p.M && n0 + c < p.N) {
             T* row = static_cast<T*>(p.c0) + m * p.ldc;
             with_act(p.gelu, [&](auto gelu) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (col + e < p.N)
-                        Elem<T>::store1(row + MSEL_IDX(col + e, p.N),
-                                        act_of<gelu.value>(a[e]) * b[e]);
+                Elem<T>::store1(row + MSEL_IDX(n0 + c, p.N), act_of<gelu.value>(g) * u);
             });
         }
     }
@@ -871,9 +862,9 @@ ProductParams gate_params(const MlpParams& p, const MlpSpace& w, const Padded& o
     return q;
 }
 
-// Tokens that the skinny kernel takes (2048 -> 5632 in bf16: 12 us for 1 token, 18 for 32, 26 for 64;
-// the tiles take 22 for each of them).
-constexpr int kSkinny = 48;
+// Tokens that the skinny kernel takes (2048 -> 5632 in bf16: 10 us for 1 token, 13 for 16, 18.5 for
+// 32, 24 for 48, and the tiles take 22 for each of them; in fp32 61 for 48, the tiles 79).
+constexpr int64_t skinny_tokens(bool bf16) { return bf16 ? 32 : 48; }
 
 template <typename T>
 hipError_t forward_skinny(const MlpParams& p, hipStream_t stream) {
@@ -887,18 +878,20 @@ hipError_t forward_skinny(const MlpParams& p, hipStream_t stream) {
     q.c0 = p.out;
     q.ldc = p.F;
     q.gelu = p.gelu;
-    const dim3 grid(static_cast<unsigned>(over(p.F, 16))), block(256);
+    const dim3 grid(static_cast<unsigned>(over(p.F, 8))), block(256);
     switch (over(p.M, 16)) {
         case 1: hipLaunchKernelGGL((skinny_kernel<T, 1>), grid, block, 0, stream, q); break;
         case 2: hipLaunchKernelGGL((skinny_kernel<T, 2>), grid, block, 0, stream, q); break;
-        default: hipLaunchKernelGGL((skinny_kernel<T, 3>), grid, block, 0, stream, q); break;
+        default:
+            if constexpr (skinny_tokens(sizeof(T) == 2) > 32)
+                hipLaunchKernelGGL((skinny_kernel<T, 3>), grid, block, 0, stream, q);
     }
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t forward(const MlpParams& p, hipStream_t stream) {
-    if (p.M <= kSkinny) return forward_skinny<T>(p, stream);
+    if (p.M <= skinny_tokens(sizeof(T) == 2)) return forward_skinny<T>(p, stream);
     const MlpSpace w(p, sizeof(T) == 2, false);
     ProductParams q = gate_params<T>(p, w, padded<T>(p, w, stream));
     q.c0 = p.out;
@@ -959,7 +952,7 @@ hipError_t backward(const MlpParams& p, hipStream_t stream) {
 }  // namespace
 
 size_t mlp_fwd_workspace_bytes(const MlpParams& p, bool bf16) {
-    if (p.M <= kSkinny) return 0;
+    if (p.M <= skinny_tokens(bf16)) return 0;
     return MlpSpace(p, bf16, false).all;
 }
 

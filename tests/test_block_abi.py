@@ -1,0 +1,327 @@
+"""The C ABI of the gated recurrence, the log probabilities and the feed-forward block on the CPU:
+struct layouts and host-side validation, with fake device addresses that nothing dereferences."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+import selective_state_space_26_amd as msel
+from selective_state_space_26_amd import _lib
+from selective_state_space_26_amd.logprob import _strided
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, NULL, SHAPE, DTYPE, ALIGN, UNSUP, WS, ALIAS, VERSION = 0, 1, 2, 3, 4, 5, 6, 7, 9
+STRUCTS = {"msel_lru_args": _lib.LruArgs, "msel_lru_grads": _lib.LruGrads,
+           "msel_logprob_args": _lib.LogprobArgs, "msel_logprob_grads": _lib.LogprobGrads,
+           "msel_gated_mlp_args": _lib.GatedMlpArgs, "msel_gated_mlp_grads": _lib.GatedMlpGrads}
+INF, NAN = float("inf"), float("nan")
+
+_fake = iter(range(0x10000000, 0x7fffffffffff, 0x10000000))
+
+
+def _addr():
+    return next(_fake)
+
+
+def _set(s, kw):
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+def test_struct_layout_matches_header(tmp_path):
+    src = tmp_path / "layout.c"
+    body = "".join(f'printf("{n} %zu\\n", sizeof({n}));\n'
+                   + "".join(f'printf("{n}.{f} %zu\\n", offsetof({n}, {f}));\n'
+                             for f, _ in s._fields_) for n, s in STRUCTS.items())
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "msel.h"\n'
+                   "int main(void) {\n" + body + "return 0; }\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), str(src), "-o",
+                    str(exe)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+    got = {k: int(v) for k, v in (line.rsplit(" ", 1) for line in out.strip().splitlines())}
+    for n, s in STRUCTS.items():
+        assert got[n] == ctypes.sizeof(s), n
+        for f, _ in s._fields_:
+            assert got[f"{n}.{f}"] == getattr(s, f).offset, (n, f)
+
+
+# ---- the gated recurrence --------------------------------------------------------------------
+
+def _lru(**kw):
+    a = _lib.LruArgs(1, 2, 3, 100, 1, 0, *[_addr() for _ in range(8)])
+    return _set(a, kw)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({}, OK), (dict(h0=None), OK), (dict(final_state=None), OK), (dict(chunk_states=None), OK),
+    (dict(dtype=0), OK), (dict(seqlen=1), OK), (dict(abi_version=2), VERSION),
+    (dict(reserved=1), VERSION), (dict(batch=0), SHAPE), (dict(dim=-1), SHAPE),
+    (dict(seqlen=0), SHAPE), (dict(seqlen=(1 << 28) + 1), SHAPE),
+    (dict(batch=1 << 16, dim=1 << 15), SHAPE), (dict(batch=1 << 20, dim=1024, seqlen=2048), SHAPE),
+    (dict(dtype=2), DTYPE), (dict(x=None), NULL), (dict(gate_a=None), NULL),
+    (dict(gate_x=None), NULL), (dict(lam=None), NULL), (dict(out=None), NULL),
+    (dict(x=0x1008), ALIGN), (dict(gate_a=0x1008), ALIGN), (dict(gate_x=0x1002), ALIGN),
+    (dict(lam=0x1002), ALIGN), (dict(h0=0x1001), ALIGN), (dict(out=0x1008), ALIGN),
+    (dict(final_state=0x1002), ALIGN), (dict(chunk_states=0x1002), ALIGN)])
+def test_lru_fwd_checks(lib, kw, code):
+    a = _lru(**kw)
+    assert lib.msel_validate_lru_fwd(ctypes.byref(a), None, 0) == code
+    assert lib.msel_validate_lru_fwd(None, None, 0) == NULL
+
+
+@pytest.mark.parametrize("out,of,code", [
+    ("out", "x", ALIAS), ("out", "gate_a", ALIAS), ("out", "gate_x", ALIAS), ("out", "lam", ALIAS),
+    ("out", "h0", ALIAS), ("final_state", "h0", OK), ("final_state", "x", ALIAS),
+    ("final_state", "out", ALIAS), ("final_state", "chunk_states", ALIAS),
+    ("chunk_states", "h0", ALIAS), ("chunk_states", "out", ALIAS)])
+def test_lru_fwd_aliases(lib, out, of, code):
+    a = _lru()
+    setattr(a, out, getattr(a, of))
+    assert lib.msel_validate_lru_fwd(ctypes.byref(a), None, 0) == code
+
+
+def test_lru_workspaces(lib):
+    # few long rows are cut into segments; no others need a workspace forward
+    for kw in (dict(seqlen=512), dict(dim=2048, seqlen=4096), dict(seqlen=1)):
+        assert lib.msel_lru_fwd_workspace_bytes(ctypes.byref(_lru(**kw))) == 0
+    a, ws = _lru(seqlen=5000), _addr()
+    need = lib.msel_lru_fwd_workspace_bytes(ctypes.byref(a))
+    assert need > 0
+    v = lambda w, n: lib.msel_validate_lru_fwd(ctypes.byref(a), w, n)  # noqa: E731
+    assert v(ws, need) == OK and v(None, need) == WS and v(ws, need - 1) == WS
+    assert v(ws + 128, need) == ALIGN and v(a.x, need) == ALIAS and v(a.final_state, need) == ALIAS
+    assert lib.msel_lru_fwd_workspace_bytes(ctypes.byref(_lru(dim=0))) == 0
+    assert lib.msel_lru_bwd_workspace_bytes(ctypes.byref(_lru(dtype=9))) == 0
+    # rebuilt chunk states take room in the backward's
+    with_states = lib.msel_lru_bwd_workspace_bytes(ctypes.byref(a))
+    assert lib.msel_lru_bwd_workspace_bytes(ctypes.byref(_lru(seqlen=5000, chunk_states=None))) \
+        > with_states
+
+
+def test_lru_bwd_checks(lib):
+    a, ws = _lru(out=None, final_state=None), _addr()
+    need = lib.msel_lru_bwd_workspace_bytes(ctypes.byref(a))
+
+    def grads(**kw):
+        return _set(_lib.LruGrads(*[_addr() for _ in range(7)]), kw)
+
+    def v(g, w=ws, n=need):
+        return lib.msel_validate_lru_bwd(ctypes.byref(a), ctypes.byref(g) if g else None, w, n)
+    assert v(grads()) == OK and v(None) == NULL
+    for f in ("dout", "dx", "dgate_a", "dgate_x"):
+        assert v(grads(**{f: None})) == NULL
+        assert v(grads(**{f: 0x1008})) == ALIGN
+    for f in ("dfinal_state", "dlam", "dh0"):
+        assert v(grads(**{f: None})) == OK
+        assert v(grads(**{f: 0x1002})) == ALIGN
+    for f in ("dx", "dgate_a", "dgate_x", "dlam", "dh0"):
+        for of in (a.x, a.gate_a, a.gate_x, a.lam, a.h0, a.chunk_states):
+            assert v(grads(**{f: of})) == ALIAS
+        g = grads()
+        setattr(g, f, g.dout)
+        assert v(g) == ALIAS
+    g = grads()
+    g.dgate_a = g.dx
+    assert v(g) == ALIAS
+    assert v(grads(), ws, need - 1) == WS and v(grads(), None, need) == WS
+    g = grads()
+    assert v(g, g.dlam, need) == ALIAS
+
+
+# ---- log probabilities -----------------------------------------------------------------------
+
+def _lp(**kw):
+    a = _lib.LogprobArgs(1, 1000, 70, 1024, 1, 1, 5, 1.0, *[_addr() for _ in range(7)])
+    return _set(a, kw)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({}, OK), (dict(top=0, top_ids=None, top_logprobs=None), OK), (dict(entropy=None), OK),
+    (dict(lse=None), OK), (dict(logprob=None, ids=None), OK), (dict(ids_64bit=0), OK),
+    (dict(scale=0.1), OK), (dict(stride=1000), OK), (dict(vocab=3, top=3), OK),
+    (dict(logits=0x1002), OK), (dict(abi_version=0), VERSION), (dict(vocab=0), SHAPE),
+    (dict(rows=0), SHAPE), (dict(rows=(1 << 30) + 1), SHAPE), (dict(stride=999), SHAPE),
+    (dict(stride=1 << 40), SHAPE), (dict(vocab=(1 << 30) + 1, stride=1 << 31), SHAPE),
+    (dict(dtype=3), DTYPE), (dict(ids_64bit=2), DTYPE), (dict(scale=0.0), SHAPE),
+    (dict(scale=-1.0), SHAPE), (dict(scale=NAN), SHAPE), (dict(scale=INF), SHAPE),
+    (dict(top=-1), SHAPE), (dict(top=65), UNSUP), (dict(vocab=3, top=4), SHAPE),
+    (dict(logits=None), NULL), (dict(ids=None), NULL), (dict(top_ids=None), NULL),
+    (dict(top_logprobs=None), NULL),
+    (dict(top=0, logprob=None, lse=None, entropy=None), NULL), (dict(logits=0x1001), ALIGN),
+    (dict(dtype=0, logits=0x1002), ALIGN), (dict(ids=0x1004), ALIGN), (dict(lse=0x1002), ALIGN),
+    (dict(top_ids=0x1004), ALIGN)])
+def test_logprob_fwd_checks(lib, kw, code):
+    a = _lp(**kw)
+    assert lib.msel_validate_logprob_fwd(ctypes.byref(a), None, 0) == code
+
+
+def test_logprob_fwd_aliases_and_workspace(lib):
+    for out in ("logprob", "lse", "entropy", "top_ids", "top_logprobs"):
+        for of in ("logits", "ids"):
+            a = _lp()
+            setattr(a, out, getattr(a, of))
+            assert lib.msel_validate_logprob_fwd(ctypes.byref(a), None, 0) == ALIAS
+    a = _lp()
+    a.entropy = a.lse
+    assert lib.msel_validate_logprob_fwd(ctypes.byref(a), None, 0) == ALIAS
+    a, ws = _lp(vocab=50257, stride=50257, rows=3), _addr()
+    need = lib.msel_logprob_fwd_workspace_bytes(ctypes.byref(a))
+    assert need > 0
+    v = lambda w, n: lib.msel_validate_logprob_fwd(ctypes.byref(a), w, n)  # noqa: E731
+    assert v(ws, need) == OK and v(ws, need - 1) == WS and v(None, need) == WS
+    assert v(ws + 64, need) == ALIGN and v(a.logits, need) == ALIAS
+    for kw in (dict(rows=10000), dict(vocab=100, stride=100, rows=3), dict(top=99), dict(scale=0)):
+        b = _lp(**{**dict(vocab=50257, stride=50257), **kw})
+        assert lib.msel_logprob_fwd_workspace_bytes(ctypes.byref(b)) == 0
+
+
+def test_every_slice_has_room_for_the_likeliest(lib):
+    """The workspace of sliced rows holds `top` keys per slice, which each slice has to have: the
+    sizes follow from the workspace's, whose sums take 12 bytes and whose keys 8."""
+    for rows in (1, 2, 7, 100, 511):
+        for vocab in (2049, 4097, 8193, 50257, 65537, 131073, 196609, 1000003):
+            for top in (1, 20, 21, 22, 64):
+                a = _lp(vocab=vocab, stride=vocab, rows=rows, top=top)
+                need = lib.msel_logprob_fwd_workspace_bytes(ctypes.byref(a))
+                if need == 0:
+                    continue
+                slices = next(s for s in range(2, 65)
+                              if (rows * s * 12 + 255) // 256 * 256 + rows * s * top * 8 == need)
+                n = min((512 + rows - 1) // rows, (vocab + 4095) // 4096, min(48, 1024 // top))
+                width = ((vocab + n - 1) // n + 63) // 64 * 64
+                assert slices == -(-vocab // width) and slices * top <= 1024
+                assert vocab - (slices - 1) * width >= top, (rows, vocab, top)
+
+
+def test_logprob_bwd_checks(lib):
+    def grads(**kw):
+        return _set(_lib.LogprobGrads(*[_addr() for _ in range(4)], 1000), kw)
+
+    def v(g, **kw):
+        return lib.msel_validate_logprob_bwd(ctypes.byref(_lp(**kw)),
+                                             ctypes.byref(g) if g else None)
+    assert v(grads()) == OK and v(None) == NULL
+    assert v(grads(dlogprob=None), ids=None) == OK
+    assert v(grads(), ids=None) == NULL
+    assert v(grads(dentropy=None), entropy=None) == OK
+    assert v(grads(), entropy=None) == NULL
+    assert v(grads(), lse=None) == NULL and v(grads(dlogits=None)) == NULL
+    assert v(grads(dlse=None)) == OK and v(grads(dstride=999)) == SHAPE
+    assert v(grads(dstride=1 << 40)) == SHAPE
+    assert v(grads(dlogits=0x1001)) == ALIGN and v(grads(dlse=0x1002)) == ALIGN
+    assert v(grads(), scale=0.0) == SHAPE
+    a = _lp()
+    for of in (a.ids, a.lse, a.entropy):
+        g = grads(dlogits=of)
+        assert lib.msel_validate_logprob_bwd(ctypes.byref(a), ctypes.byref(g)) == ALIAS
+    # in place with the logits' stride, and not beside them
+    for at, stride, code in ((a.logits, 1024, OK), (a.logits, 1000, SHAPE),
+                             (a.logits + 2000, 1024, ALIAS), (a.logits - 1024, 1024, ALIAS),
+                             (a.logits + 2 * (69 * 1024 + 1000), 1024, OK)):
+        g = grads(dlogits=at, dstride=stride)
+        assert lib.msel_validate_logprob_bwd(ctypes.byref(a), ctypes.byref(g)) == code
+    g = grads()
+    g.dlogits = g.dlogprob
+    assert v(g) == ALIAS
+
+
+def test_strided_rows_are_read_from_the_tensor():
+    t = torch.zeros(4, 6, 10)
+    assert _strided(t, "t") == (24, 10)
+    assert _strided(t[..., :7], "t") == (24, 10)
+    assert _strided(t[:, 0, :7], "t") == (4, 60)
+    assert _strided(t[:1, :1, :7], "t") == (1, 7)
+    assert _strided(t[0, 0], "t") == (1, 10)
+    assert _strided(torch.zeros(5, 1).expand(5, 1), "t") == (5, 1)
+    for bad in (t[:, :3], t.transpose(0, 1), t[..., ::2], t.transpose(1, 2),
+                torch.zeros(1, 10).expand(4, 10)):
+        if bad.shape == (4, 10):  # rows on top of each other: the library refuses the stride
+            assert _strided(bad, "t") == (4, 0)
+            continue
+        with pytest.raises(ValueError):
+            _strided(bad, "t")
+
+
+# ---- the gated feed-forward block ------------------------------------------------------------
+
+def _mlp(**kw):
+    a = _lib.GatedMlpArgs(1, 768, 2048, 1, 1000, 0, 0, *[_addr() for _ in range(4)])
+    return _set(a, kw)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({}, OK), (dict(activation=1), OK), (dict(dtype=0), OK), (dict(tokens=1), OK),
+    (dict(abi_version=3), VERSION), (dict(reserved=1), VERSION), (dict(dim=0), SHAPE),
+    (dict(hidden=0), SHAPE), (dict(tokens=0), SHAPE), (dict(tokens=(1 << 24) + 1), SHAPE),
+    (dict(tokens=1 << 24, hidden=(1 << 16) + 64), SHAPE), (dict(dim=(1 << 17) + 1), UNSUP),
+    (dict(hidden=(1 << 17) + 1), UNSUP), (dict(dtype=2), DTYPE), (dict(activation=2), DTYPE),
+    (dict(x=None), NULL), (dict(w_gate=None), NULL), (dict(w_up=None), NULL),
+    (dict(out=None), NULL), (dict(x=0x1008), ALIGN), (dict(w_gate=0x1004), ALIGN),
+    (dict(w_up=0x1002), ALIGN), (dict(out=0x1008), ALIGN)])
+def test_mlp_fwd_checks(lib, kw, code):
+    assert lib.msel_validate_gated_mlp_fwd(ctypes.byref(_mlp(**kw)), None, 0) == code
+
+
+def test_mlp_aliases_and_workspaces(lib):
+    for of in ("x", "w_gate", "w_up"):
+        a = _mlp()
+        a.out = getattr(a, of)
+        assert lib.msel_validate_gated_mlp_fwd(ctypes.byref(a), None, 0) == ALIAS
+    # widths of whole stages and few tokens need no copies forward
+    assert lib.msel_gated_mlp_fwd_workspace_bytes(ctypes.byref(_mlp())) == 0
+    assert lib.msel_gated_mlp_fwd_workspace_bytes(ctypes.byref(_mlp(dim=770, tokens=8))) == 0
+    a, ws = _mlp(dim=770), _addr()
+    need = lib.msel_gated_mlp_fwd_workspace_bytes(ctypes.byref(a))
+    assert need >= 2 * 832 * (1000 + 2 * 2048)
+    v = lambda w, n: lib.msel_validate_gated_mlp_fwd(ctypes.byref(a), w, n)  # noqa: E731
+    assert v(ws, need) == OK and v(ws, need - 1) == WS and v(None, need) == WS
+    assert v(ws + 16, need) == ALIGN and v(a.w_up, need) == ALIAS
+    assert lib.msel_gated_mlp_fwd_workspace_bytes(ctypes.byref(_mlp(dim=0))) == 0
+
+    a = _mlp(out=None)
+    need = lib.msel_gated_mlp_bwd_workspace_bytes(ctypes.byref(a))
+    assert need >= 2 * 1000 * 4096
+
+    def grads(**kw):
+        return _set(_lib.GatedMlpGrads(*[_addr() for _ in range(4)]), kw)
+
+    def b(g, w=ws, n=need):
+        return lib.msel_validate_gated_mlp_bwd(ctypes.byref(a), ctypes.byref(g) if g else None, w,
+                                               n)
+    assert b(grads()) == OK and b(None) == NULL and b(grads(dout=None)) == NULL
+    assert b(grads(dx=None)) == OK and b(grads(dw_gate=None, dw_up=None)) == OK
+    assert b(grads(dw_gate=None)) == NULL and b(grads(dw_up=None)) == NULL
+    assert b(grads(dx=None, dw_gate=None, dw_up=None)) == NULL
+    for f in ("dout", "dx", "dw_gate", "dw_up"):
+        assert b(grads(**{f: 0x1008})) == ALIGN
+    for f in ("dx", "dw_gate", "dw_up"):
+        for of in (a.x, a.w_gate, a.w_up):
+            assert b(grads(**{f: of})) == ALIAS
+    g = grads()
+    g.dw_up = g.dw_gate
+    assert b(g) == ALIAS
+    assert b(grads(), None, need) == WS and b(grads(), ws, need - 1) == WS
+    g = grads()
+    assert b(g, g.dout, need) == ALIAS
+
+
+def test_tensors_of_the_host_are_refused():
+    x = torch.zeros(2, 3, 5)
+    lam = torch.zeros(3)
+    for f in (lambda: msel.msel_lru_fwd(x, x, x, lam), lambda: msel.msel_lru_bwd(x, x, x, lam, x),
+              lambda: msel.msel_lru_fwd(x[0], x[0], x[0], lam),
+              lambda: msel.msel_logprob_fwd(x), lambda: msel.msel_logprob_bwd(x, None, lam),
+              lambda: msel.msel_logprob_fwd(x[:0]),
+              lambda: msel.msel_gated_mlp_fwd(x, x[0], x[0]),
+              lambda: msel.msel_gated_mlp_bwd(x, x[0], x[0], x)):
+        with pytest.raises(ValueError):
+            f()

@@ -1,0 +1,270 @@
+"""The gated recurrence, the log probabilities and the feed-forward block as programs call them: in
+the checked build, on another stream, two at once, captured in graphs, with a caller's workspace,
+twice alike."""
+import pytest
+
+from helpers import log
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import selective_state_space_26_amd as msel  # noqa: E402
+from selective_state_space_26_amd import _lib  # noqa: E402
+
+from lm_helpers import normal  # noqa: E402
+
+
+def _lru(shape, dtype, chunks=True):
+    t = dict(x=normal(shape, dtype, 1), gate_a=normal(shape, dtype, 2),
+             gate_x=normal(shape, dtype, 3), lam=-normal(shape[1:2], "f32", 4).abs(),
+             h0=normal(shape[:2], "f32", 5))
+    dout = normal(shape, dtype, 6)
+
+    def run():
+        out, final, cs = msel.msel_lru_fwd(**t, return_chunk_states=True)
+        g = msel.msel_lru_bwd(**t, dout=dout, dfinal_state=final,
+                              chunk_states=cs if chunks else None, want_dh0=True)
+        return dict(out=out, final=final, cs=cs, **g)
+    return run, [*t.values(), dout]
+
+
+def _logprob(rows, vocab, dtype, top):
+    x = normal((rows, vocab), dtype, 1, 3.0)
+    ids = (torch.arange(rows, device="cuda") * 7 - 3) % (vocab + 2)
+    dlp, dh = normal((rows,), "f32", 2), normal((rows,), "f32", 3)
+
+    def run():
+        r = msel.msel_logprob_fwd(x, ids, 0.9, top, want_entropy=True)
+        r["dlogits"] = msel.msel_logprob_bwd(x, ids, r["lse"], dlp, dlp, dh, r["entropy"], 0.9)
+        return {k: v for k, v in r.items() if v is not None}
+    return run, [x, dlp, dh]
+
+
+def _mlp(tokens, dim, hidden, dtype, act="silu"):
+    x, wg = normal((tokens, dim), dtype, 1), normal((hidden, dim), dtype, 2, dim ** -0.5)
+    wu, dout = normal((hidden, dim), dtype, 3, dim ** -0.5), normal((tokens, hidden), dtype, 4)
+
+    def run():
+        return dict(out=msel.msel_gated_mlp_fwd(x, wg, wu, act),
+                    **msel.msel_gated_mlp_bwd(x, wg, wu, dout, act))
+    return run, [x, wg, wu, dout]
+
+
+# every kernel and every plan that a call can take
+CASES = {
+    "lru_step": lambda: _lru((5, 70, 1), "bf16"),
+    "lru_lane": lambda: _lru((3, 50, 7), "f32"),
+    "lru_16": lambda: _lru((3, 50, 99), "bf16"),
+    "lru_wave": lambda: _lru((2, 50, 400), "f32", chunks=False),
+    "lru_rows": lambda: _lru((3, 700, 530), "bf16"),
+    "lru_full_tiles": lambda: _lru((8, 1024, 2048), "bf16"),
+    "lru_4_waves": lambda: _lru((1, 200, 2500), "f32", chunks=False),
+    "lru_16_waves": lambda: _lru((1, 150, 9001), "bf16"),
+    "lru_16_waves_f32": lambda: _lru((1, 130, 33000), "f32"),
+    "lru_long_rows": lambda: _lru((1, 4100, 32768), "bf16", chunks=False),
+    "lru_segments": lambda: _lru((2, 3, 6000), "f32", chunks=False),
+    "lru_most_segments": lambda: _lru((1, 2, 33001), "bf16"),
+    "logprob_4x1": lambda: _logprob(300, 15, "f32", 5),
+    "logprob_4x4": lambda: _logprob(70, 61, "f32", 10),
+    "logprob_16": lambda: _logprob(33, 400, "bf16", 64),
+    "logprob_64": lambda: _logprob(9, 1001, "f32", 20),
+    "logprob_held": lambda: _logprob(600, 3001, "bf16", 3),
+    "logprob_slices": lambda: _logprob(3, 50257, "f32", 20),
+    "logprob_slices_wide": lambda: _logprob(1, 400001, "bf16", 64),
+    "logprob_slices_no_top": lambda: _logprob(7, 20001, "bf16", 0),
+    "logprob_wide": lambda: _logprob(600, 9001, "f32", 0),
+    "logprob_wide_top": lambda: _logprob(520, 17001, "bf16", 8),
+    "mlp_1": lambda: _mlp(1, 200, 90, "bf16"),
+    "mlp_few": lambda: _mlp(30, 129, 65, "bf16", "gelu"),
+    "mlp_few_f32": lambda: _mlp(45, 33, 70, "f32"),
+    "mlp_odd": lambda: _mlp(333, 205, 311, "bf16"),
+    "mlp_odd_f32": lambda: _mlp(190, 77, 300, "f32", "gelu"),
+    "mlp_split": lambda: _mlp(900, 128, 1024, "bf16"),
+    "mlp_wide": lambda: _mlp(4500, 256, 2100, "bf16"),
+    "mlp_wide_f32": lambda: _mlp(4300, 64, 2200, "f32"),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_in_range_and_twice_alike(name):
+    """The checked build counts no index out of its buffer, and it and a second run give the same
+    bits."""
+    log(f"checked build, {name}")
+    run, _ = CASES[name]()
+    with _lib.using(_lib.LIB_CHECKED_PATH):
+        msel.bound_violations()
+        got = {k: v.clone() for k, v in run().items() if v is not None}
+        count, f, line = msel.bound_violations()
+        assert count == 0, f"{count} out-of-range indexes, the first at {f}:{line}"
+    for _ in range(2):
+        again = run()
+        for k, v in got.items():
+            assert torch.equal(v, again[k]), k
+
+
+GRAPHS = ["lru_step", "lru_lane", "lru_rows", "lru_4_waves", "lru_segments", "logprob_4x1",
+          "logprob_slices", "logprob_wide_top", "mlp_few", "mlp_odd", "mlp_split"]
+
+
+@pytest.mark.parametrize("name", GRAPHS)
+def test_replays_match_eager_steps(name):
+    log(f"graph {name}")
+    run, inputs = CASES[name]()
+    run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        run()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            cap = run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    cap = {k: v for k, v in cap.items() if v is not None}
+    for k in range(4):
+        for t in inputs:  # new values in the same memory
+            t.copy_(t.flip(0) * 0.75)
+        for v in cap.values():
+            v.fill_(-1)
+        eager = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, v in cap.items():
+            assert torch.equal(v, eager[n]), (k, n)
+
+
+@pytest.mark.parametrize("name", GRAPHS)
+def test_two_graphs_side_by_side(name):
+    """Two captured calls, each with the workspace that its capture took, replayed on two streams at
+    once."""
+    log(f"two graphs {name}")
+    made = [CASES[name]() for _ in range(2)]
+    for t in made[1][1]:
+        t.copy_(t.flip(0) * 0.5)
+    refs = [{k: v.clone() for k, v in run().items() if v is not None} for run, _ in made]
+    torch.cuda.synchronize()
+    streams, graphs, caps = [torch.cuda.Stream() for _ in made], [], []
+    for (run, _), s in zip(made, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s):
+            run()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(g, stream=s):
+                caps.append(run())
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for cap, ref in zip(caps, refs):
+        for k, v in ref.items():
+            assert torch.equal(cap[k], v), k
+
+
+@pytest.mark.parametrize("name", ["lru_rows", "lru_segments", "logprob_slices", "logprob_wide",
+                                  "mlp_few", "mlp_odd"])
+def test_runs_on_the_current_stream(name):
+    """Inputs written on a side stream behind long work there: a call that went to another stream
+    would read what was in them before, or zeros that come after."""
+    log(f"streams {name}")
+    run, inputs = CASES[name]()
+    ref = {k: v.clone() for k, v in run().items() if v is not None}
+    keep = [t.clone() for t in inputs]
+    for t in inputs:
+        t.zero_()
+    m = torch.randn(4096, 4096, device="cuda").bfloat16()
+    out = torch.empty_like(m)
+    torch.mm(m, m, out=out)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(200):  # some 100 us each
+            torch.mm(m, m, out=out)
+        for t, k in zip(inputs, keep):
+            t.copy_(k)
+        got = {k: v.clone() for k, v in run().items() if v is not None}
+        for t in inputs:
+            t.zero_()
+    torch.cuda.synchronize()
+    for k, v in ref.items():
+        assert torch.equal(got[k], v), k
+
+
+@pytest.mark.parametrize("name", [n for n in CASES if n != "lru_long_rows"])
+def test_nothing_is_written_behind_the_workspace(name):
+    log(f"workspace {name}")
+    run, _ = CASES[name]()
+    ref = run()
+    guard, taken = 1 << 16, []
+
+    def ask(workspace, need, dev):
+        if need == 0:
+            return None, 0
+        buf = torch.full((need + guard,), 0x5A, device=dev, dtype=torch.uint8)
+        taken.append((need, buf))
+        return buf, need  # the library is told of the size that it asked for
+    with pytest.MonkeyPatch.context() as m:
+        for mod in ("lru", "logprob", "gated_mlp"):
+            m.setattr(f"selective_state_space_26_amd.{mod}._workspace", ask)
+        got = run()
+    torch.cuda.synchronize()
+    for need, buf in taken:
+        assert bool((buf[need:] == 0x5A).all())
+    for k, v in ref.items():
+        assert v is None or torch.equal(v, got[k]), k
+
+
+def test_a_workspace_of_the_caller():
+    log("a workspace of the caller")
+    x, wg, wu = normal((200, 70), "bf16", 1), normal((90, 70), "bf16", 2), normal((90, 70), "bf16", 3)
+    ws = torch.empty(1 << 22, device="cuda", dtype=torch.uint8)
+    ref = msel.msel_gated_mlp_fwd(x, wg, wu)
+    assert torch.equal(msel.msel_gated_mlp_fwd(x, wg, wu, workspace=ws), ref)
+    assert torch.equal(msel.msel_gated_mlp_fwd(x, wg, wu, workspace=ws[:8]), ref)  # too small: its own
+    for bad in (ws.cpu(), ws[::2]):
+        with pytest.raises((ValueError, TypeError)):
+            msel.msel_gated_mlp_fwd(x, wg, wu, workspace=bad)
+    with pytest.raises(RuntimeError):  # not on 256 bytes
+        msel.msel_gated_mlp_fwd(x, wg, wu, workspace=ws[16:])
+
+
+def test_rows_beyond_32_bits_of_elements():
+    """Offsets past 2^31 elements: the last rows equal the same rows alone."""
+    log("large offsets")
+    rows, vocab = 43000, 50257  # 2.16e9 logits
+    x = torch.empty((rows, vocab), device="cuda", dtype=torch.bfloat16)
+    x[-64:].normal_(0.0, 3.0, generator=torch.Generator(device="cuda").manual_seed(1))
+    x[:-64] = 0.5
+    ids = torch.arange(rows, device="cuda")
+    r = msel.msel_logprob_fwd(x, ids, want_entropy=True, top=2)
+    tail, tid = x[-64:], ids[-64:]  # the same lines of memory
+    one = msel.msel_logprob_fwd(tail, tid, want_entropy=True, top=2)
+    near = lambda a, b: float((a - b).abs().max()) <= 1e-4  # noqa: E731
+    assert near(r["lse"][-64:], one["lse"]) and near(r["entropy"][-64:], one["entropy"])
+    assert near(r["logprob"][-64:], one["logprob"])
+    assert torch.equal(r["top_ids"][-64:], one["top_ids"])
+    dlp = torch.ones(rows, device="cuda")
+    d = msel.msel_logprob_bwd(x, ids, r["lse"], dlp)
+    assert torch.equal(d[-64:], msel.msel_logprob_bwd(tail, tid, r["lse"][-64:].contiguous(),
+                                                      dlp[-64:]))
+    del x, d
+    L = 40000
+    t = {k: torch.empty((1, 54000, L), device="cuda", dtype=torch.bfloat16).fill_(0.5)
+         for k in ("x", "gate_a", "gate_x")}
+    for i, v in enumerate(t.values()):
+        v[:, -3:].copy_(normal((1, 3, L), "bf16", i))
+    lam = -torch.ones(54000, device="cuda")
+    out, final, cs = msel.msel_lru_fwd(**t, lam=lam, return_chunk_states=True)
+    part = {k: v[:, -3:].contiguous() for k, v in t.items()}
+    o1, f1, c1 = msel.msel_lru_fwd(**part, lam=lam[-3:].contiguous(), return_chunk_states=True)
+    near = lambda a, b: float((a.float() - b.float()).abs().max()) <= 2e-2  # noqa: E731
+    assert near(out[:, -3:], o1) and near(final[:, -3:], f1) and near(cs[:, -3:], c1)
+    assert bool((out[:, 0] == out[:, 100]).all())
