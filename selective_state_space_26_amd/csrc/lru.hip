@@ -435,8 +435,9 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void lru_bwd_kernel(LruPar
             if constexpr (TEAM >= 64) {
                 const int c = min(__builtin_amdgcn_readfirstlane(t / kTile), p.nchunks - 1);
                 h = p.chunks[MSEL_IDX(row * p.nchunks + c, rows * p.nchunks)];
-            } else {
-                h = p.h0 != nullptr ? p.h0[MSEL_IDX(row, rows)] : 0.0f;
+            } else {  // a row is one chunk: its state, or without chunk states the row's own
+                const float* const from = p.chunks != nullptr ? p.chunks : p.h0;
+                h = from != nullptr ? from[MSEL_IDX(row, rows)] : 0.0f;
             }
             if (t0 - tile >= t_lo) {
                 nx = ld_row(x, t - tile, p.L);

@@ -156,3 +156,37 @@ def test_optional_outputs():
     g = msel.msel_lru_bwd(**t, dout=dout, want_dlam=False)
     assert g["dlam"] is None and g["dh0"] is None
     assert torch.equal(g["dx"], msel.msel_lru_bwd(**t, dout=dout)["dx"])
+
+
+@pytest.mark.parametrize("shape", [(3, 50, 1), (3, 50, 7), (2, 9, 99), (2, 9, 300), (1, 5, 1500)])
+def test_chunk_states_stand_for_the_carried_state(shape):
+    """The backward starts from the chunk states that it is given, at every length: h0 itself is
+    not needed then."""
+    t = _inputs(shape, "f32", True)
+    dout = normal(shape, "f32", 6)
+    _, _, chunks = msel.msel_lru_fwd(**t, return_chunk_states=True)
+    both = msel.msel_lru_bwd(**t, dout=dout, chunk_states=chunks, want_dh0=True)
+    t["h0"] = None
+    alone = msel.msel_lru_bwd(**t, dout=dout, chunk_states=chunks, want_dh0=True)
+    for k in both:
+        assert torch.equal(both[k], alone[k]), k
+
+
+@pytest.mark.parametrize("shape", [(1, 130, 4700), (2, 100, 8300)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_blocks_of_a_row(shape, dtype):
+    """Rows that a whole block of 16 wavefronts (8 in the backward) works on, over several of its
+    tiles and a part of one."""
+    log(f"lru blocks {shape} {dtype}")
+    t = _inputs(shape, dtype, True)
+    dout, dfinal = normal(shape, dtype, 6), normal(shape[:2], "f32", 7)
+    out, final, chunks = msel.msel_lru_fwd(**t, return_chunk_states=True)
+    ref = block.lru_fwd(*_oracle_args(t), values(t["h0"]))
+    within("out", out, ref["out"], ref["out_err"])
+    within("final", final, ref["final"], ref["final_err"])
+    got = msel.msel_lru_bwd(**t, dout=dout, dfinal_state=dfinal, chunk_states=chunks,
+                            want_dh0=True)
+    ref = block.lru_bwd(*_oracle_args(t), values(dout), values(t["h0"]), values(dfinal))
+    for k, r in (("dx", "dx"), ("dgate_a", "dga"), ("dgate_x", "dgx"), ("dlam", "dlam"),
+                 ("dh0", "dh0")):
+        within(k, got[k], ref[r], ref[r + "_err"])
