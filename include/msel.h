@@ -687,7 +687,7 @@ msel_status msel_grad_clip(const msel_grad_args *args, void *workspace, size_t w
 typedef struct {
     int32_t abi_version;    /* must be MSEL_ABI_VERSION                                    */
     int32_t batch;          /* >= 1                                                        */
-    int32_t dim;            /* channels, >= 1; batch * dim up to 2^30                       */
+    int32_t dim;            /* channels, 1..2^27; batch * dim up to 2^30                    */
     int32_t seqlen;         /* 1..MSEL_MAX_SEQLEN                                          */
     int32_t dtype;          /* msel_dtype of x, gate_a, gate_x, out and of their gradients  */
     int32_t reserved;       /* must be 0                                                   */

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxChannels = int64_t(1) << 27;  // dlam's sum: 64 of them per block of 1024
 
 typedef std::initializer_list<const void*> Pointers;
 
@@ -62,7 +63,8 @@ msel_status check_lru_sizes(const msel_lru_args* a) {
     if (a->abi_version != MSEL_ABI_VERSION || a->reserved != 0) return MSEL_ERR_VERSION;
     if (a->batch < 1 || a->dim < 1 || a->seqlen < 1) return MSEL_ERR_SHAPE;
     const int64_t rows = static_cast<int64_t>(a->batch) * a->dim;
-    if (a->seqlen > MSEL_MAX_SEQLEN || rows > kMaxRows || rows > kMaxElems / a->seqlen)
+    if (a->seqlen > MSEL_MAX_SEQLEN || a->dim > kMaxChannels || rows > kMaxRows ||
+        rows > kMaxElems / a->seqlen)
         return MSEL_ERR_SHAPE;
     return is_dtype(a->dtype) ? MSEL_OK : MSEL_ERR_DTYPE;
 }

@@ -28,7 +28,7 @@ namespace {
 constexpr int kStep = 8;  // steps per lane: 16 bytes of bf16
 constexpr int kTile = 64 * kStep;
 static_assert(kTile == kChunk, "a wavefront's tile starts at a chunk boundary");
-constexpr unsigned kMaxBlocks = 1u << 22;  // a grid has fewer than 2^32 threads
+constexpr unsigned kMaxBlocks = 1u << 21;  // of up to 1024: a grid has fewer than 2^32 threads
 constexpr int kMaxSegments = 63;           // a wavefront composes them and h0
 
 // One step's factors.

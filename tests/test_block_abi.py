@@ -325,3 +325,15 @@ def test_tensors_of_the_host_are_refused():
               lambda: msel.msel_gated_mlp_bwd(x, x[0], x[0], x)):
         with pytest.raises(ValueError):
             f()
+
+
+@pytest.mark.parametrize("batch,dim,code", [(8, 1 << 27, OK), (1, 1 << 27, OK),
+                                            (1, (1 << 27) + 1, SHAPE), (9, 1 << 27, SHAPE)])
+def test_lru_channels_that_a_grid_holds(lib, batch, dim, code):
+    a = _lru(batch=batch, dim=dim, seqlen=1)
+    g = _lib.LruGrads(*[_addr() for _ in range(7)])
+    need = lib.msel_lru_bwd_workspace_bytes(ctypes.byref(a))
+    assert (need > 0) == (code == OK)
+    ws = _addr()
+    assert lib.msel_validate_lru_fwd(ctypes.byref(a), ws, 1 << 50) == code
+    assert lib.msel_validate_lru_bwd(ctypes.byref(a), ctypes.byref(g), ws, 1 << 50) == code
