@@ -63,7 +63,8 @@ __device__ __forceinline__ void act_grad(float z, float& v, float& slope) {
     const float s = sigmoid_f(GELU ? kTwoC * z * fmaf(0.044715f * z, z, 1.0f) : z);
     v = z * s;
     const float w = v - v * s;
-    slope = GELU ? fmaf(w, kTwoC * fmaf(0.134145f * z, z, 1.0f), s) : w + s;
+    // w is 0 long before the polynomial beside it leaves fp32's range
+    slope = GELU ? fmaf(w, kTwoC * fminf(fmaf(0.134145f * z, z, 1.0f), 1e30f), s) : w + s;
 }
 // f(GELU as a type): one branch around a whole epilogue, not two activations per element.
 template <typename Fn>

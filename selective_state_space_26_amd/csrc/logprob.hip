@@ -28,6 +28,8 @@ namespace msel {
 namespace {
 
 constexpr float kLowest = -3.402823466e38f;
+// A scale for powers of 2; finite for every finite scale, since it multiplies differences of 0.
+__device__ __forceinline__ float base2(float scale) { return fminf(scale * kLog2e, -kLowest); }
 constexpr int kThreads = 256;
 constexpr int kCandidates = 1024;
 constexpr unsigned kMaxBlocks = 1u << 22;  // a grid has fewer than 2^32 threads
@@ -219,7 +221,7 @@ template <typename T, int TEAM, int NV>
 __global__ __launch_bounds__(kThreads) void narrow_fwd_kernel(LogprobParams p) {
     using Row = NarrowRow<T, TEAM, NV>;
     const int l = threadIdx.x % TEAM;
-    const float k2 = p.scale * kLog2e;
+    const float k2 = base2(p.scale);
     constexpr int kTeams = kThreads / TEAM;
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kTeams; r0 < p.rows;
          r0 += static_cast<int64_t>(gridDim.x) * kTeams) {
@@ -258,7 +260,7 @@ struct RowGrad {
         cp = (p.dlse != nullptr ? p.dlse[at] : 0.0f) - dt;
         ch = p.dentropy != nullptr ? p.dentropy[at] : 0.0f;
         h = p.dentropy != nullptr ? p.in_entropy[at] : 0.0f;
-        k2 = p.scale * kLog2e;
+        k2 = base2(p.scale);
         m = 0.0f;
         lse = p.in_lse[at] * kLog2e;
         dead = false;
@@ -533,7 +535,7 @@ template <typename T, bool ENTROPY, bool TOP>
 __global__ __launch_bounds__(kThreads) void wide_fwd_kernel(LogprobParams p) {
     __shared__ Sums part[kThreads / 64];
     __shared__ typename std::conditional<TOP, TopList, char>::type list;
-    const float k2 = p.scale * kLog2e;
+    const float k2 = base2(p.scale);
     const int64_t units = p.rows * p.slices;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t r = p.slices == 1 ? u : u / p.slices;
@@ -558,7 +560,7 @@ __global__ __launch_bounds__(kThreads) void held_fwd_kernel(LogprobParams p) {
     constexpr int kRound = kThreads * VE, N = kHeldCols / kRound;
     __shared__ Sums part[kThreads / 64];
     __shared__ typename std::conditional<TOP, TopList, char>::type list;
-    const float k2 = p.scale * kLog2e;
+    const float k2 = base2(p.scale);
     const int64_t units = p.rows * p.slices;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t r = p.slices == 1 ? u : u / p.slices;
@@ -596,7 +598,7 @@ __global__ __launch_bounds__(kThreads) void held_fwd_kernel(LogprobParams p) {
 // The slices of a row joined, a block per row.  Up to kCandidates keys.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void join_kernel(LogprobParams p) {
-    const float k2 = p.scale * kLog2e;
+    const float k2 = base2(p.scale);
     const Sums* parts = static_cast<const Sums*>(p.ws);
     const Key* keys = reinterpret_cast<const Key*>(static_cast<const char*>(p.ws) +
                                                    sums_bytes(p.rows, p.slices));

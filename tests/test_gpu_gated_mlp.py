@@ -166,3 +166,24 @@ def test_refusals():
         with pytest.raises((TypeError, ValueError, RuntimeError)):
             f()
             pytest.fail(f"call {i} was not refused")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("size", [30.0, 1e15, 1e21])
+def test_gates_far_out(act, size):
+    """Where the gate is saturated its slope is 1 or 0, however large its argument: one input, a
+    hidden unit for each sign, and nothing added or lost."""
+    x = torch.tensor([[size]], device="cuda")
+    wg = torch.tensor([[1.0], [-1.0]], device="cuda")
+    wu = torch.full((2, 1), 2.0 ** -40, device="cuda")
+    dout = torch.ones((1, 2), device="cuda")
+    u = size * 2.0 ** -40
+    out = msel.msel_gated_mlp_fwd(x, wg, wu, act)
+    assert out[0, 0].item() == pytest.approx(size * u, rel=1e-6) and abs(out[0, 1].item()) < 1e-8
+    g = msel.msel_gated_mlp_bwd(x, wg, wu, dout, act)
+    # dx = dG wg + dU wu = u + size 2^-40, dw_gate = u x for the open unit and 0 for the closed one
+    assert g["dx"].item() == pytest.approx(2 * u, rel=1e-6)
+    for k, v in (("dw_gate", u * size), ("dw_up", size * size)):
+        if v < 3e38:
+            assert g[k][0].item() == pytest.approx(v, rel=1e-6)
+        assert abs(g[k][1].item()) < 1e-7 * max(1.0, size)

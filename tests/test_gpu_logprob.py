@@ -229,3 +229,29 @@ def test_refusals():
         with pytest.raises((TypeError, ValueError, RuntimeError)):
             f()
             pytest.fail(f"call {i} was not refused")
+
+
+@pytest.mark.parametrize("vocab", [50, 700, 1500, 9000, 40000])
+@pytest.mark.parametrize("scale", [3.0e38, 1e-38])
+def test_scales_at_the_ends_of_fp32(vocab, scale):
+    """At the largest scale a row's largest logit has all the probability, at the smallest every
+    logit the same."""
+    x = normal((3, vocab), "f32", 3).clamp(-8, 8)
+    ids = torch.tensor([0, 1, 2], device="cuda")
+    best = torch.tensor([0, 9, 2], device="cuda")
+    x.scatter_(1, best[:, None], 9.0)
+    r = msel.msel_logprob_fwd(x, ids, scale, want_entropy=True)
+    one, dh = torch.ones(3, device="cuda"), torch.full((3,), 0.5, device="cuda")
+    d = msel.msel_logprob_bwd(x, ids, r["lse"], one, None, dh, r["entropy"], scale)
+    if scale > 1:
+        assert r["logprob"].tolist() == [0.0, -float("inf"), 0.0]
+        assert r["entropy"].tolist() == [0.0, 0.0, 0.0]
+        want = torch.zeros_like(x)
+        want[1, 1], want[1, 9] = scale, -scale
+        assert torch.equal(d, want)
+    else:
+        # log V and its negative to a few roundings of their sums (V / 256 + 20 terms one after another)
+        lse = torch.log(torch.tensor(float(vocab), dtype=torch.float64))
+        for k, v in (("logprob", -lse), ("lse", lse), ("entropy", lse)):
+            assert (r[k].double().cpu() - v).abs().max() < 2 ** -24 * (vocab / 256 + 40 + 4 * lse)
+        assert torch.isfinite(d).all()
