@@ -683,6 +683,9 @@ msel_status msel_grad_clip(const msel_grad_args *args, void *workspace, size_t w
  * [dim] fp32; h0, final_state, dfinal_state, dh0 [batch, dim] fp32; chunk_states [batch, dim,
  * msel_num_chunks(seqlen)] fp32, entry c the state before step c * msel_chunk_len().  States and
  * sums are fp32.
+ *
+ * Here and in the two sections below an output that shares memory with an input, another output or
+ * the workspace, in part too, is refused (MSEL_ERR_ALIAS), but for what may be equal.
  * ---------------------------------------------------------------------------------------- */
 typedef struct {
     int32_t abi_version;    /* must be MSEL_ABI_VERSION                                    */

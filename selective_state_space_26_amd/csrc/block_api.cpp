@@ -36,22 +36,31 @@ bool all_aligned(Pointers ps, uintptr_t a) {
     return std::all_of(ps.begin(), ps.end(), [=](const void* p) { return aligned(p, a); });
 }
 
-// Whether an output equals an input or another output (null ones aside).
-bool aliased(Pointers outs, Pointers ins) {
-    for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
-        if (*o == nullptr) continue;
-        if (std::find(ins.begin(), ins.end(), *o) != ins.end()) return true;
-        if (std::find(outs.begin(), o, *o) != o) return true;
+// The memory that an argument names (none for a null or an empty one).
+struct Memory {
+    uintptr_t from = 0, to = 0;
+    Memory(const void* p, uint64_t bytes)
+        : from(reinterpret_cast<uintptr_t>(p)), to(p == nullptr || bytes == 0 ? 0 : from + bytes) {}
+    bool meets(const Memory& o) const { return from < o.to && o.from < to; }
+};
+typedef std::initializer_list<Memory> Memories;
+
+// Whether an output shares memory with an input or another output.
+bool aliased(Memories outs, Memories ins) {
+    for (const Memory* o = outs.begin(); o != outs.end(); ++o) {
+        const auto met = [o](const Memory& m) { return o->meets(m); };
+        if (std::any_of(ins.begin(), ins.end(), met) || std::any_of(outs.begin(), o, met))
+            return true;
     }
     return false;
 }
 
-// Of a workspace that may share its address with none of `others`.
-msel_status check_workspace(const void* ws, size_t have, size_t need, Pointers others) {
+// Of a workspace that shares memory with none of `others`.
+msel_status check_workspace(const void* ws, size_t have, size_t need, Memories others) {
     if (need == 0) return MSEL_OK;
     if (ws == nullptr || have < need) return MSEL_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return MSEL_ERR_ALIGN;
-    return aliased({ws}, others) ? MSEL_ERR_ALIAS : MSEL_OK;
+    return aliased({{ws, need}}, others) ? MSEL_ERR_ALIAS : MSEL_OK;
 }
 
 size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -78,6 +87,18 @@ msel_status check_lru(const msel_lru_args* a) {
         return MSEL_ERR_ALIGN;
     return MSEL_OK;
 }
+
+// Bytes of the recurrence's tensors.
+struct LruBytes {
+    uint64_t act, lam, state, chunks;
+    explicit LruBytes(const msel_lru_args* a) {
+        const uint64_t rows = static_cast<uint64_t>(a->batch) * static_cast<uint64_t>(a->dim);
+        act = rows * static_cast<uint64_t>(a->seqlen) * elem_bytes(a->dtype);
+        lam = static_cast<uint64_t>(a->dim) * 4;
+        state = rows * 4;
+        chunks = rows * static_cast<uint64_t>(msel_num_chunks(a->seqlen)) * 4;
+    }
+};
 
 // The parts of a workspace, in the order in which they lie.
 struct LruSpace {
@@ -132,14 +153,15 @@ bool logprob_aligned(const msel_logprob_args* a) {
            aligned(a->top_ids, 8);
 }
 
-// Bytes from the first logit of strided rows to the last.
-uintptr_t span_of(const msel_logprob_args* a, int64_t stride) {
-    return static_cast<uintptr_t>((a->rows - 1) * stride + a->vocab) * elem_bytes(a->dtype);
+// From the first logit of strided rows to the last, a value per row, and the ids.
+Memory logits_at(const msel_logprob_args* a, const void* p, int64_t stride) {
+    return {p, static_cast<uint64_t>((a->rows - 1) * stride + a->vocab) * elem_bytes(a->dtype)};
 }
-
-bool meet(const void* a, uintptr_t na, const void* b, uintptr_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
+Memory rows_at(const msel_logprob_args* a, const void* p) {
+    return {p, static_cast<uint64_t>(a->rows) * 4};
+}
+Memory ids_at(const msel_logprob_args* a) {
+    return {a->ids, static_cast<uint64_t>(a->rows) * (a->ids_64bit ? 8 : 4)};
 }
 
 size_t logprob_ws(const msel_logprob_args* a) {
@@ -177,6 +199,17 @@ msel_status check_mlp(const msel_gated_mlp_args* a) {
     return all_aligned({a->x, a->w_gate, a->w_up}, 16) ? MSEL_OK : MSEL_ERR_ALIGN;
 }
 
+// Bytes of the block's tensors.
+struct MlpBytes {
+    uint64_t x, w, out;
+    explicit MlpBytes(const msel_gated_mlp_args* a) {
+        const uint64_t e = elem_bytes(a->dtype), m = static_cast<uint64_t>(a->tokens);
+        x = m * static_cast<uint64_t>(a->dim) * e;
+        w = static_cast<uint64_t>(a->hidden) * static_cast<uint64_t>(a->dim) * e;
+        out = m * static_cast<uint64_t>(a->hidden) * e;
+    }
+};
+
 msel::MlpParams mlp_params(const msel_gated_mlp_args* a, void* ws) {
     msel::MlpParams p{};
     p.M = a->tokens;
@@ -200,14 +233,17 @@ msel_status msel_validate_lru_fwd(const msel_lru_args* a, const void* workspace,
     if (s != MSEL_OK) return s;
     if (a->out == nullptr) return MSEL_ERR_NULL;
     if (!aligned(a->out, 16) || !aligned(a->final_state, 4)) return MSEL_ERR_ALIGN;
+    const LruBytes n(a);
+    const Memory x{a->x, n.act}, ga{a->gate_a, n.act}, gx{a->gate_x, n.act}, lam{a->lam, n.lam};
+    const Memory h0{a->h0, n.state}, out{a->out, n.act}, chunks{a->chunk_states, n.chunks};
+    const Memory state{a->final_state, n.state};
     // final_state may be h0 itself: a row's state is read before it is written
-    const void* const state = a->final_state == a->h0 ? nullptr : a->final_state;
-    if (aliased({a->out, state, a->chunk_states}, {a->x, a->gate_a, a->gate_x, a->lam, a->h0}) ||
-        aliased({a->final_state}, {a->out, a->x, a->gate_a, a->gate_x, a->lam, a->chunk_states}))
+    const Memory from = a->final_state == a->h0 ? Memory(nullptr, 0) : h0;
+    if (aliased({out, chunks}, {x, ga, gx, lam, h0}) ||
+        aliased({state}, {x, ga, gx, lam, from, out, chunks}))
         return MSEL_ERR_ALIAS;
     return check_workspace(workspace, workspace_bytes, lru_space(a, false).all(),
-                           {a->x, a->gate_a, a->gate_x, a->lam, a->h0, a->out, a->final_state,
-                            a->chunk_states});
+                           {x, ga, gx, lam, h0, out, state, chunks});
 }
 
 size_t msel_lru_fwd_workspace_bytes(const msel_lru_args* a) {
@@ -238,13 +274,15 @@ msel_status msel_validate_lru_bwd(const msel_lru_args* a, const msel_lru_grads* 
     if (!all_aligned({g->dout, g->dx, g->dgate_a, g->dgate_x}, 16) ||
         !all_aligned({g->dfinal_state, g->dlam, g->dh0}, 4))
         return MSEL_ERR_ALIGN;
-    if (aliased({g->dx, g->dgate_a, g->dgate_x, g->dlam, g->dh0},
-                {a->x, a->gate_a, a->gate_x, a->lam, a->h0, a->chunk_states, g->dout,
-                 g->dfinal_state}))
+    const LruBytes n(a);
+    const Memory x{a->x, n.act}, ga{a->gate_a, n.act}, gx{a->gate_x, n.act}, lam{a->lam, n.lam};
+    const Memory h0{a->h0, n.state}, chunks{a->chunk_states, n.chunks}, dout{g->dout, n.act};
+    const Memory dfinal{g->dfinal_state, n.state}, dx{g->dx, n.act}, dga{g->dgate_a, n.act};
+    const Memory dgx{g->dgate_x, n.act}, dlam{g->dlam, n.lam}, dh0{g->dh0, n.state};
+    if (aliased({dx, dga, dgx, dlam, dh0}, {x, ga, gx, lam, h0, chunks, dout, dfinal}))
         return MSEL_ERR_ALIAS;
     return check_workspace(workspace, workspace_bytes, lru_space(a, true).all(),
-                           {a->x, a->gate_a, a->gate_x, a->lam, a->h0, a->chunk_states, g->dout,
-                            g->dfinal_state, g->dx, g->dgate_a, g->dgate_x, g->dlam, g->dh0});
+                           {x, ga, gx, lam, h0, chunks, dout, dfinal, dx, dga, dgx, dlam, dh0});
 }
 
 msel_status msel_lru_bwd(const msel_lru_args* a, const msel_lru_grads* g, void* workspace,
@@ -286,12 +324,15 @@ msel_status msel_validate_logprob_fwd(const msel_logprob_args* a, const void* wo
     if (a->top == 0 && a->logprob == nullptr && a->lse == nullptr && a->entropy == nullptr)
         return MSEL_ERR_NULL;  // nothing is asked for
     if (!logprob_aligned(a)) return MSEL_ERR_ALIGN;
-    if (aliased({a->logprob, a->lse, a->entropy, a->top_ids, a->top_logprobs},
-                {a->logits, a->ids}))
+    const uint64_t tops = static_cast<uint64_t>(a->rows) * static_cast<uint64_t>(a->top);
+    const Memory logits = logits_at(a, a->logits, a->stride), ids = ids_at(a);
+    const Memory logprob = rows_at(a, a->logprob), lse = rows_at(a, a->lse);
+    const Memory entropy = rows_at(a, a->entropy), top_ids{a->top_ids, tops * 8};
+    const Memory top_logprobs{a->top_logprobs, tops * 4};
+    if (aliased({logprob, lse, entropy, top_ids, top_logprobs}, {logits, ids}))
         return MSEL_ERR_ALIAS;
     return check_workspace(workspace, workspace_bytes, logprob_ws(a),
-                           {a->logits, a->ids, a->logprob, a->lse, a->entropy, a->top_ids,
-                            a->top_logprobs});
+                           {logits, ids, logprob, lse, entropy, top_ids, top_logprobs});
 }
 
 size_t msel_logprob_fwd_workspace_bytes(const msel_logprob_args* a) {
@@ -328,10 +369,12 @@ msel_status msel_validate_logprob_bwd(const msel_logprob_args* a, const msel_log
         return MSEL_ERR_ALIGN;
     // in place, a row's gradient lies where the row lies; else they share nothing
     if (g->dlogits == a->logits && g->dstride != a->stride) return MSEL_ERR_SHAPE;
-    if (g->dlogits != a->logits &&
-        meet(a->logits, span_of(a, a->stride), g->dlogits, span_of(a, g->dstride)))
+    const Memory dlogits = logits_at(a, g->dlogits, g->dstride);
+    if (g->dlogits != a->logits && dlogits.meets(logits_at(a, a->logits, a->stride)))
         return MSEL_ERR_ALIAS;
-    if (aliased({g->dlogits}, {a->ids, a->lse, a->entropy, g->dlogprob, g->dlse, g->dentropy}))
+    if (aliased({dlogits}, {ids_at(a), rows_at(a, a->lse), rows_at(a, a->entropy),
+                            rows_at(a, g->dlogprob), rows_at(a, g->dlse),
+                            rows_at(a, g->dentropy)}))
         return MSEL_ERR_ALIAS;
     return MSEL_OK;
 }
@@ -357,9 +400,11 @@ msel_status msel_validate_gated_mlp_fwd(const msel_gated_mlp_args* a, const void
     if (s != MSEL_OK) return s;
     if (a->out == nullptr) return MSEL_ERR_NULL;
     if (!aligned(a->out, 16)) return MSEL_ERR_ALIGN;
-    if (aliased({a->out}, {a->x, a->w_gate, a->w_up})) return MSEL_ERR_ALIAS;
+    const MlpBytes n(a);
+    const Memory x{a->x, n.x}, wg{a->w_gate, n.w}, wu{a->w_up, n.w}, out{a->out, n.out};
+    if (aliased({out}, {x, wg, wu})) return MSEL_ERR_ALIAS;
     return check_workspace(workspace, workspace_bytes, msel_gated_mlp_fwd_workspace_bytes(a),
-                           {a->x, a->w_gate, a->w_up, a->out});
+                           {x, wg, wu, out});
 }
 
 size_t msel_gated_mlp_fwd_workspace_bytes(const msel_gated_mlp_args* a) {
@@ -391,10 +436,12 @@ msel_status msel_validate_gated_mlp_bwd(const msel_gated_mlp_args* a,
         (g->dx == nullptr && g->dw_gate == nullptr))
         return MSEL_ERR_NULL;
     if (!all_aligned({g->dout, g->dx, g->dw_gate, g->dw_up}, 16)) return MSEL_ERR_ALIGN;
-    if (aliased({g->dx, g->dw_gate, g->dw_up}, {a->x, a->w_gate, a->w_up, g->dout}))
-        return MSEL_ERR_ALIAS;
+    const MlpBytes n(a);
+    const Memory x{a->x, n.x}, wg{a->w_gate, n.w}, wu{a->w_up, n.w}, dout{g->dout, n.out};
+    const Memory dx{g->dx, n.x}, dwg{g->dw_gate, n.w}, dwu{g->dw_up, n.w};
+    if (aliased({dx, dwg, dwu}, {x, wg, wu, dout})) return MSEL_ERR_ALIAS;
     return check_workspace(workspace, workspace_bytes, msel_gated_mlp_bwd_workspace_bytes(a),
-                           {a->x, a->w_gate, a->w_up, g->dout, g->dx, g->dw_gate, g->dw_up});
+                           {x, wg, wu, dout, dx, dwg, dwu});
 }
 
 msel_status msel_gated_mlp_bwd(const msel_gated_mlp_args* a, const msel_gated_mlp_grads* g,

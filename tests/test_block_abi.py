@@ -331,9 +331,98 @@ def test_tensors_of_the_host_are_refused():
                                             (1, (1 << 27) + 1, SHAPE), (9, 1 << 27, SHAPE)])
 def test_lru_channels_that_a_grid_holds(lib, batch, dim, code):
     a = _lru(batch=batch, dim=dim, seqlen=1)
-    g = _lib.LruGrads(*[_addr() for _ in range(7)])
+    g = _lib.LruGrads()
+    fields = [(a, f) for f, _ in a._fields_[6:]] + [(g, f) for f, _ in g._fields_]
+    for k, (s, f) in enumerate(fields):
+        setattr(s, f, (k + 1) << 40)
     need = lib.msel_lru_bwd_workspace_bytes(ctypes.byref(a))
     assert (need > 0) == (code == OK)
-    ws = _addr()
+    ws = 1 << 46
     assert lib.msel_validate_lru_fwd(ctypes.byref(a), ws, 1 << 50) == code
     assert lib.msel_validate_lru_bwd(ctypes.byref(a), ctypes.byref(g), ws, 1 << 50) == code
+
+
+# ---- memory that is shared in part -------------------------------------------------------------
+
+def _first_and_last(base, size, other, step):
+    """Addresses at which a tensor of `other` bytes shares the first or the last `step` bytes of
+    one of `size` bytes at `base`, and the nearest ones at which it does not."""
+    return (base - other + step, base + size - step), (base - other, base + size)
+
+
+def _check_parts(call, s, outs, tensors, step):
+    """Every output over a part of every other tensor is refused, and right beside it is not."""
+    for out, n_out in outs.items():
+        kept = getattr(s[out], out)
+        for name, n in tensors.items():
+            if name == out:
+                continue
+            near, beside = _first_and_last(getattr(s[name], name), n, n_out, step)
+            for at in near:
+                setattr(s[out], out, at)
+                assert call() == ALIAS, (out, name)
+            for at in beside:
+                setattr(s[out], out, at)
+                assert call() == OK, (out, name)
+        setattr(s[out], out, kept)
+    assert call() == OK
+
+
+def test_lru_shared_in_part(lib):
+    a, ws = _lru(batch=4, dim=16, seqlen=512, dtype=0), _addr()
+    act, lam, state = 4 * 16 * 512 * 4, 16 * 4, 4 * 16 * 4
+    acts, ins = ("x", "gate_a", "gate_x"), {}
+    ins = {**dict.fromkeys(acts, act), "lam": lam, "h0": state}
+    outs = {"out": act, "final_state": state, "chunk_states": state}
+    _check_parts(lambda: lib.msel_validate_lru_fwd(ctypes.byref(a), ws, 1 << 24),
+                 dict.fromkeys([*ins, *outs], a), outs, {**ins, **outs}, 16)
+    a.final_state = a.h0
+    assert lib.msel_validate_lru_fwd(ctypes.byref(a), ws, 1 << 24) == OK
+    g = _lib.LruGrads(*[_addr() for _ in range(7)])
+    ins = {**ins, "chunk_states": state, "dout": act, "dfinal_state": state}
+    outs = {"dx": act, "dgate_a": act, "dgate_x": act, "dlam": lam, "dh0": state}
+    where = {k: g if hasattr(g, k) else a for k in [*ins, *outs]}
+
+    def call():
+        return lib.msel_validate_lru_bwd(ctypes.byref(a), ctypes.byref(g), ws, 1 << 24)
+    _check_parts(call, where, outs, {**ins, **outs}, 16)
+    need = lib.msel_lru_bwd_workspace_bytes(ctypes.byref(a))
+    for t in where:
+        kept, ws = ws, getattr(where[t], t) - need + 256 & ~255
+        assert call() == ALIAS, t
+        ws = kept
+
+
+def test_logprob_shared_in_part(lib):
+    rows, vocab, stride, top = 64, 1000, 1024, 4
+    a = _lib.LogprobArgs(1, vocab, rows, stride, 1, 0, top, 1.0, *[_addr() for _ in range(7)])
+    span, row = ((rows - 1) * stride + vocab) * 2, rows * 4
+    ins = {"logits": span, "ids": row}
+    outs = {"logprob": row, "lse": row, "entropy": row, "top_ids": row * top * 2,
+            "top_logprobs": row * top}
+    _check_parts(lambda: lib.msel_validate_logprob_fwd(ctypes.byref(a), None, 0),
+                 dict.fromkeys([*ins, *outs], a), outs, {**ins, **outs}, 8)
+    g = _lib.LogprobGrads(*[_addr() for _ in range(4)], stride)
+    ins = {**ins, "lse": row, "entropy": row, "dlogprob": row, "dlse": row, "dentropy": row}
+    where = {k: g if hasattr(g, k) else a for k in [*ins, "dlogits"]}
+
+    def call():
+        return lib.msel_validate_logprob_bwd(ctypes.byref(a), ctypes.byref(g))
+    _check_parts(call, where, {"dlogits": span}, {**ins, "dlogits": span}, 8)
+    g.dlogits = a.logits
+    assert call() == OK
+
+
+def test_gated_mlp_shared_in_part(lib):
+    tokens, dim, hidden = 64, 128, 256
+    a, ws = _lib.GatedMlpArgs(1, dim, hidden, 1, tokens, 0, 0, *[_addr() for _ in range(4)]), _addr()
+    ins = {"x": tokens * dim * 2, "w_gate": hidden * dim * 2, "w_up": hidden * dim * 2}
+    outs = {"out": tokens * hidden * 2}
+    _check_parts(lambda: lib.msel_validate_gated_mlp_fwd(ctypes.byref(a), ws, 1 << 24),
+                 dict.fromkeys([*ins, *outs], a), outs, {**ins, **outs}, 16)
+    g = _lib.GatedMlpGrads(*[_addr() for _ in range(4)])
+    outs = {"dx": ins["x"], "dw_gate": ins["w_gate"], "dw_up": ins["w_up"]}
+    ins["dout"] = tokens * hidden * 2
+    where = {k: g if hasattr(g, k) else a for k in [*ins, *outs]}
+    _check_parts(lambda: lib.msel_validate_gated_mlp_bwd(ctypes.byref(a), ctypes.byref(g), ws,
+                                                         1 << 24), where, outs, {**ins, **outs}, 16)
