@@ -828,7 +828,8 @@ typedef struct {
 } msel_gated_mlp_args;
 
 /* With G = x Wg^T and U = x Wu^T formed again: dG = dout * U * act'(G), dU = dout * act(G), both
- * rounded to `dtype` (they are operands of products), and
+ * rounded to `dtype` (they are operands of products; gradients of few elements keep what is left
+ * as a second number), and
  *   dx = dG Wg + dU Wu,  dw_gate = dG^T x,  dw_up = dU^T x. */
 typedef struct {
     const void *dout;       /* required                                                    */

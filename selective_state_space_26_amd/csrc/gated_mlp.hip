@@ -33,6 +33,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kStageBytes = 128;  // of k per stage
 constexpr int kRing = 2;          // stages in LDS
 constexpr int kSteps = kStageBytes / 32;
+// fp32: stages whose products are summed before their sum is added to another.  An MFMA adds 2 products
+// and rounds, and a row of 2048 such steps was off by up to 2.4 times as much as parts of 256 are (2
+// tokens of 1998: 1.1e-6 of the result).  777 x 1000 -> 2603, backward: 308 us, 306 without.
+constexpr int kPartStages = 16;
 
 template <typename T>
 constexpr int kStageK = kStageBytes / static_cast<int>(sizeof(T));
@@ -94,7 +98,8 @@ struct ProductParams {
     const void* b1;  // the other weight
     int64_t lda, ldb;
     int64_t wa, wb;  // elements of a row of A and B that may be read, where they lie by rows of k
-    int stages, half;  // stages in all, and of one part of B
+    int stages, half;  // stages in all, and of one part: B0, B1, then both with the low parts of A
+    int64_t low;       // kWeights: elements from A to its low parts
     int splits, per_split;  // blocks that share a tile's stages, and stages of each
     void* c0;        // rows [0, rows0) of C
     void* c1;        // rows from `split` on; those between go nowhere
@@ -102,6 +107,7 @@ struct ProductParams {
     float* part;       // not null: C goes there, [splits][M][N]
     const void* dout;  // kGateGrad: [M, N]
     int hp;            // kGateGrad: dG in columns [0, hp) of C, dU in [hp, 2 hp)
+    int with_low;      // kGateGrad: what their rounding left in [2 hp, 4 hp)
     int gelu;
     int tm, tn;        // tiles
 };
@@ -304,23 +310,55 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     }
     const int64_t step_a = kRowsA ? kStageK<T> * p.lda * static_cast<int64_t>(sizeof(T)) : kStageBytes;
     const int64_t step_b = kRowsB ? kStageK<T> * p.ldb * static_cast<int64_t>(sizeof(T)) : kStageBytes;
-    // rows of k that stage k has, where it has not all
-    const auto rows_of = [&](int k) -> int {
-        const int64_t left = p.K - static_cast<int64_t>(k < p.half ? k : k - p.half) * kStageK<T>;
-        return left < kStageK<T> ? static_cast<int>(left) : kStageK<T>;
+    // where a stage's operands are, in bytes from the first one's, and the rows of k that its part (of
+    // up to 4) has from it on
+    struct Stage {
+        int64_t a, b, left;
+        int part;
     };
-    // loads [i0, i1) of stage k
-    const auto load_part = [&](int k, int buf, int i0, int i1) {
-        const int kb = k < p.half ? k : k - p.half;
-        const int64_t other = k < p.half ? 0
-                                         : static_cast<const char*>(p.b1) -
-                                               static_cast<const char*>(p.b0);
-        const int rows = rows_of(k);
+    const auto begin_part = [&](Stage& g) {
+        if constexpr (KIND == Kind::kInput)  // A goes on, B is the other weight
+            g.b = (g.part & 1) != 0 ? static_cast<const char*>(p.b1) - static_cast<const char*>(p.b0) : 0;
+        if constexpr (KIND == Kind::kWeights) {  // A's low parts, B again
+            g.a = g.part * p.low * static_cast<int64_t>(sizeof(T));
+            g.b = 0;
+        }
+        g.left = p.K;
+    };
+    const auto advance = [&](Stage& g) {
+        g.a += step_a;
+        g.b += step_b;
+        if constexpr (kRowsB) {
+            g.left -= kStageK<T>;
+            if (g.left <= 0) {
+                ++g.part;
+                begin_part(g);
+            }
+        }
+    };
+    const auto stage_at = [&](int k) {
+        Stage g{k * step_a, k * step_b, 0, 0};
+        if constexpr (kRowsB) {
+            g.part = k / p.half;
+            begin_part(g);
+            k -= g.part * p.half;
+            if constexpr (kRowsA) g.a += k * step_a;
+            g.b += k * step_b;
+            g.left -= k * static_cast<int64_t>(kStageK<T>);
+        }
+        return g;
+    };
+    const auto rows_of = [&](const Stage& g) -> int {
+        return kRowsB && g.left < kStageK<T> ? static_cast<int>(g.left) : kStageK<T>;
+    };
+    // loads [i0, i1) of a stage
+    const auto load_part = [&](const Stage& stage, int buf, int i0, int i1) {
+        const int rows = rows_of(stage);
 #pragma unroll
         for (int i = 0; i < LA + LB; ++i) {
             if (i < i0 || i >= i1) continue;
             const bool a = i < LA;
-            const char* g = src[i] + (a ? k * step_a : kb * step_b + (kDual ? 0 : other));
+            const char* g = src[i] + (a ? stage.a : stage.b);
             if ((a ? kRowsA : kRowsB) && rows < kStageK<T>) {  // uniform
                 const int r = a ? (i * kThreads + tid) / OpA::kChunks
                                 : ((i - LA) * kThreads + tid) / OpB::kChunks;
@@ -338,6 +376,21 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    // fp32: the sums of the stages before the last kPartStages (the largest tiles have no registers for
+    // them)
+    constexpr bool kParts = sizeof(T) == 4 && MI < 4;
+    f32x16 sum[kParts ? MI : 1][2];
+    const auto add_part = [&](bool first_one) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    sum[i][j][e] = first_one ? acc[i][j][e] : sum[i][j][e] + acc[i][j][e];
+                    acc[i][j][e] = 0.0f;
+                }
+    };
 
     // kGateGrad: dout's tile in the order in which the results go out; loaded before the product
     // where the registers for it are there (32 in bf16)
@@ -360,10 +413,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
 
     const int first = split * p.per_split, last = min(p.stages, first + p.per_split);
     // waits for stage k, which has `after` loads behind it; rows of k past the end become 0
-    const auto enter_stage = [&](int k, auto after) {
+    const auto enter_stage = [&](int k, int rows, auto after) {
         barrier_after<decltype(after)::value>();
-        if (!kRowsB || rows_of(k) == kStageK<T>) return;  // uniform
-        const int rows = rows_of(k);
+        if (!kRowsB || rows == kStageK<T>) return;  // uniform
         const u32x4 zero = {0, 0, 0, 0};
         char* at = lds + ((k - first) & 1) * kStage;
         if (kRowsA)
@@ -381,12 +433,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
 #pragma unroll
         for (int j = 0; j < 2; ++j) fb[to][j] = OpB::read(sa + OpA::kBytes, wn * 2 + j, s, lane);
     };
-    load_part(first, 0, 0, LA + LB);
+    Stage loading = stage_at(first);  // the last stage whose loads are out
+    const int first_rows = rows_of(loading);
+    load_part(loading, 0, 0, LA + LB);
     if (first + 1 < last) {
-        load_part(first + 1, 1, 0, LA + LB);
-        enter_stage(first, std::integral_constant<int, LA + LB>());
+        advance(loading);
+        load_part(loading, 1, 0, LA + LB);
+        enter_stage(first, first_rows, std::integral_constant<int, LA + LB>());
     } else {
-        enter_stage(first, std::integral_constant<int, 0>());
+        enter_stage(first, first_rows, std::integral_constant<int, 0>());
     }
     read_step(first, 0, 0);
     // A stage's loads go out between the MFMAs, half of them in the step before it is entered and
@@ -400,9 +455,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
             if (s + 1 < kSteps) {
                 read_step(k, s + 1, cur ^ 1);
             } else if (k + 1 < last) {
-                enter_stage(k + 1, std::integral_constant<int, 0>());
+                enter_stage(k + 1, rows_of(loading), std::integral_constant<int, 0>());
                 read_step(k + 1, 0, cur ^ 1);
             }
+            if (s + 1 == kSteps && k + 2 < last) advance(loading);
             __builtin_amdgcn_sched_barrier(0);  // the reads first, the MFMAs over their latency
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
@@ -410,11 +466,21 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
                 for (int j = 0; j < 2; ++j)
                     mfma_step(static_cast<const T*>(nullptr), fb[cur][j], fa[cur][i], acc[i][j]);
                 if (s + 1 == kSteps && k + 2 < last)
-                    load_part(k + 2, (k - first) & 1, i * kPer, (i + 1) * kPer);
+                    load_part(loading, (k - first) & 1, i * kPer, (i + 1) * kPer);
                 if (s == 0 && k > first && k + 1 < last)
-                    load_part(k + 1, (k + 1 - first) & 1, kHalf + i * kPer, kHalf + (i + 1) * kPer);
+                    load_part(loading, (k + 1 - first) & 1, kHalf + i * kPer, kHalf + (i + 1) * kPer);
                 __builtin_amdgcn_sched_barrier(0);
             }
+        }
+        if constexpr (kParts)
+            if ((k - first) % kPartStages == kPartStages - 1) add_part(k - first < kPartStages);
+    }
+    if constexpr (kParts) {
+        if (last - first >= kPartStages) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] += sum[i][j];
         }
     }
     __syncthreads();  // the ring becomes the tile on its way out
@@ -467,7 +533,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
                                  &dout[i], 16);
             }
             __syncthreads();
-            // dG over dout, a lane's own columns; dU waits where U was
+            // dG over dout, a lane's own columns; dU waits where U was (and dG where G was, for its
+            // low part: the largest tiles have no registers for that)
+            constexpr bool kLow = sizeof(T) == 2 && MI < 4;
             with_act(p.gelu, [&](auto gelu) {
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
@@ -493,18 +561,40 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
                     }
                     Tile::put(lds, r0 + i * 32, col, g);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[i][1][e] = u[e];
+                    for (int e = 0; e < 16; ++e) {
+                        if constexpr (kLow) acc[i][0][e] = g[e];
+                        acc[i][1][e] = u[e];
+                    }
                 }
             });
             send(Tile(), to(0, p.hp));
-            __syncthreads();
+            const auto put_all = [&](auto j, auto value) {
+                __syncthreads();
 #pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                float u[16];
-                values(acc[i][1], u);
-                Tile::put(lds, r0 + i * 32, col, u);
-            }
+                for (int i = 0; i < MI; ++i) {
+                    float v[16];
+                    values(acc[i][j.value], v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = value(v[e]);
+                    Tile::put(lds, r0 + i * 32, col, v);
+                }
+            };
+            const std::integral_constant<int, 0> dg;
+            const std::integral_constant<int, 1> du;
+            put_all(du, [](float v) { return v; });
             send(Tile(), to(p.hp, p.hp));
+            if constexpr (kLow) {
+                if (p.with_low) {  // uniform
+                    const auto rest = [](float v) {
+                        const float r = v - bf16lo(pack_bf16(v, 0.0f));
+                        return r == r ? r : 0.0f;  // of an infinity nothing
+                    };
+                    put_all(dg, rest);
+                    send(Tile(), to(2 * p.hp, p.hp));
+                    put_all(du, rest);
+                    send(Tile(), to(3 * p.hp, p.hp));
+                }
+            }
         }
     } else {
         // fp32 in two halves: the first 32 of each wavefront's 64 columns, then the others
@@ -720,18 +810,19 @@ struct ProductPlan {
 };
 
 // The cheapest by a model in cycles: the blocks of a CU take turns on its matrix cores, at the share
-// of the peak that such tiles reach (256 x 256: 2.2 us a stage, 128 x 128: 0.84, 64 x 128: 0.42), but
-// a stage takes no less than the way of its loads, which the blocks that a CU holds share; then a
-// fixed part per block, and for split stages the parts' way through the last-level cache.  16384 x
-// 768 by 4096: 256 x 256 without a split 140 us, 128 x 128 162; 1024 rows: 8 parts 20 us, one 60.
-ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf16) {
+// of the peak that such tiles reach (below, fitted to measured products), but a stage takes no less
+// than the way of its loads, which the blocks that a CU holds share; then a fixed part per block, and
+// for split stages the parts' way through the last-level cache.  16384 x 768 by 4096: 256 x 256
+// without a split 140 us, 128 x 128 162; 1024 rows: 8 parts 20 us, one 60.
+ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf16,
+                         int first_tile = 0) {
     constexpr int rows_of[] = {256, 128, 64}, cols_of[] = {256, 128, 128}, held[] = {1, 2, 3};
     constexpr double share16[] = {0.8, 0.52, 0.5}, share32[] = {0.74, 0.74, 0.7};
     constexpr int kCus = 256;
     constexpr double kLoads = 2000.0;
     ProductPlan best{1, 1};
     double least = 0.0;
-    for (int t = 0; t < 3; ++t) {
+    for (int t = first_tile; t < 3; ++t) {
         const int64_t tiles = over(M, rows_of[t]) * over(cols, cols_of[t]);
         const double area = rows_of[t] * cols_of[t];
         const double stage = area * (bf16 ? 64 / 2048.0 / share16[t] : 32 / 128.0 / share32[t]);
@@ -794,10 +885,16 @@ hipError_t launch_split(ProductParams p, const ProductPlan& q, float* part, hipS
     return hipGetLastError();
 }
 
+// Gradients of so few elements take dG and dU in two bf16 parts each, as good as unrounded: over few
+// elements the roundings do not average out (1 x 160 -> 4792: dx is off by 1.65 times what its own
+// rounding is, by 1.41 times in large ones).  8 x 768 -> 2048: 36 us, 29 with one part.
+constexpr int64_t kFew = 4096;
+
 // Parts of the workspace: offsets in bytes, absent parts take none.
 struct MlpSpace {
     int64_t dp, hp;  // width and hidden width in whole stages
     size_t x = 0, wg = 0, wu = 0, dgu = 0, part = 0, all = 0;
+    int parts_of = 1;  // bf16 numbers that dG and dU are held in, each
     ProductPlan gate, input, weights;
     MlpSpace(const MlpParams& p, bool bf16, bool bwd) {
         const size_t elem = bf16 ? 2 : 4;
@@ -814,13 +911,14 @@ struct MlpSpace {
             wg = take(static_cast<size_t>(p.F * dp) * elem);
             wu = take(static_cast<size_t>(p.F * dp) * elem);
         }
+        if (bwd && bf16 && p.M * std::min(p.D, p.F) <= kFew) parts_of = 2;
         gate = plan_product(bwd ? Kind::kGateGrad : Kind::kGate, p.M, 2 * (bwd ? hp : p.F),
-                            static_cast<int>(dp / q), bf16);
+                            static_cast<int>(dp / q), bf16, parts_of > 1 ? 1 : 0);
         if (!bwd) return;
-        dgu = take(static_cast<size_t>(p.M * 2 * hp) * elem);
-        input = plan_product(Kind::kInput, p.M, p.D, static_cast<int>(2 * hp / q), bf16);
+        dgu = take(static_cast<size_t>(p.M * 2 * parts_of * hp) * elem);
+        input = plan_product(Kind::kInput, p.M, p.D, static_cast<int>(2 * parts_of * hp / q), bf16);
         weights = plan_product(Kind::kWeights, hp + p.F, p.D,
-                               static_cast<int>(over(p.M, q)), bf16);
+                               static_cast<int>(parts_of * over(p.M, q)), bf16);
         size_t parts = 0;  // of one product at a time
         if (input.splits > 1) parts = static_cast<size_t>(input.splits) * p.M * p.D;
         if (weights.splits > 1)
@@ -908,8 +1006,9 @@ hipError_t backward(const MlpParams& p, hipStream_t stream) {
     const Padded o = padded<T>(p, w, stream);
     ProductParams q = gate_params<T>(p, w, o);
     q.c0 = ws + w.dgu;
-    q.ldc = 2 * w.hp;
+    q.ldc = 2 * w.parts_of * w.hp;
     q.hp = static_cast<int>(w.hp);
+    q.with_low = w.parts_of > 1;
     q.dout = p.dout;
     hipError_t e = launch_product<T, Kind::kGateGrad>(q, w.gate, stream);
     if (e != hipSuccess) return e;
@@ -919,9 +1018,9 @@ hipError_t backward(const MlpParams& p, hipStream_t stream) {
         r.N = p.D;
         r.K = p.F;
         r.half = static_cast<int>(w.hp / kStageK<T>);
-        r.stages = 2 * r.half;
+        r.stages = 2 * w.parts_of * r.half;
         r.a = ws + w.dgu;
-        r.lda = 2 * w.hp;
+        r.lda = 2 * w.parts_of * w.hp;
         r.b0 = o.wg;
         r.b1 = o.wu;
         r.ldb = r.wb = w.dp;
@@ -937,9 +1036,11 @@ hipError_t backward(const MlpParams& p, hipStream_t stream) {
         r.split = w.hp;
         r.N = p.D;
         r.K = p.M;
-        r.stages = r.half = static_cast<int>(over(p.M, kStageK<T>));
+        r.half = static_cast<int>(over(p.M, kStageK<T>));
+        r.stages = w.parts_of * r.half;
         r.a = ws + w.dgu;
-        r.lda = r.wa = 2 * w.hp;
+        r.wa = r.low = 2 * w.hp;
+        r.lda = 2 * w.parts_of * w.hp;
         r.b0 = r.b1 = o.x;
         r.ldb = r.wb = w.dp;
         r.ldc = p.D;

@@ -187,3 +187,44 @@ def test_gates_far_out(act, size):
         if v < 3e38:
             assert g[k][0].item() == pytest.approx(v, rel=1e-6)
         assert abs(g[k][1].item()) < 1e-7 * max(1.0, size)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("shape", [(1, 160, 4792), (4, 2088, 40), (7, 128, 40), (31, 129, 130),
+                                   (70, 58, 300), (130, 1, 700), (4000, 300, 1)])
+def test_gradients_of_few_elements_are_as_good_as_unrounded(shape, act):
+    """dG and dU as two bf16 numbers each: the first is off by 2^-8 of the value at most, the second
+    is what the first left, off by 2^-8 of that, so that 2^-16 is left of the value (256 roundoffs
+    of fp32)."""
+    log(f"mlp few elements {shape} {act}")
+    x, wg, wu = _inputs(shape, "bf16")
+    dout = normal((shape[0], shape[2]), "bf16", 4)
+    r = msel.msel_gated_mlp_bwd(x, wg, wu, dout, act)
+    vx, vg, vu, vd = (values(t) for t in (x, wg, wu, dout))
+    ref = block.mlp_bwd(vx, vg, vu, vd, act == "gelu")
+    g, u, eg, eu = _products(vx, vg, vu)
+    a, s = block.act(g, act == "gelu")
+    near = 4 * np.abs(g) + 4 * np.abs(g) ** 3 + 16
+    adg, adu = np.abs(ref["dg"]), np.abs(ref["du"])
+    edg = np.abs(vd) * (np.abs(u) * (1.2 * eg + near * (np.abs(s) + 1)) + np.abs(s) * eu) + 256 * adg
+    edu = np.abs(vd) * (1.2 * eg + np.abs(a) * near) + 256 * adu
+    # the sums have twice the terms; the second ones are 2^-8 of the first
+    within("dx", r["dx"], ref["dx"], edg @ np.abs(vg) + edu @ np.abs(vu)
+           + sums(4 * shape[2]) * (adg @ np.abs(vg) + adu @ np.abs(vu)))
+    k = sums(2 * shape[0])
+    within("dw_gate", r["dw_gate"], ref["dwg"], (edg + k * adg).T @ np.abs(vx))
+    within("dw_up", r["dw_up"], ref["dwu"], (edu + k * adu).T @ np.abs(vx))
+
+
+@pytest.mark.parametrize("tokens", [60, 300])
+def test_long_sums_in_fp32(tokens):
+    """A sum of 4096 products in parts of 512, two products a rounding.  A part's roundings are u / sqrt 3
+    of a running sum that grows as a random walk: sqrt(256 / 2) of them, 6.5 u of the part, and so of the
+    whole, whose 8 parts' roundings add in squares; 1.2 u for adding them.  Two such factors and
+    some roundings of the activation: 10 u of the result's norm.  (In one row it is 27.)"""
+    x, wg, wu = _inputs((tokens, 4096, 200), "f32")
+    out = msel.msel_gated_mlp_fwd(x, wg, wu)
+    X, G, U = x.double(), wg.double(), wu.double()
+    g = X @ G.T
+    ref = g * torch.sigmoid(g) * (X @ U.T)
+    assert float((out.double() - ref).norm() / ref.norm()) <= 14 * U32
