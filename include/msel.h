@@ -844,7 +844,7 @@ msel_status msel_validate_gated_mlp_bwd(const msel_gated_mlp_args *args,
                                         const msel_gated_mlp_grads *grads, const void *workspace,
                                         size_t workspace_bytes);
 /* Bytes of workspace the two entry points need (0 for invalid sizes): copies of operands whose
- * rows are no multiple of a tile's, and in the backward of transposed ones and of dG and dU. */
+ * rows are no multiple of 16 bytes, parts of split sums, and in the backward dG and dU. */
 size_t msel_gated_mlp_fwd_workspace_bytes(const msel_gated_mlp_args *args);
 size_t msel_gated_mlp_bwd_workspace_bytes(const msel_gated_mlp_args *args);
 /* Both deterministic; the workspace is 256-byte aligned. */

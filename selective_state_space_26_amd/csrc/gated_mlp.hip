@@ -15,7 +15,7 @@
 // backward's products over the hidden width and over the tokens read their operands by rows of k, as
 // they lie in memory; LDS turns them (the transposing reads of gfx950).
 //
-// Operands whose rows are no multiple of a stage are copied into padded rows first.
+// Operands whose rows are no multiple of 16 bytes, or below a stage, are copied into padded rows first.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -35,7 +35,7 @@ constexpr int kRing = 2;          // stages in LDS
 constexpr int kSteps = kStageBytes / 32;
 // fp32: stages whose products are summed before their sum is added to another.  An MFMA adds 2 products
 // and rounds, and a row of 2048 such steps was off by up to 2.4 times as much as parts of 256 are (2
-// tokens of 1998: 1.1e-6 of the result).  777 x 1000 -> 2603, backward: 308 us, 306 without.
+// tokens of 1998: 1.1e-6 of the result).  They cost 0.5% of a product's time.
 constexpr int kPartStages = 16;
 
 template <typename T>
@@ -69,6 +69,11 @@ __device__ __forceinline__ void act_grad(float z, float& v, float& slope) {
     const float w = v - v * s;
     // w is 0 long before the polynomial beside it leaves fp32's range
     slope = GELU ? fmaf(w, kTwoC * fminf(fmaf(0.134145f * z, z, 1.0f), 1e30f), s) : w + s;
+}
+// What a value's rounding to bf16 leaves (nothing of an infinity).
+__device__ __forceinline__ float rest_of(float v) {
+    const float r = v - bf16lo(pack_bf16(v, 0.0f));
+    return r == r ? r : 0.0f;
 }
 // f(GELU as a type): one branch around a whole epilogue, not two activations per element.
 template <typename Fn>
@@ -104,7 +109,7 @@ struct ProductParams {
     void* c0;        // rows [0, rows0) of C
     void* c1;        // rows from `split` on; those between go nowhere
     int64_t rows0, split, ldc;
-    float* part;       // not null: C goes there, [splits][M][N]
+    float* part;       // not null: C goes there, [splits][M][N], or G and U, [splits][2][M][N]
     const void* dout;  // kGateGrad: [M, N]
     int hp;            // kGateGrad: dG in columns [0, hp) of C, dU in [hp, 2 hp)
     int with_low;      // kGateGrad: what their rounding left in [2 hp, 4 hp)
@@ -325,44 +330,51 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
         }
         g.left = p.K;
     };
+    // the last stage of rows of consecutive k ends with the rows: what it has in common with the one
+    // before becomes 0 in LDS
+    const auto end_row = [&](Stage& g) {
+        if (g.left < kStageK<T>) g.a = g.b = p.K * static_cast<int64_t>(sizeof(T)) - kStageBytes;
+    };
     const auto advance = [&](Stage& g) {
         g.a += step_a;
         g.b += step_b;
-        if constexpr (kRowsB) {
-            g.left -= kStageK<T>;
-            if (g.left <= 0) {
-                ++g.part;
-                begin_part(g);
-            }
+        g.left -= kStageK<T>;
+        if constexpr (kDual) {
+            end_row(g);
+        } else if (g.left <= 0) {
+            ++g.part;
+            begin_part(g);
         }
     };
     const auto stage_at = [&](int k) {
-        Stage g{k * step_a, k * step_b, 0, 0};
-        if constexpr (kRowsB) {
+        Stage g{k * step_a, k * step_b, p.K, 0};
+        if constexpr (!kDual) {
             g.part = k / p.half;
             begin_part(g);
             k -= g.part * p.half;
             if constexpr (kRowsA) g.a += k * step_a;
             g.b += k * step_b;
-            g.left -= k * static_cast<int64_t>(kStageK<T>);
         }
+        g.left -= k * static_cast<int64_t>(kStageK<T>);
+        if constexpr (kDual) end_row(g);
         return g;
     };
-    const auto rows_of = [&](const Stage& g) -> int {
-        return kRowsB && g.left < kStageK<T> ? static_cast<int>(g.left) : kStageK<T>;
+    // k that a stage has: elements of its rows (whole chunks), or rows
+    const auto size_of = [&](const Stage& g) -> int {
+        return g.left < kStageK<T> ? static_cast<int>(g.left) : kStageK<T>;
     };
     // loads [i0, i1) of a stage
     const auto load_part = [&](const Stage& stage, int buf, int i0, int i1) {
-        const int rows = rows_of(stage);
+        [[maybe_unused]] const int size = size_of(stage);
 #pragma unroll
         for (int i = 0; i < LA + LB; ++i) {
             if (i < i0 || i >= i1) continue;
             const bool a = i < LA;
             const char* g = src[i] + (a ? stage.a : stage.b);
-            if ((a ? kRowsA : kRowsB) && rows < kStageK<T>) {  // uniform
+            if ((a ? kRowsA : kRowsB) && size < kStageK<T>) {  // uniform
                 const int r = a ? (i * kThreads + tid) / OpA::kChunks
                                 : ((i - LA) * kThreads + tid) / OpB::kChunks;
-                if (r >= rows) g -= (r - rows + 1) * (a ? p.lda : p.ldb) * static_cast<int64_t>(sizeof(T));
+                if (r >= size) g -= (r - size + 1) * (a ? p.lda : p.ldb) * static_cast<int64_t>(sizeof(T));
             }
             const int at = buf * kStage + (i * kThreads + wave * 64) * 16;
             __builtin_amdgcn_global_load_lds((GlobalVoid*)g, (LdsVoid*)(lds + at), 16, 0, 0);
@@ -409,20 +421,27 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
                 dout[i] = ld_part<T, VE>(row + n, p.N - n);
         }
     };
-    if constexpr (KIND == Kind::kGateGrad && sizeof(T) == 2) load_dout();
+    if constexpr (KIND == Kind::kGateGrad && sizeof(T) == 2)
+        if (p.part == nullptr) load_dout();
 
     const int first = split * p.per_split, last = min(p.stages, first + p.per_split);
-    // waits for stage k, which has `after` loads behind it; rows of k past the end become 0
-    const auto enter_stage = [&](int k, int rows, auto after) {
+    // waits for stage k, which has `after` loads behind it; what it has too much becomes 0
+    const auto enter_stage = [&](int k, int size, auto after) {
         barrier_after<decltype(after)::value>();
-        if (!kRowsB || rows == kStageK<T>) return;  // uniform
+        if (size == kStageK<T>) return;  // uniform
         const u32x4 zero = {0, 0, 0, 0};
         char* at = lds + ((k - first) & 1) * kStage;
-        if (kRowsA)
-            for (int i = rows * OpA::kChunks + tid; i < OpA::kBytes / 16; i += kThreads)
-                *reinterpret_cast<u32x4*>(at + i * 16) = zero;
-        for (int i = rows * OpB::kChunks + tid; i < OpB::kBytes / 16; i += kThreads)
-            *reinterpret_cast<u32x4*>(at + OpA::kBytes + i * 16) = zero;
+        if constexpr (kDual) {  // rows of both operands alike
+            for (int i = tid; i < kStage / 16; i += kThreads)
+                if ((i % 8 ^ OpA::swizzle(i / 8)) < 8 - size / OpA::kPerChunk)
+                    *reinterpret_cast<u32x4*>(at + i * 16) = zero;
+        } else {
+            if (kRowsA)
+                for (int i = size * OpA::kChunks + tid; i < OpA::kBytes / 16; i += kThreads)
+                    *reinterpret_cast<u32x4*>(at + i * 16) = zero;
+            for (int i = size * OpB::kChunks + tid; i < OpB::kBytes / 16; i += kThreads)
+                *reinterpret_cast<u32x4*>(at + OpA::kBytes + i * 16) = zero;
+        }
         __syncthreads();
     };
     u32x4 fa[2][MI], fb[2][2];  // fragments of a step and of the next
@@ -434,14 +453,14 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
         for (int j = 0; j < 2; ++j) fb[to][j] = OpB::read(sa + OpA::kBytes, wn * 2 + j, s, lane);
     };
     Stage loading = stage_at(first);  // the last stage whose loads are out
-    const int first_rows = rows_of(loading);
+    const int first_size = size_of(loading);
     load_part(loading, 0, 0, LA + LB);
     if (first + 1 < last) {
         advance(loading);
         load_part(loading, 1, 0, LA + LB);
-        enter_stage(first, first_rows, std::integral_constant<int, LA + LB>());
+        enter_stage(first, first_size, std::integral_constant<int, LA + LB>());
     } else {
-        enter_stage(first, first_rows, std::integral_constant<int, 0>());
+        enter_stage(first, first_size, std::integral_constant<int, 0>());
     }
     read_step(first, 0, 0);
     // A stage's loads go out between the MFMAs, half of them in the step before it is entered and
@@ -452,19 +471,26 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int cur = s & 1;
+            const auto mfmas = [&](int i, int j) {
+                mfma_step(static_cast<const T*>(nullptr), fb[cur][j], fa[cur][i], acc[i][j]);
+            };
+            // the first MFMA waits for fragments that were read during the step before; the next reads go
+            // out behind it, or it would wait for them too (777 x 1000 -> 2603 in fp32, backward: 288
+            // us so, 280 this way)
+            mfmas(0, 0);
+            __builtin_amdgcn_sched_barrier(0);
             if (s + 1 < kSteps) {
                 read_step(k, s + 1, cur ^ 1);
             } else if (k + 1 < last) {
-                enter_stage(k + 1, rows_of(loading), std::integral_constant<int, 0>());
+                enter_stage(k + 1, size_of(loading), std::integral_constant<int, 0>());
                 read_step(k + 1, 0, cur ^ 1);
             }
             if (s + 1 == kSteps && k + 2 < last) advance(loading);
-            __builtin_amdgcn_sched_barrier(0);  // the reads first, the MFMAs over their latency
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    mfma_step(static_cast<const T*>(nullptr), fb[cur][j], fa[cur][i], acc[i][j]);
+                for (int j = i == 0 ? 1 : 0; j < 2; ++j) mfmas(i, j);
                 if (s + 1 == kSteps && k + 2 < last)
                     load_part(loading, (k - first) & 1, i * kPer, (i + 1) * kPer);
                 if (s == 0 && k > first && k + 1 < last)
@@ -511,7 +537,26 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
                 store_columns<T, VE>(static_cast<T*>(p.c0) + m * p.ldc + shift, n0 + c, cols, raw);
             };
         };
-        if constexpr (KIND == Kind::kGate) {
+        if (p.part != nullptr) {
+            using Part = OutTile<float, CW>;
+            static_assert(BM * CW * sizeof(float) <= kRing * kStage, "fits");
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (j > 0) __syncthreads();
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    float v[16];
+                    values(acc[i][j], v);
+                    Part::put(lds, r0 + i * 32, col, v);
+                }
+                send(Part(), [&](int64_t m, int c, const char* from) {
+                    RawVec<float, 4> raw;
+                    __builtin_memcpy(&raw, from, 16);
+                    float* row = p.part + ((split * 2 + j) * p.M + m) * p.N;
+                    store_columns<float, 4>(row, n0 + c, p.N, raw);
+                });
+            }
+        } else if constexpr (KIND == Kind::kGate) {
             with_act(p.gelu, [&](auto gelu) {
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
@@ -585,13 +630,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
             send(Tile(), to(p.hp, p.hp));
             if constexpr (kLow) {
                 if (p.with_low) {  // uniform
-                    const auto rest = [](float v) {
-                        const float r = v - bf16lo(pack_bf16(v, 0.0f));
-                        return r == r ? r : 0.0f;  // of an infinity nothing
-                    };
-                    put_all(dg, rest);
+                    put_all(dg, [](float v) { return rest_of(v); });
                     send(Tile(), to(2 * p.hp, p.hp));
-                    put_all(du, rest);
+                    put_all(du, [](float v) { return rest_of(v); });
                     send(Tile(), to(3 * p.hp, p.hp));
                 }
             }
@@ -771,7 +812,70 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, int splits
     }
 }
 
-// The operands' rows, padded with zeros to whole stages: dst[r][c] = src[r][c] for c < cols, 0 up to
+// What comes of G and U whose stages were split: sums of their parts in order, then as in the product's
+// own epilogue.  Four columns a thread.
+template <typename T, Kind KIND>
+__global__ __launch_bounds__(256) void gate_join_kernel(ProductParams p) {
+    constexpr bool kGrad = KIND == Kind::kGateGrad;
+    const int cols = kGrad ? p.hp : p.N, per = (cols + 3) / 4;
+    const int64_t n = p.M * per;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t m = MSEL_IDX(i / per, p.M);
+        const int c = static_cast<int>(i - m * per) * 4, valid = p.N - c;  // beyond N all is 0
+        float sums[2][4] = {};
+        for (int s = 0; s < p.splits; ++s) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float v[4];
+                to_f32<float, 4>(ld_part<float, 4>(p.part + ((s * 2 + j) * p.M + m) * p.N + c, valid), v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sums[j][e] += v[e];
+            }
+        }
+        T* const out = static_cast<T*>(p.c0) + m * p.ldc + c;
+        const auto put = [&](int shift, const float (&v)[4]) {
+            const RawVec<T, 4> raw = from_f32<T, 4>(v);
+            if constexpr (kGrad)
+                st_raw<T, 4>(out + shift, raw);
+            else
+                st_part<T, 4>(out, raw, valid);
+        };
+        with_act(p.gelu, [&](auto gelu) {
+            if constexpr (!kGrad) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = act_of<gelu.value>(sums[0][e]) * sums[1][e];
+                put(0, v);
+            } else {
+                float d[4], g[4], u[4];
+                to_f32<T, 4>(ld_part<T, 4>(static_cast<const T*>(p.dout) + m * p.N + c, valid), d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v, slope;
+                    act_grad<gelu.value>(sums[0][e], v, slope);
+                    g[e] = d[e] * sums[1][e] * slope;
+                    u[e] = d[e] * v;
+                }
+                put(0, g);
+                put(p.hp, u);
+                if constexpr (sizeof(T) == 2) {
+                    if (p.with_low) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            g[e] = rest_of(g[e]);
+                            u[e] = rest_of(u[e]);
+                        }
+                        put(2 * p.hp, g);
+                        put(3 * p.hp, u);
+                    }
+                }
+            }
+        });
+    }
+}
+
+// The operands' rows, padded with zeros to whole chunks of 16 bytes: dst[r][c] = src[r][c] for c < cols, 0 up to
 // ldd; one operand per blockIdx.y.
 struct PadParams {
     const void* src[3];
@@ -813,7 +917,8 @@ struct ProductPlan {
 // of the peak that such tiles reach (below, fitted to measured products), but a stage takes no less
 // than the way of its loads, which the blocks that a CU holds share; then a fixed part per block, and
 // for split stages the parts' way through the last-level cache.  16384 x 768 by 4096: 256 x 256
-// without a split 140 us, 128 x 128 162; 1024 rows: 8 parts 20 us, one 60.
+// without a split 140 us, 128 x 128 162; 1024 rows: 8 parts 20 us, one 60; forward, 181 x 2880 -> 64 in
+// fp32: split 19 us, not split 103.
 ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf16,
                          int first_tile = 0) {
     constexpr int rows_of[] = {256, 128, 64}, cols_of[] = {256, 128, 128}, held[] = {1, 2, 3};
@@ -826,7 +931,7 @@ ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf
         const int64_t tiles = over(M, rows_of[t]) * over(cols, cols_of[t]);
         const double area = rows_of[t] * cols_of[t];
         const double stage = area * (bf16 ? 64 / 2048.0 / share16[t] : 32 / 128.0 / share32[t]);
-        for (int s = 1; s <= (dual(kind) ? 1 : 16) && (s == 1 || stages / s >= 4); ++s) {
+        for (int s = 1; s <= 16 && (s == 1 || stages / s >= 4); ++s) {
             const int64_t turns = over(tiles * s, kCus), full = turns / held[t];
             const int rest = static_cast<int>(turns % held[t]);
             const double a_stage = full * std::max(held[t] * stage, kLoads) +
@@ -871,6 +976,20 @@ hipError_t launch_product(const ProductParams& p, const ProductPlan& q, hipStrea
     }
 }
 
+// Those of G and U: their parts in `part`, then what comes of their sums.
+template <typename T, Kind KIND>
+hipError_t launch_gate(ProductParams p, const ProductPlan& q, float* part, hipStream_t stream) {
+    if (q.splits == 1) return launch_product<T, KIND>(p, q, stream);
+    p.part = part;
+    p.splits = q.splits;
+    const hipError_t e = launch_product<T, KIND>(p, q, stream);
+    if (e != hipSuccess) return e;
+    const int64_t units = p.M * over(KIND == Kind::kGateGrad ? p.hp : p.N, 4);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(over(units, 256), kMaxBlocks)));
+    hipLaunchKernelGGL((gate_join_kernel<T, KIND>), grid, dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
 // A product whose stages may be split: its parts in `part`, then their sum.
 template <typename T, Kind KIND>
 hipError_t launch_split(ProductParams p, const ProductPlan& q, float* part, hipStream_t stream) {
@@ -892,14 +1011,15 @@ constexpr int64_t kFew = 4096;
 
 // Parts of the workspace: offsets in bytes, absent parts take none.
 struct MlpSpace {
-    int64_t dp, hp;  // width and hidden width in whole stages
+    int64_t dp, hp;  // rows of the operands (whole chunks, at least a stage), the hidden width in stages
     size_t x = 0, wg = 0, wu = 0, dgu = 0, part = 0, all = 0;
     int parts_of = 1;  // bf16 numbers that dG and dU are held in, each
     ProductPlan gate, input, weights;
     MlpSpace(const MlpParams& p, bool bf16, bool bwd) {
         const size_t elem = bf16 ? 2 : 4;
         const int64_t q = kStageBytes / static_cast<int64_t>(elem);
-        dp = over(p.D, q) * q;
+        const int64_t chunk = 16 / static_cast<int64_t>(elem);
+        dp = p.D < q ? q : over(p.D, chunk) * chunk;
         hp = over(p.F, q) * q;
         const auto take = [&](size_t bytes) {
             const size_t at = all;
@@ -913,21 +1033,26 @@ struct MlpSpace {
         }
         if (bwd && bf16 && p.M * std::min(p.D, p.F) <= kFew) parts_of = 2;
         gate = plan_product(bwd ? Kind::kGateGrad : Kind::kGate, p.M, 2 * (bwd ? hp : p.F),
-                            static_cast<int>(dp / q), bf16, parts_of > 1 ? 1 : 0);
-        if (!bwd) return;
+                            static_cast<int>(over(dp, q)), bf16, parts_of > 1 ? 1 : 0);
+        size_t parts = 0;  // of one product at a time
+        if (gate.splits > 1) parts = static_cast<size_t>(gate.splits) * 2 * p.M * p.F;
+        if (!bwd) {
+            part = take(parts * sizeof(float));
+            return;
+        }
         dgu = take(static_cast<size_t>(p.M * 2 * parts_of * hp) * elem);
         input = plan_product(Kind::kInput, p.M, p.D, static_cast<int>(2 * parts_of * hp / q), bf16);
         weights = plan_product(Kind::kWeights, hp + p.F, p.D,
                                static_cast<int>(parts_of * over(p.M, q)), bf16);
-        size_t parts = 0;  // of one product at a time
-        if (input.splits > 1) parts = static_cast<size_t>(input.splits) * p.M * p.D;
+        if (input.splits > 1)
+            parts = std::max(parts, static_cast<size_t>(input.splits) * p.M * p.D);
         if (weights.splits > 1)
             parts = std::max(parts, static_cast<size_t>(weights.splits) * (hp + p.F) * p.D);
         part = take(parts * sizeof(float));
     }
 };
 
-// The operands with rows of whole stages.
+// The operands with rows of whole chunks, at least a stage.
 struct Padded {
     const void* x;
     const void* wg;
@@ -952,7 +1077,7 @@ ProductParams gate_params(const MlpParams& p, const MlpSpace& w, const Padded& o
     q.M = p.M;
     q.N = p.F;
     q.K = w.dp;
-    q.stages = q.half = static_cast<int>(w.dp / kStageK<T>);
+    q.stages = q.half = static_cast<int>(over(w.dp, kStageK<T>));
     q.lda = q.ldb = w.dp;
     q.a = o.x;
     q.b0 = o.wg;
@@ -995,7 +1120,8 @@ hipError_t forward(const MlpParams& p, hipStream_t stream) {
     ProductParams q = gate_params<T>(p, w, padded<T>(p, w, stream));
     q.c0 = p.out;
     q.ldc = p.F;
-    return launch_product<T, Kind::kGate>(q, w.gate, stream);
+    return launch_gate<T, Kind::kGate>(
+        q, w.gate, reinterpret_cast<float*>(static_cast<char*>(p.ws) + w.part), stream);
 }
 
 template <typename T>
@@ -1010,7 +1136,7 @@ hipError_t backward(const MlpParams& p, hipStream_t stream) {
     q.hp = static_cast<int>(w.hp);
     q.with_low = w.parts_of > 1;
     q.dout = p.dout;
-    hipError_t e = launch_product<T, Kind::kGateGrad>(q, w.gate, stream);
+    hipError_t e = launch_gate<T, Kind::kGateGrad>(q, w.gate, part, stream);
     if (e != hipSuccess) return e;
     if (p.dx != nullptr) {
         ProductParams r{};

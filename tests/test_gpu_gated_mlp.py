@@ -228,3 +228,14 @@ def test_long_sums_in_fp32(tokens):
     g = X @ G.T
     ref = g * torch.sigmoid(g) * (X @ U.T)
     assert float((out.double() - ref).norm() / ref.norm()) <= 14 * U32
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(50, 2048, 130), (200, 1000, 70), (90, 1032, 65), (60, 777, 33),
+                                   (130, 4096, 5), (5, 900, 700)])
+def test_long_rows_of_few_columns(shape, dtype, act):
+    """So few tiles that both projections' sums are split over blocks, with whole and partial last
+    stages, and hidden widths that no vector divides."""
+    test_forward(shape, dtype, act)
+    test_backward(shape, dtype, act)
