@@ -13,7 +13,8 @@
 // same elements and the activation and the product need no exchange.
 // The MFMA's rows are C's columns, so that a lane holds consecutive columns of a row of C.  The
 // backward's products over the hidden width and over the tokens read their operands by rows of k, as
-// they lie in memory; LDS turns them (the transposing reads of gfx950).
+// they lie in memory; LDS turns them (the transposing reads of gfx950), and their bf16 stages come
+// through registers.
 //
 // Operands whose rows are no multiple of 16 bytes, or below a stage, are copied into padded rows first.
 #include <hip/hip_runtime.h>
@@ -258,6 +259,11 @@ __device__ __forceinline__ void barrier_after() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// What this wavefront wrote to LDS and read from it has arrived, and the others' has.
+__device__ __forceinline__ void barrier_of_lds() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // WM x WN wavefronts, each MI x 2 MFMA tiles of 32 x 32: a block computes WM MI 32 rows by
 // WN 64 columns (in the fused products WN 32 columns of both weights).
 template <typename T, int WM, int WN, int MI, Kind KIND>
@@ -270,6 +276,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     using OpB = Operand<T, BN, kRowsB, true>;
     constexpr int LA = OpA::kBytes / 16 / kThreads, LB = OpB::kBytes / 16 / kThreads;
     constexpr int kStage = OpA::kBytes + OpB::kBytes;
+    // bf16 operands by rows of k: the compiler lets no transposing read pass a load that goes to LDS
+    // (each waited for all of them), so that such stages come through registers: dx of 16384 x 768 ->
+    // 2048 145 us before, 116 so, the weights' gradients 136 and 112
+    constexpr bool kHeld = sizeof(T) == 2 && !kDual;
     constexpr int CW = kDual ? BN / 2 : BN;  // columns of C
     static_assert(LA * kThreads * 16 == OpA::kBytes && LB * kThreads * 16 == OpB::kBytes,
                   "whole rounds");
@@ -284,9 +294,13 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
 
     // this thread's chunks of the first stage.  Rows and columns past the end repeat the last ones
     // (their results are not stored); rows of k past the end are zeroed in LDS.
-    const char* src[LA + LB];
+    // By rows of k a thread's chunks are the same columns of rows kRoundA or kRoundB apart: one address.
+    constexpr int kRoundA = kThreads / OpA::kChunks, kRoundB = kThreads / OpB::kChunks;
+    static_assert(kRoundA % 8 == 0 && kRoundB % 8 == 0, "the swizzle is that of the first row");
+    constexpr int SA = kRowsA ? 1 : LA, SB = kRowsB ? 1 : LB;
+    const char* src[SA + SB];
 #pragma unroll
-    for (int i = 0; i < LA; ++i) {
+    for (int i = 0; i < SA; ++i) {
         const int at = i * kThreads + tid, r = at / OpA::kChunks;
         const int chunk = (at % OpA::kChunks) ^ OpA::swizzle(r);
         const T* a = static_cast<const T*>(p.a);
@@ -299,22 +313,25 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
         }
     }
 #pragma unroll
-    for (int i = 0; i < LB; ++i) {
+    for (int i = 0; i < SB; ++i) {
         const int at = i * kThreads + tid, r = at / OpB::kChunks;
         const int chunk = (at % OpB::kChunks) ^ OpB::swizzle(r);
         const T* b = static_cast<const T*>(p.b0);
         if constexpr (kRowsB) {
             const int64_t c = min<int64_t>(n0 + chunk * OpB::kPerChunk, p.wb - OpB::kPerChunk);
-            src[LA + i] =
+            src[SA + i] =
                 reinterpret_cast<const char*>(b + r * p.ldb + MSEL_SPAN(c, OpB::kPerChunk, p.wb));
         } else {
             if (r & 32) b = static_cast<const T*>(p.b1);
             const int64_t n = min(n0 + (r >> 6) * 32 + order32(r & 31), p.N - 1);
-            src[LA + i] = reinterpret_cast<const char*>(b + MSEL_IDX(n, p.N) * p.ldb) + chunk * 16;
+            src[SA + i] = reinterpret_cast<const char*>(b + MSEL_IDX(n, p.N) * p.ldb) + chunk * 16;
         }
     }
-    const int64_t step_a = kRowsA ? kStageK<T> * p.lda * static_cast<int64_t>(sizeof(T)) : kStageBytes;
-    const int64_t step_b = kRowsB ? kStageK<T> * p.ldb * static_cast<int64_t>(sizeof(T)) : kStageBytes;
+    const int64_t ld_a = p.lda * static_cast<int64_t>(sizeof(T));
+    const int64_t ld_b = p.ldb * static_cast<int64_t>(sizeof(T));
+    const int64_t step_a = kRowsA ? kStageK<T> * ld_a : kStageBytes;
+    const int64_t step_b = kRowsB ? kStageK<T> * ld_b : kStageBytes;
+    const int64_t round_a = kRoundA * ld_a, round_b = kRoundB * ld_b;
     // where a stage's operands are, in bytes from the first one's, and the rows of k that its part (of
     // up to 4) has from it on
     struct Stage {
@@ -363,22 +380,63 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     const auto size_of = [&](const Stage& g) -> int {
         return g.left < kStageK<T> ? static_cast<int>(g.left) : kStageK<T>;
     };
+    // kHeld: this thread's first chunk of a stage, from the stage's start, which its buffer ends behind
+    // its last row: chunks of rows past the end are read as 0.  The spans of a stage are below 2^32
+    // (256 rows of 2^20 bytes).
+    [[maybe_unused]] u32x4 held[kHeld ? LA + LB : 1];
+    [[maybe_unused]] int from_a = 0, from_b = 0;
+    if constexpr (kHeld) {
+        const int ra = tid / OpA::kChunks, rb = tid / OpB::kChunks;
+        const int ca = (tid % OpA::kChunks ^ OpA::swizzle(ra)) * OpA::kPerChunk;
+        const int cb = (tid % OpB::kChunks ^ OpB::swizzle(rb)) * OpB::kPerChunk;
+        const int64_t a0 = kRowsA ? min(m0 + ca, p.wa - OpA::kPerChunk) : ca;
+        const int64_t b0 = min<int64_t>(n0 + cb, p.wb - OpB::kPerChunk);
+        from_a = static_cast<int>((ra * p.lda + a0) * sizeof(T));
+        from_b = static_cast<int>((rb * p.ldb + b0) * sizeof(T));
+    }
+    const auto buffer_of = [](const void* base, int64_t bytes) {
+        const uint32_t n = bytes < 0xffffffff ? static_cast<uint32_t>(bytes) : 0xffffffffu;
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(n),
+                                                 0x00020000);
+    };
     // loads [i0, i1) of a stage
     const auto load_part = [&](const Stage& stage, int buf, int i0, int i1) {
-        [[maybe_unused]] const int size = size_of(stage);
+        if constexpr (kHeld) {
+            const char* const a = static_cast<const char*>(p.a) + stage.a + (kRowsA ? 0 : m0 * ld_a);
+            const auto from = buffer_of(a, kRowsA ? stage.left * ld_a : (p.M - m0) * ld_a - stage.a);
+            const auto other = buffer_of(static_cast<const char*>(p.b0) + stage.b, stage.left * ld_b);
 #pragma unroll
-        for (int i = 0; i < LA + LB; ++i) {
-            if (i < i0 || i >= i1) continue;
-            const bool a = i < LA;
-            const char* g = src[i] + (a ? stage.a : stage.b);
-            if ((a ? kRowsA : kRowsB) && size < kStageK<T>) {  // uniform
-                const int r = a ? (i * kThreads + tid) / OpA::kChunks
-                                : ((i - LA) * kThreads + tid) / OpB::kChunks;
-                if (r >= size) g -= (r - size + 1) * (a ? p.lda : p.ldb) * static_cast<int64_t>(sizeof(T));
+            for (int i = i0; i < i1; ++i)
+                held[i] = __builtin_bit_cast(
+                    u32x4, i < LA ? __builtin_amdgcn_raw_buffer_load_b128(
+                                        from, from_a + i * static_cast<int>(round_a), 0, 0)
+                                  : __builtin_amdgcn_raw_buffer_load_b128(
+                                        other, from_b + (i - LA) * static_cast<int>(round_b), 0, 0));
+        } else {
+            const int size = size_of(stage);
+            // rows of this thread's first chunks behind the stage's end
+            [[maybe_unused]] const int past_a = tid / OpA::kChunks - size, past_b = tid / OpB::kChunks - size;
+#pragma unroll
+            for (int i = 0; i < LA + LB; ++i) {
+                if (i < i0 || i >= i1) continue;
+                const bool a = i < LA;
+                const char* g = a ? src[kRowsA ? 0 : i] + (stage.a + (kRowsA ? i * round_a : 0))
+                                  : src[SA + (kRowsB ? 0 : i - LA)] +
+                                        (stage.b + (kRowsB ? (i - LA) * round_b : 0));
+                if ((a ? kRowsA : kRowsB) && size < kStageK<T>) {  // uniform
+                    const int past = a ? past_a + i * kRoundA : past_b + (i - LA) * kRoundB;
+                    if (past >= 0) g -= (past + 1) * (a ? ld_a : ld_b);
+                }
+                const int at = buf * kStage + (i * kThreads + wave * 64) * 16;
+                __builtin_amdgcn_global_load_lds((GlobalVoid*)g, (LdsVoid*)(lds + at), 16, 0, 0);
             }
-            const int at = buf * kStage + (i * kThreads + wave * 64) * 16;
-            __builtin_amdgcn_global_load_lds((GlobalVoid*)g, (LdsVoid*)(lds + at), 16, 0, 0);
         }
+    };
+    // kHeld: loads [i0, i1) go to LDS
+    const auto write_part = [&](int buf, int i0, int i1) {
+#pragma unroll
+        for (int i = i0; i < i1; ++i)
+            *reinterpret_cast<u32x4*>(lds + buf * kStage + (i * kThreads + tid) * 16) = held[i];
     };
 
     f32x16 acc[MI][2];
@@ -427,6 +485,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     const int first = split * p.per_split, last = min(p.stages, first + p.per_split);
     // waits for stage k, which has `after` loads behind it; what it has too much becomes 0
     const auto enter_stage = [&](int k, int size, auto after) {
+        if constexpr (kHeld) {
+            barrier_of_lds();
+            return;
+        }
         barrier_after<decltype(after)::value>();
         if (size == kStageK<T>) return;  // uniform
         const u32x4 zero = {0, 0, 0, 0};
@@ -455,7 +517,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     Stage loading = stage_at(first);  // the last stage whose loads are out
     const int first_size = size_of(loading);
     load_part(loading, 0, 0, LA + LB);
-    if (first + 1 < last) {
+    if constexpr (kHeld) {
+        write_part(0, 0, LA + LB);
+        if (first + 1 < last) advance(loading);
+        load_part(loading, 1, 0, LA + LB);
+        enter_stage(first, first_size, std::integral_constant<int, 0>());
+    } else if (first + 1 < last) {
         advance(loading);
         load_part(loading, 1, 0, LA + LB);
         enter_stage(first, first_size, std::integral_constant<int, LA + LB>());
@@ -481,20 +548,32 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
             __builtin_amdgcn_sched_barrier(0);
             if (s + 1 < kSteps) {
                 read_step(k, s + 1, cur ^ 1);
-            } else if (k + 1 < last) {
+            } else if (kHeld || k + 1 < last) {
                 enter_stage(k + 1, size_of(loading), std::integral_constant<int, 0>());
                 read_step(k + 1, 0, cur ^ 1);
             }
-            if (s + 1 == kSteps && k + 2 < last) advance(loading);
+            if (!kHeld && s + 1 == kSteps && k + 2 < last) advance(loading);
+            if (kHeld && s == 0 && k + 2 < last) advance(loading);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
 #pragma unroll
                 for (int j = i == 0 ? 1 : 0; j < 2; ++j) mfmas(i, j);
-                if (s + 1 == kSteps && k + 2 < last)
-                    load_part(loading, (k - first) & 1, i * kPer, (i + 1) * kPer);
-                if (s == 0 && k > first && k + 1 < last)
-                    load_part(loading, (k + 1 - first) & 1, kHalf + i * kPer, kHalf + (i + 1) * kPer);
+                if constexpr (kHeld) {
+                    // stage k + 1 goes to LDS and k + 2 is loaded behind it, half of both in steps 0 and 1
+                    // (past the last stage that one again, to no use)
+                    if (s < 2) {
+                        const int i0 = s * kHalf + i * kPer;
+                        write_part((k + 1 - first) & 1, i0, i0 + kPer);
+                        load_part(loading, 0, i0, i0 + kPer);
+                    }
+                } else {
+                    if (s + 1 == kSteps && k + 2 < last)
+                        load_part(loading, (k - first) & 1, i * kPer, (i + 1) * kPer);
+                    if (s == 0 && k > first && k + 1 < last)
+                        load_part(loading, (k + 1 - first) & 1, kHalf + i * kPer,
+                                  kHalf + (i + 1) * kPer);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
