@@ -111,8 +111,10 @@ __device__ __forceinline__ void add_term(float x, float m, float k2, float& s, f
     w = fmaf(e, fmaxf(d, -200.0f), w);
 }
 
-// The sums moved to stand at m.
+// The sums moved to stand at m.  Rounded as they are written: fused with the first addition of a
+// reduction over lanes, the products would round differently in each of two lanes that add theirs.
 __device__ __forceinline__ void rebase(Sums& a, float m, float k2) {
+#pragma clang fp contract(off)
     const float d = (a.m() - m) * k2;
     const float c = exp2_hw(d);
     a.w = c * fmaf(a.s, fmaxf(d, -200.0f), a.w);
@@ -144,7 +146,7 @@ struct RowOut {
         entropy = dead ? 0.0f : log_s - kLn2 * t.w / t.s;
     }
     __device__ __forceinline__ float logprob(float x, float scale) const {
-        return dead ? -INFINITY : (x - m) * scale - log_s;
+        return dead ? -INFINITY : fmaf(x - m, scale, -log_s);
     }
 };
 

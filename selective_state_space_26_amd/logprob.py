@@ -12,6 +12,7 @@ Layouts, as in include/msel.h:
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -37,6 +38,13 @@ def _strided(t, name):
             raise ValueError(f"the rows of {name} must be strided alike")
         n *= size
     return rows, vocab if step is None else step
+
+
+@functools.lru_cache(maxsize=1024)
+def _need_bytes(rows, vocab, top, code):
+    """Bytes of workspace the forward needs for these sizes."""
+    a = _lib.LogprobArgs(_lib.ABI_VERSION, vocab, rows, vocab, code, 0, top, 1.0)
+    return _lib.load().msel_logprob_fwd_workspace_bytes(ctypes.byref(a))
 
 
 def _args(logits, ids, scale):
@@ -74,7 +82,10 @@ def msel_logprob_fwd(logits, ids=None, scale=1.0, top=0, want_lse=True, want_ent
     dev, shape = logits.device, logits.shape[:-1]
 
     def rows(*more, dtype=torch.float32):
-        return torch.empty(shape + more, device=dev, dtype=dtype)
+        size = (*shape, *more)  # one by one: 0.8 us less than as a torch.Size
+        if not size:
+            return torch.empty((), device=dev, dtype=dtype)
+        return torch.empty(*size, device=dev, dtype=dtype)
     logprob = rows() if ids is not None else None
     lse = rows() if want_lse else None
     entropy = rows() if want_entropy else None
@@ -82,7 +93,7 @@ def msel_logprob_fwd(logits, ids=None, scale=1.0, top=0, want_lse=True, want_ent
     top_logprobs = rows(top) if top > 0 else None
     a.logprob, a.lse, a.entropy = _at(logprob), _at(lse), _at(entropy)
     a.top_ids, a.top_logprobs = _at(top_ids), _at(top_logprobs)
-    need = _lib.load().msel_logprob_fwd_workspace_bytes(ctypes.byref(a))
+    need = _need_bytes(a.rows, a.vocab, a.top, a.dtype)
     workspace, size = _workspace(workspace, need, dev)
     _call("msel_logprob_fwd", dev, ctypes.byref(a), _at(workspace), size)
     return {"logprob": logprob, "lse": lse, "entropy": entropy, "top_ids": top_ids,
@@ -103,7 +114,7 @@ def msel_logprob_bwd(logits, ids, lse, dlogprob=None, dlse=None, dentropy=None, 
         _need(t, name, shape, torch.float32, dev)
     a.lse, a.entropy = lse.data_ptr(), _at(entropy)
     if dlogits is None:
-        dlogits = torch.empty(logits.shape, device=dev, dtype=logits.dtype)
+        dlogits = torch.empty(*logits.shape, device=dev, dtype=logits.dtype)
         dstride = a.vocab
     else:
         if not isinstance(dlogits, torch.Tensor):

@@ -20,10 +20,14 @@ from .norm import _at, _handle
 from .scan import _dtype_code, _int32, _need, _workspace, num_chunks
 
 
+# the current device's index without torch.cuda's checks around it, where this build of PyTorch has it
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _call(fn, dev, *args):
     """The library's entry point on the current stream of the tensors' device."""
     call = getattr(_lib.load(), fn)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         code = call(*args, _handle(dev))
     else:
         with torch.cuda.device(dev):
@@ -46,13 +50,13 @@ def _args(x, gate_a, gate_x, lam, h0):
     if dev.type != "cuda":
         raise ValueError("tensors must be on the GPU")
     code = _dtype_code(dt)
-    bsz, dim, L = x.shape
+    shape = bsz, dim, L = x.shape
     for name, t in (("gate_a", gate_a), ("gate_x", gate_x), ("lam", lam)):
         if t is None:
             raise TypeError(f"{name} must be a torch.Tensor")
-    _need(x, "x", x.shape, dt, dev)
-    _need(gate_a, "gate_a", x.shape, dt, dev)
-    _need(gate_x, "gate_x", x.shape, dt, dev)
+    _need(x, "x", shape, dt, dev)
+    _need(gate_a, "gate_a", shape, dt, dev)
+    _need(gate_x, "gate_x", shape, dt, dev)
     _need(lam, "lam", (dim,), torch.float32, dev)
     _need(h0, "h0", (bsz, dim), torch.float32, dev)
     return _lib.LruArgs(_lib.ABI_VERSION, _int32(bsz, "batch"), _int32(dim, "dim"),
@@ -71,16 +75,16 @@ def msel_lru_fwd(x, gate_a, gate_x, lam, h0=None, return_final_state=True,
     chunk_states or None): out holds every h_t, chunk_states what msel_lru_bwd starts from.  A
     given final_state may be h0 itself, which is then updated in place."""
     a = _args(x, gate_a, gate_x, lam, h0)
-    dev, (bsz, dim, L) = x.device, x.shape
+    dev, bsz, dim, L = x.device, a.batch, a.dim, a.seqlen
     out = torch.empty_like(x) if out is None else _need(out, "out", x.shape, x.dtype, dev)
     if final_state is not None:
         _need(final_state, "final_state", (bsz, dim), torch.float32, dev)
     elif return_final_state:
-        final_state = torch.empty((bsz, dim), device=dev, dtype=torch.float32)
+        final_state = torch.empty(bsz, dim, device=dev, dtype=torch.float32)
     if chunk_states is not None:
         _need(chunk_states, "chunk_states", (bsz, dim, num_chunks(L)), torch.float32, dev)
     elif return_chunk_states:
-        chunk_states = torch.empty((bsz, dim, num_chunks(L)), device=dev, dtype=torch.float32)
+        chunk_states = torch.empty(bsz, dim, num_chunks(L), device=dev, dtype=torch.float32)
     a.out, a.final_state, a.chunk_states = out.data_ptr(), _at(final_state), _at(chunk_states)
     need = _need_bytes("msel_lru_fwd_workspace_bytes", bsz, dim, L, a.dtype, False)
     workspace, size = _workspace(workspace, need, dev)
@@ -102,8 +106,8 @@ def msel_lru_bwd(x, gate_a, gate_x, lam, dout, h0=None, dfinal_state=None, chunk
     _need(chunk_states, "chunk_states", (bsz, dim, num_chunks(L)), torch.float32, dev)
     a.chunk_states = _at(chunk_states)
     dx, dga, dgx = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
-    dlam = torch.empty((dim,), device=dev, dtype=torch.float32) if want_dlam else None
-    dh0 = torch.empty((bsz, dim), device=dev, dtype=torch.float32) if want_dh0 else None
+    dlam = torch.empty(dim, device=dev, dtype=torch.float32) if want_dlam else None
+    dh0 = torch.empty(bsz, dim, device=dev, dtype=torch.float32) if want_dh0 else None
     g = _lib.LruGrads(dout.data_ptr(), _at(dfinal_state), dx.data_ptr(), dga.data_ptr(),
                       dgx.data_ptr(), _at(dlam), _at(dh0))
     need = _need_bytes("msel_lru_bwd_workspace_bytes", bsz, dim, L, a.dtype,
