@@ -995,9 +995,10 @@ struct ProductPlan {
 // The cheapest by a model in cycles: the blocks of a CU take turns on its matrix cores, at the share
 // of the peak that such tiles reach (below, fitted to measured products), but a stage takes no less
 // than the way of its loads, which the blocks that a CU holds share; then a fixed part per block, and
-// for split stages the parts' way through the last-level cache.  16384 x 768 by 4096: 256 x 256
-// without a split 140 us, 128 x 128 162; 1024 rows: 8 parts 20 us, one 60; forward, 181 x 2880 -> 64 in
-// fp32: split 19 us, not split 103.
+// for split stages the join's launch (a call's second one in the forward) and the parts' way through the
+// last-level cache.  dG and dU of 16384 x 768 -> 2048: 256 x 256 158 us, 128 x 128 185.  Backward of
+// 1024 x 768 -> 2048: dx alone 38 us, its sums not split 49; forward of 181 x 2880 -> 64 in fp32: 19 us,
+// not split 103.
 ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf16,
                          int first_tile = 0) {
     constexpr int rows_of[] = {256, 128, 64}, cols_of[] = {256, 128, 128}, held[] = {1, 2, 3};
@@ -1016,7 +1017,7 @@ ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf
             const double a_stage = full * std::max(held[t] * stage, kLoads) +
                                    (rest > 0 ? std::max(rest * stage, kLoads) : 0.0);
             double cost = over(stages, s) * a_stage + turns * (1000.0 + area / 12.0);
-            if (s > 1) cost += 4000.0 + static_cast<double>(s) * M * cols * 8 / 6000.0;
+            if (s > 1) cost += (dual(kind) ? 18000.0 : 12000.0) + static_cast<double>(s) * M * cols * 8 / 6000.0;
             if (least == 0.0 || cost < least) {
                 least = cost;
                 best = {t, s};
@@ -1165,9 +1166,14 @@ ProductParams gate_params(const MlpParams& p, const MlpSpace& w, const Padded& o
     return q;
 }
 
-// Tokens that the skinny kernel takes (2048 -> 5632 in bf16: 10 us for 1 token, 13 for 16, 18.5 for
-// 32, 24 for 48, and the tiles take 22 for each of them; in fp32 61 for 48, the tiles 79).
-constexpr int64_t skinny_tokens(bool bf16) { return bf16 ? 32 : 48; }
+// Whether the skinny kernel takes a call: up to 16 tokens, and up to 32 (48 in fp32) where the weights
+// are small, where the launch of the parts' join would show (768 -> 2048 in bf16: 10 us for 32 tokens,
+// the tiles 14; 2048 -> 5632: 11.5 for 8, 13 for 16, 19 for 32, the tiles 15.5, 16 and 17; 4096 -> 8192: 30
+// for 16, 44 for 32, the tiles 27 and 28).
+bool is_skinny(const MlpParams& p, bool bf16) {
+    const int64_t weights = int64_t(2) * p.D * p.F * (bf16 ? 2 : 4);
+    return p.M <= 16 || (p.M <= (bf16 ? 32 : 48) && weights <= int64_t(32) << 20);
+}
 
 template <typename T>
 hipError_t forward_skinny(const MlpParams& p, hipStream_t stream) {
@@ -1186,7 +1192,7 @@ hipError_t forward_skinny(const MlpParams& p, hipStream_t stream) {
         case 1: hipLaunchKernelGGL((skinny_kernel<T, 1>), grid, block, 0, stream, q); break;
         case 2: hipLaunchKernelGGL((skinny_kernel<T, 2>), grid, block, 0, stream, q); break;
         default:
-            if constexpr (skinny_tokens(sizeof(T) == 2) > 32)
+            if constexpr (sizeof(T) == 4)
                 hipLaunchKernelGGL((skinny_kernel<T, 3>), grid, block, 0, stream, q);
     }
     return hipGetLastError();
@@ -1194,7 +1200,7 @@ hipError_t forward_skinny(const MlpParams& p, hipStream_t stream) {
 
 template <typename T>
 hipError_t forward(const MlpParams& p, hipStream_t stream) {
-    if (p.M <= skinny_tokens(sizeof(T) == 2)) return forward_skinny<T>(p, stream);
+    if (is_skinny(p, sizeof(T) == 2)) return forward_skinny<T>(p, stream);
     const MlpSpace w(p, sizeof(T) == 2, false);
     ProductParams q = gate_params<T>(p, w, padded<T>(p, w, stream));
     q.c0 = p.out;
@@ -1259,7 +1265,7 @@ hipError_t backward(const MlpParams& p, hipStream_t stream) {
 }  // namespace
 
 size_t mlp_fwd_workspace_bytes(const MlpParams& p, bool bf16) {
-    if (p.M <= skinny_tokens(bf16)) return 0;
+    if (is_skinny(p, bf16)) return 0;
     return MlpSpace(p, bf16, false).all;
 }
 

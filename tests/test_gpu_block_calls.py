@@ -83,6 +83,8 @@ CASES = {
     "mlp_odd": lambda: _mlp(333, 205, 311, "bf16"),
     "mlp_odd_f32": lambda: _mlp(190, 77, 300, "f32", "gelu"),
     "mlp_split": lambda: _mlp(900, 128, 1024, "bf16"),
+    "mlp_long_rows": lambda: _mlp(200, 1000, 70, "bf16"),
+    "mlp_long_rows_f32": lambda: _mlp(130, 4096, 5, "f32", "gelu"),
     "mlp_wide": lambda: _mlp(4500, 256, 2100, "bf16"),
     "mlp_wide_f32": lambda: _mlp(4300, 64, 2200, "f32"),
 }
@@ -106,7 +108,7 @@ def test_in_range_and_twice_alike(name):
 
 
 GRAPHS = ["lru_step", "lru_lane", "lru_rows", "lru_4_waves", "lru_segments", "logprob_4x1",
-          "logprob_slices", "logprob_wide_top", "mlp_few", "mlp_odd", "mlp_split"]
+          "logprob_slices", "logprob_wide_top", "mlp_few", "mlp_odd", "mlp_split", "mlp_long_rows"]
 
 
 @pytest.mark.parametrize("name", GRAPHS)
