@@ -85,13 +85,43 @@ __device__ __forceinline__ void suffix16(float& P, float& S) {
                  : [P] "+v"(P), [S] "+v"(S));
 }
 
+// The same over 4 or 8 lanes of 16: a pair is composed with the one that lies a shift away, where the
+// team has a lane there.
+template <int SHIFT>
+__device__ __forceinline__ void compose_from(float& P, float& S, bool has) {
+    const float p = dpp<SHIFT, 0xf>(P, P), s = dpp<SHIFT, 0xf>(S, S);
+    S = has ? fmaf(P, s, S) : S;
+    P = has ? P * p : P;
+}
+template <int TEAM>
+__device__ __forceinline__ void scan_part(float& P, float& S) {
+    const int l = lane_id() % TEAM;
+    compose_from<kRowShr1>(P, S, l >= 1);
+    compose_from<kRowShr2>(P, S, l >= 2);
+    if constexpr (TEAM == 8) compose_from<kRowShr4>(P, S, l >= 4);
+}
+template <int TEAM>
+__device__ __forceinline__ void suffix_part(float& P, float& S) {
+    const int l = TEAM - 1 - lane_id() % TEAM;
+    compose_from<kRowShl1>(P, S, l >= 1);
+    compose_from<kRowShl2>(P, S, l >= 2);
+    if constexpr (TEAM == 8) compose_from<kRowShl4>(P, S, l >= 4);
+}
+
 // The state that enters each lane, from the lanes' own pairs (P, S) and the state h that enters
-// the team (1, 16 or 64 lanes); h becomes the one that leaves it (in every lane).
+// the team (1, 4, 8, 16 or 64 lanes); h becomes the one that leaves it (in every lane).
 template <int TEAM>
 __device__ __forceinline__ float enter_forward(float P, float S, float& h) {
     if constexpr (TEAM == 1) {
         const float in = h;
         h = fmaf(P, h, S);
+        return in;
+    } else if constexpr (TEAM < 16) {
+        scan_part<TEAM>(P, S);
+        const float before = fmaf(dpp<kRowShr1, 0xf>(P, P), h, dpp<kRowShr1, 0xf>(S, S));
+        const float in = lane_id() % TEAM == 0 ? h : before;
+        const float out = fmaf(P, h, S);
+        h = __shfl(out, lane_id() | (TEAM - 1));
         return in;
     } else if constexpr (TEAM == 16) {
         scan16(P, S);
@@ -147,6 +177,13 @@ __device__ __forceinline__ float enter_backward(float P, float S, float& e) {
     if constexpr (TEAM == 1) {
         const float in = e;
         e = fmaf(P, e, S);
+        return in;
+    } else if constexpr (TEAM < 16) {
+        suffix_part<TEAM>(P, S);
+        const float behind = fmaf(dpp<kRowShl1, 0xf>(P, P), e, dpp<kRowShl1, 0xf>(S, S));
+        const float in = lane_id() % TEAM == TEAM - 1 ? e : behind;
+        const float out = fmaf(P, e, S);
+        e = __shfl(out, lane_id() & -TEAM);
         return in;
     } else if constexpr (TEAM == 16) {
         suffix16(P, S);
@@ -304,7 +341,7 @@ __global__ __launch_bounds__(256) void lru_summary_kernel(LruParams p) {
     }
 }
 
-// The forward.  A team of 1, 16 or 64 lanes, or of several wavefronts, per row, or a wavefront per
+// The forward.  A team of 1 to 64 lanes, or of several wavefronts, per row, or a wavefront per
 // segment of a row when there are several (their pairs known).  out may be null (states only).
 // PAST: out is stored past the caches.
 template <typename T, int TEAM, bool PAST>
@@ -528,9 +565,9 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void lru_bwd_kernel(LruPar
         if (p.dlam_part != nullptr) {
             if constexpr (TEAM >= 64) {
                 dlam = wave_sum_fused(dlam);
-            } else if constexpr (TEAM == 16) {
+            } else {
 #pragma unroll
-                for (int k = 8; k > 0; k /= 2) dlam += __shfl_xor(dlam, k);
+                for (int k = TEAM / 2; k > 0; k /= 2) dlam += __shfl_xor(dlam, k);
             }
             if constexpr (kBlock) {
                 if (lane_id() == 0) sums[wave] = dlam;
@@ -550,7 +587,8 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void lru_bwd_kernel(LruPar
 
 }  // namespace
 
-// Teams: a lane for a row of up to 8 steps, 16 lanes up to 128, then wavefronts.  A wavefront a row
+// Teams: as few of 1, 4, 8, 16 and 64 lanes as hold a row, 8 steps each (41 x 3992 rows of 14 in bf16,
+// forward and backward: 13 and 26 us, 39 and 76 with 16 lanes).  Above 512 steps a wavefront a row
 // where there are rows enough; four, whose loads are one stretch of 4 KB, where many rows fill their
 // tiles of 2048 steps (12288 x 2048 bf16, forward and backward: 107 us, 110 with one) or where fewer
 // rows than that leave wavefronts wanting (1536 x 16384: 109, 130); sixteen (eight in the backward,
@@ -565,6 +603,8 @@ LruPlan lru_plan(int64_t rows, int L, bool bwd) {
     const int most = bwd ? 512 : 1024;
     if (L <= kStep) {
         q.team = 1;
+    } else if (L <= 8 * kStep) {
+        q.team = L <= 4 * kStep ? 4 : 8;
     } else if (L <= 16 * kStep) {
         q.team = 16;
     } else if (q.tiles == 1) {
@@ -630,6 +670,8 @@ hipError_t forward(LruParams p, hipStream_t stream) {
     const bool past = past_cache(rows * p.L * static_cast<int64_t>(sizeof(T)));
     switch (q.team) {
         case 1: launch_fwd<T, 1>(p, past, units, stream); break;
+        case 4: launch_fwd<T, 4>(p, past, units, stream); break;
+        case 8: launch_fwd<T, 8>(p, past, units, stream); break;
         case 16: launch_fwd<T, 16>(p, past, units, stream); break;
         case 64: launch_fwd<T, 64>(p, past, units, stream); break;
         case 256: launch_fwd<T, 256>(p, past, units, stream); break;
@@ -653,6 +695,8 @@ hipError_t backward(LruParams p, hipStream_t stream) {
     const bool past = past_cache(3 * rows * p.L * static_cast<int64_t>(sizeof(T)));
     switch (q.team) {
         case 1: launch_bwd<T, 1>(p, past, units, stream); break;
+        case 4: launch_bwd<T, 4>(p, past, units, stream); break;
+        case 8: launch_bwd<T, 8>(p, past, units, stream); break;
         case 16: launch_bwd<T, 16>(p, past, units, stream); break;
         case 64: launch_bwd<T, 64>(p, past, units, stream); break;
         case 256: launch_bwd<T, 256>(p, past, units, stream); break;

@@ -58,6 +58,8 @@ CASES = {
     "lru_step": lambda: _lru((5, 70, 1), "bf16"),
     "lru_lane": lambda: _lru((3, 50, 7), "f32"),
     "lru_16": lambda: _lru((3, 50, 99), "bf16"),
+    "lru_4": lambda: _lru((3, 50, 21), "bf16"),
+    "lru_8": lambda: _lru((3, 50, 61), "f32"),
     "lru_wave": lambda: _lru((2, 50, 400), "f32", chunks=False),
     "lru_rows": lambda: _lru((3, 700, 530), "bf16"),
     "lru_full_tiles": lambda: _lru((8, 1024, 2048), "bf16"),

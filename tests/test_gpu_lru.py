@@ -190,3 +190,13 @@ def test_blocks_of_a_row(shape, dtype):
     for k, r in (("dx", "dx"), ("dgate_a", "dga"), ("dgate_x", "dgx"), ("dlam", "dlam"),
                  ("dh0", "dh0")):
         within(k, got[k], ref[r], ref[r + "_err"])
+
+
+@pytest.mark.parametrize("carried", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(5, 70, 14), (3, 41, 25), (7, 50, 32), (3, 70, 33), (2, 50, 50),
+                                   (3, 37, 64), (2, 9, 65), (9, 31, 17)])
+def test_short_rows(shape, dtype, carried):
+    """Rows that 4, 8 or 16 lanes hold, in part and whole, with teams left over in the last block."""
+    test_forward(shape, dtype, carried)
+    test_backward(shape, dtype, carried)
