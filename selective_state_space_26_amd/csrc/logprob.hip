@@ -710,6 +710,15 @@ Narrow narrow_of(int V, bool bf16) {
     return {0, 0};
 }
 
+// Whether a narrow row's many likeliest tokens are found by a block all the same: teams take a pass over
+// their registers per token, a block ranks what reaches its bound, or the whole of a short row.  A bound
+// needs lanes with columns in all 4 wavefronts.  256 rows, 64 tokens: of 250 columns 12 us, teams 47; of
+// 2000 in bf16 12, 79; but of 500, with two wavefronts empty, 22, 38 for 64 and 15 for 20 tokens.  Many
+// rows fill the chip with teams: 4096 of 250 take 58 us by blocks, 48 by teams.
+bool top_by_block(int64_t rows, int V, int top, bool bf16) {
+    return top > 16 && rows <= 1024 && (V <= 256 || V >= 224 * (bf16 ? 8 : 4));
+}
+
 // Slices of a row: enough blocks for the chip, of about 4096 columns at least, no more than a
 // wavefront joins and than the joined keys' list holds.  The last slice has V / n - 64 (n - 1)
 // columns or more, which for up to n = 48 is above 1000, so more than kMaxTop.
@@ -758,7 +767,8 @@ template <typename T>
 hipError_t forward(LogprobParams p, hipStream_t stream) {
     const dim3 block(kThreads);
     const Narrow narrow = narrow_of(p.V, sizeof(T) == 2);
-    if (narrow.team != 0) return launch_narrow<T>(p, narrow, false, stream);
+    if (narrow.team != 0 && !top_by_block(p.rows, p.V, p.top, sizeof(T) == 2))
+        return launch_narrow<T>(p, narrow, false, stream);
     slice_rows(p.rows, p.V, p.top, kFwdBlocks, p.slices, p.slice);
     const dim3 grid = grid_for(p.rows * p.slices);
     if (p.slice <= kHeld && p.top > 0)

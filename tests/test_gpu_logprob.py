@@ -255,3 +255,11 @@ def test_scales_at_the_ends_of_fp32(vocab, scale):
         for k, v in (("logprob", -lse), ("lse", lse), ("entropy", lse)):
             assert (r[k].double().cpu() - v).abs().max() < 2 ** -24 * (vocab / 256 + 40 + 4 * lse)
         assert torch.isfinite(d).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(3, 17), (5, 250), (900, 256), (1030, 200), (4, 500), (600, 897),
+                                   (6, 1800), (1025, 1000)])
+def test_many_likeliest_tokens_of_narrow_rows(shape, dtype):
+    """Up to 64 tokens, where a block takes a narrow row for them and where teams do."""
+    test_forward(shape, dtype, 1.0)
