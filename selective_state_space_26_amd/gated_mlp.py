@@ -10,6 +10,7 @@ Layouts, as in include/msel.h, all float32 or all bfloat16, contiguous:
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -19,6 +20,13 @@ from .norm import _at, _rows
 from .scan import _dtype_code, _int32, _need, _workspace
 
 _ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+@functools.lru_cache(maxsize=1024)
+def _need_bytes(fn, dim, hidden, code, tokens):
+    """Bytes of workspace for these sizes."""
+    a = _lib.GatedMlpArgs(_lib.ABI_VERSION, dim, hidden, code, tokens, 0, 0)
+    return getattr(_lib.load(), fn)(ctypes.byref(a))
 
 
 def _args(x, w_gate, w_up, activation):
@@ -47,7 +55,7 @@ def msel_gated_mlp_fwd(x, w_gate, w_up, activation="silu", out=None, workspace=N
     dev = x.device
     out = x.new_empty(shape) if out is None else _need(out, "out", shape, x.dtype, dev)
     a.out = out.data_ptr()
-    need = _lib.load().msel_gated_mlp_fwd_workspace_bytes(ctypes.byref(a))
+    need = _need_bytes("msel_gated_mlp_fwd_workspace_bytes", a.dim, a.hidden, a.dtype, a.tokens)
     workspace, size = _workspace(workspace, need, dev)
     _call("msel_gated_mlp_fwd", dev, ctypes.byref(a), _at(workspace), size)
     return out
@@ -66,7 +74,7 @@ def msel_gated_mlp_bwd(x, w_gate, w_up, dout, activation="silu", want_dx=True,
     dwg, dwu = ((torch.empty_like(w_gate), torch.empty_like(w_up)) if want_dweights
                 else (None, None))
     g = _lib.GatedMlpGrads(dout.data_ptr(), _at(dx), _at(dwg), _at(dwu))
-    need = _lib.load().msel_gated_mlp_bwd_workspace_bytes(ctypes.byref(a))
+    need = _need_bytes("msel_gated_mlp_bwd_workspace_bytes", a.dim, a.hidden, a.dtype, a.tokens)
     workspace, size = _workspace(workspace, need, dev)
     _call("msel_gated_mlp_bwd", dev, ctypes.byref(a), ctypes.byref(g), _at(workspace), size)
     return {"dx": dx, "dw_gate": dwg, "dw_up": dwu}
