@@ -239,3 +239,33 @@ def test_long_rows_of_few_columns(shape, dtype, act):
     stages, and hidden widths that no vector divides."""
     test_forward(shape, dtype, act)
     test_backward(shape, dtype, act)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(200, 1000, 70), (60, 1032, 65), (40, 777, 130), (300, 72, 520),
+                                   (700, 200, 1100)])
+def test_what_is_not_finite_stays_where_it_belongs(shape, dtype, bad):
+    """A token that is not finite changes nothing in the other tokens' rows, and a hidden unit's weights
+    nothing in the other units' columns and gradients, at sizes with partial tiles, stages and parts:
+    what pads them must not meet it."""
+    log(f"mlp not finite {shape} {dtype} {bad}")
+    m, d, f = shape
+    x, wg, wu = _inputs(shape, dtype)
+    dout = normal((m, f), dtype, 4)
+    out = msel.msel_gated_mlp_fwd(x, wg, wu)
+    clean = msel.msel_gated_mlp_bwd(x, wg, wu, dout)
+    for token in (0, m - 1):
+        y = x.clone()
+        y[token, d - 1] = bad
+        others = torch.arange(m, device="cuda") != token
+        assert torch.equal(msel.msel_gated_mlp_fwd(y, wg, wu)[others], out[others])
+        assert torch.equal(msel.msel_gated_mlp_bwd(y, wg, wu, dout)["dx"][others], clean["dx"][others])
+    for unit in (0, f - 1):
+        w = wg.clone()
+        w[unit, d - 1] = bad
+        others = torch.arange(f, device="cuda") != unit
+        assert torch.equal(msel.msel_gated_mlp_fwd(x, w, wu)[:, others], out[:, others])
+        g = msel.msel_gated_mlp_bwd(x, w, wu, dout, want_dx=False)
+        for k in ("dw_gate", "dw_up"):
+            assert torch.equal(g[k][others], clean[k][others]), k
