@@ -6,17 +6,17 @@
 // stages of 128 bytes of k in turn, loaded without a register between (global_load_lds).  A step's
 // fragments are read from LDS during the MFMAs of the step before, across the stages' borders too:
 // a stage's place is loaded again as soon as its last fragments have been read, before they are
-// used.  A row of a stage is 8 chunks of 16 bytes, chunk c of row r at place c ^ (r / 2 & 7): the 16
-// lanes that LDS serves together read one chunk of 16 rows, which then cover all 64 banks.  The
-// result goes out through LDS too, in whole rows of the tile.  In the fused product the
-// B rows of a wavefront are 32 rows of Wg and the same 32 of Wu, so that a lane holds G and U of the
-// same elements and the activation and the product need no exchange.
-// The MFMA's rows are C's columns, so that a lane holds consecutive columns of a row of C.  The
-// backward's products over the hidden width and over the tokens read their operands by rows of k, as
-// they lie in memory; LDS turns them (the transposing reads of gfx950), and their bf16 stages come
-// through registers.
+// used.  A row of a stage is 8 chunks of 16 bytes, chunk c of row r at place c ^ (r / 2 & 7): the
+// 16 lanes that LDS serves together read one chunk of 16 rows, which then cover all 64 banks.  The
+// result goes out through LDS too, in whole rows of the tile.  In the fused product the B rows of a
+// wavefront are 32 rows of Wg and the same 32 of Wu, so that a lane holds G and U of the same
+// elements and the activation and the product need no exchange. The MFMA's rows are C's columns, so
+// that a lane holds consecutive columns of a row of C.  The backward's products over the hidden
+// width and over the tokens read their operands by rows of k, as they lie in memory; LDS turns them
+// (the transposing reads of gfx950), and their bf16 stages come through registers.
 //
-// Operands whose rows are no multiple of 16 bytes, or below a stage, are copied into padded rows first.
+// Operands whose rows are no multiple of 16 bytes, or below a stage, are copied into padded rows
+// first.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -34,9 +34,9 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kStageBytes = 128;  // of k per stage
 constexpr int kRing = 2;          // stages in LDS
 constexpr int kSteps = kStageBytes / 32;
-// fp32: stages whose products are summed before their sum is added to another.  An MFMA adds 2 products
-// and rounds, and a row of 2048 such steps was off by up to 2.4 times as much as parts of 256 are (2
-// tokens of 1998: 1.1e-6 of the result).  They cost 0.5% of a product's time.
+// fp32: stages whose products are summed before their sum is added to another.  An MFMA adds 2
+// products and rounds, and a row of 2048 such steps was off by up to 2.4 times as much as parts of
+// 256 are (2 tokens of 1998: 1.1e-6 of the result).  They cost 0.5% of a product's time.
 constexpr int kPartStages = 16;
 
 template <typename T>
@@ -118,9 +118,9 @@ struct ProductParams {
     int tm, tn;        // tiles
 };
 
-// The tile of a block and its part of the stages: consecutive tiles on one XCD, in bands of 8 tiles of
-// rows, so that the blocks that run together share rows of both operands in its L2 (in a grid that
-// gives each part to all XCDs, 61% of the L2's reads missed).
+// The tile of a block and its part of the stages: consecutive tiles on one XCD, in bands of 8 tiles
+// of rows, so that the blocks that run together share rows of both operands in its L2 (in a grid
+// that gives each part to all XCDs, 61% of the L2's reads missed).
 __device__ __forceinline__ bool tile_at(const ProductParams& p, int& m, int& n, int& part) {
     const int64_t tiles = static_cast<int64_t>(p.tm) * p.tn, all = tiles * p.splits;
     const int64_t bid = blockIdx.y * static_cast<int64_t>(gridDim.x) + blockIdx.x;
@@ -151,7 +151,8 @@ __device__ __forceinline__ int order32(int i) {
 // An operand of W rows (or columns of C's side) per stage in LDS, by chunks of 16 bytes.
 //
 // Consecutive k: [W][8 chunks], chunk c of row r at place c ^ (r / 2 & 7): two rows are as long as
-// the 64 banks, and the 16 lanes that LDS serves together read one chunk of 16 rows.  ORDER: rows in the order order32.
+// the 64 banks, and the 16 lanes that LDS serves together read one chunk of 16 rows.  ORDER: rows
+// in the order order32.
 //
 // By rows of k: [rows of k][W columns].  bf16 fragments are read with the transposing read, which
 // gives each lane of 16 the 4 values of its column from 4 rows of 16 columns; two such groups read
@@ -208,9 +209,9 @@ struct Operand {
     }
 };
 
-// A tile of C on its way out: BM rows of W columns of type U in LDS, in chunks of 16 bytes, swizzled
-// so that 16 rows of one chunk (a wavefront writes them) and a row's chunks (it reads them) both
-// cover all banks.
+// A tile of C on its way out: BM rows of W columns of type U in LDS, in chunks of 16 bytes,
+// swizzled so that 16 rows of one chunk (a wavefront writes them) and a row's chunks (it reads
+// them) both cover all banks.
 template <typename U, int W>
 struct OutTile {
     static constexpr int kPerChunk = 16 / static_cast<int>(sizeof(U));
@@ -276,9 +277,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     using OpB = Operand<T, BN, kRowsB, true>;
     constexpr int LA = OpA::kBytes / 16 / kThreads, LB = OpB::kBytes / 16 / kThreads;
     constexpr int kStage = OpA::kBytes + OpB::kBytes;
-    // bf16 operands by rows of k: the compiler lets no transposing read pass a load that goes to LDS
-    // (each waited for all of them), so that such stages come through registers: dx of 16384 x 768 ->
-    // 2048 145 us before, 116 so, the weights' gradients 136 and 112
+    // bf16 operands by rows of k: the compiler lets no transposing read pass a load that goes to
+    // LDS (each waited for all of them), so that such stages come through registers: dx of 16384 x
+    // 768 -> 2048 145 us before, 116 so, the weights' gradients 136 and 112
     constexpr bool kHeld = sizeof(T) == 2 && !kDual;
     constexpr int CW = kDual ? BN / 2 : BN;  // columns of C
     static_assert(LA * kThreads * 16 == OpA::kBytes && LB * kThreads * 16 == OpB::kBytes,
@@ -294,7 +295,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
 
     // this thread's chunks of the first stage.  Rows and columns past the end repeat the last ones
     // (their results are not stored); rows of k past the end are zeroed in LDS.
-    // By rows of k a thread's chunks are the same columns of rows kRoundA or kRoundB apart: one address.
+    // By rows of k a thread's chunks are the same columns of rows kRoundA or kRoundB apart: one
+    // address.
     constexpr int kRoundA = kThreads / OpA::kChunks, kRoundB = kThreads / OpB::kChunks;
     static_assert(kRoundA % 8 == 0 && kRoundB % 8 == 0, "the swizzle is that of the first row");
     constexpr int SA = kRowsA ? 1 : LA, SB = kRowsB ? 1 : LB;
@@ -332,8 +334,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     const int64_t step_a = kRowsA ? kStageK<T> * ld_a : kStageBytes;
     const int64_t step_b = kRowsB ? kStageK<T> * ld_b : kStageBytes;
     const int64_t round_a = kRoundA * ld_a, round_b = kRoundB * ld_b;
-    // where a stage's operands are, in bytes from the first one's, and the rows of k that its part (of
-    // up to 4) has from it on
+    // where a stage's operands are, in bytes from the first one's, and the rows of k that its part
+    // (of up to 4) has from it on
     struct Stage {
         int64_t a, b, left;
         int part;
@@ -347,8 +349,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
         }
         g.left = p.K;
     };
-    // the last stage of rows of consecutive k ends with the rows: what it has in common with the one
-    // before becomes 0 in LDS
+    // the last stage of rows of consecutive k ends with the rows: what it has in common with the
+    // one before becomes 0 in LDS
     const auto end_row = [&](Stage& g) {
         if (g.left < kStageK<T>) g.a = g.b = p.K * static_cast<int64_t>(sizeof(T)) - kStageBytes;
     };
@@ -380,9 +382,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     const auto size_of = [&](const Stage& g) -> int {
         return g.left < kStageK<T> ? static_cast<int>(g.left) : kStageK<T>;
     };
-    // kHeld: this thread's first chunk of a stage, from the stage's start, which its buffer ends behind
-    // its last row: chunks of rows past the end are read as 0.  The spans of a stage are below 2^32
-    // (256 rows of 2^20 bytes).
+    // kHeld: this thread's first chunk of a stage, from the stage's start, which its buffer ends
+    // behind its last row: chunks of rows past the end are read as 0.  The spans of a stage are
+    // below 2^32 (256 rows of 2^20 bytes).
     [[maybe_unused]] u32x4 held[kHeld ? LA + LB : 1];
     [[maybe_unused]] int from_a = 0, from_b = 0;
     if constexpr (kHeld) {
@@ -446,8 +448,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    // fp32: the sums of the stages before the last kPartStages (the largest tiles have no registers for
-    // them)
+    // fp32: the sums of the stages before the last kPartStages (the largest tiles have no registers
+    // for them)
     constexpr bool kParts = sizeof(T) == 4 && MI < 4;
     f32x16 sum[kParts ? MI : 1][2];
     const auto add_part = [&](bool first_one) {
@@ -541,9 +543,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
             const auto mfmas = [&](int i, int j) {
                 mfma_step(static_cast<const T*>(nullptr), fb[cur][j], fa[cur][i], acc[i][j]);
             };
-            // the first MFMA waits for fragments that were read during the step before; the next reads go
-            // out behind it, or it would wait for them too (777 x 1000 -> 2603 in fp32, backward: 288
-            // us so, 280 this way)
+            // the first MFMA waits for fragments that were read during the step before; the next
+            // reads go out behind it, or it would wait for them too (777 x 1000 -> 2603 in fp32,
+            // backward: 288 us so, 280 this way)
             mfmas(0, 0);
             __builtin_amdgcn_sched_barrier(0);
             if (s + 1 < kSteps) {
@@ -560,8 +562,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
 #pragma unroll
                 for (int j = i == 0 ? 1 : 0; j < 2; ++j) mfmas(i, j);
                 if constexpr (kHeld) {
-                    // stage k + 1 goes to LDS and k + 2 is loaded behind it, half of both in steps 0 and 1
-                    // (past the last stage that one again, to no use)
+                    // stage k + 1 goes to LDS and k + 2 is loaded behind it, half of both in steps
+                    // 0 and 1 (past the last stage that one again, to no use)
                     if (s < 2) {
                         const int i0 = s * kHalf + i * kPer;
                         write_part((k + 1 - first) & 1, i0, i0 + kPer);
@@ -891,8 +893,8 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, int splits
     }
 }
 
-// What comes of G and U whose stages were split: sums of their parts in order, then as in the product's
-// own epilogue.  Four columns a thread.
+// What comes of G and U whose stages were split: sums of their parts in order, then as in the
+// product's own epilogue.  Four columns a thread.
 template <typename T, Kind KIND>
 __global__ __launch_bounds__(256) void gate_join_kernel(ProductParams p) {
     constexpr bool kGrad = KIND == Kind::kGateGrad;
@@ -954,8 +956,8 @@ __global__ __launch_bounds__(256) void gate_join_kernel(ProductParams p) {
     }
 }
 
-// The operands' rows, padded with zeros to whole chunks of 16 bytes: dst[r][c] = src[r][c] for c < cols, 0 up to
-// ldd; one operand per blockIdx.y.
+// The operands' rows, padded with zeros to whole chunks of 16 bytes: dst[r][c] = src[r][c] for c <
+// cols, 0 up to ldd; one operand per blockIdx.y.
 struct PadParams {
     const void* src[3];
     void* dst[3];
@@ -992,13 +994,13 @@ struct ProductPlan {
     int splits;
 };
 
-// The cheapest by a model in cycles: the blocks of a CU take turns on its matrix cores, at the share
-// of the peak that such tiles reach (below, fitted to measured products), but a stage takes no less
-// than the way of its loads, which the blocks that a CU holds share; then a fixed part per block, and
-// for split stages the join's launch (a call's second one in the forward) and the parts' way through the
-// last-level cache.  dG and dU of 16384 x 768 -> 2048: 256 x 256 158 us, 128 x 128 185.  Backward of
-// 1024 x 768 -> 2048: dx alone 38 us, its sums not split 49; forward of 181 x 2880 -> 64 in fp32: 19 us,
-// not split 103.
+// The cheapest by a model in cycles: the blocks of a CU take turns on its matrix cores, at the
+// share of the peak that such tiles reach (below, fitted to measured products), but a stage takes
+// no less than the way of its loads, which the blocks that a CU holds share; then a fixed part per
+// block, and for split stages the join's launch (a call's second one in the forward) and the parts'
+// way through the last-level cache.  dG and dU of 16384 x 768 -> 2048: 256 x 256 158 us, 128 x 128
+// 185.  Backward of 1024 x 768 -> 2048: dx alone 38 us, its sums not split 49; forward of 181 x
+// 2880 -> 64 in fp32: 19 us, not split 103.
 ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf16,
                          int first_tile = 0) {
     constexpr int rows_of[] = {256, 128, 64}, cols_of[] = {256, 128, 128}, held[] = {1, 2, 3};
@@ -1084,9 +1086,9 @@ hipError_t launch_split(ProductParams p, const ProductPlan& q, float* part, hipS
     return hipGetLastError();
 }
 
-// Gradients of so few elements take dG and dU in two bf16 parts each, as good as unrounded: over few
-// elements the roundings do not average out (1 x 160 -> 4792: dx is off by 1.65 times what its own
-// rounding is, by 1.41 times in large ones).  8 x 768 -> 2048: 36 us, 29 with one part.
+// Gradients of so few elements take dG and dU in two bf16 parts each, as good as unrounded: over
+// few elements the roundings do not average out (1 x 160 -> 4792: dx is off by 1.65 times what its
+// own rounding is, by 1.41 times in large ones).  4 x 768 -> 2048: 36 us, 29 with one part.
 constexpr int64_t kFew = 4096;
 
 // Parts of the workspace: offsets in bytes, absent parts take none.
@@ -1166,10 +1168,10 @@ ProductParams gate_params(const MlpParams& p, const MlpSpace& w, const Padded& o
     return q;
 }
 
-// Whether the skinny kernel takes a call: up to 16 tokens, and up to 32 (48 in fp32) where the weights
-// are small, where the launch of the parts' join would show (768 -> 2048 in bf16: 10 us for 32 tokens,
-// the tiles 14; 2048 -> 5632: 11.5 for 8, 13 for 16, 19 for 32, the tiles 15.5, 16 and 17; 4096 -> 8192: 30
-// for 16, 44 for 32, the tiles 27 and 28).
+// Whether the skinny kernel takes a call: up to 16 tokens, and up to 32 (48 in fp32) where the
+// weights are small, where the launch of the parts' join would show (768 -> 2048 in bf16: 10 us for
+// 32 tokens, the tiles 14; 2048 -> 5632: 11.5 for 8, 13 for 16, 19 for 32, the tiles 15.5, 16 and
+// 17; 4096 -> 8192: 30 for 16, 44 for 32, the tiles 27 and 28).
 bool is_skinny(const MlpParams& p, bool bf16) {
     const int64_t weights = int64_t(2) * p.D * p.F * (bf16 ? 2 : 4);
     return p.M <= 16 || (p.M <= (bf16 ? 32 : 48) && weights <= int64_t(32) << 20);

@@ -10,12 +10,13 @@
 // HBM bounds it: one read forward, one read and one write backward, against about 12 and 14 VALU
 // slots per element, 4 of them the exp.
 //
-// The likeliest tokens, by value and then by index: about the k / 4-th largest of a wavefront's lane
-// maxima is reached by k / 4 of its elements, so that k elements of the block's reach the least of
-// its 4 wavefronts' bounds.  The row's second reading (from the caches, or registers) keeps only the
-// elements at or above it, less than 2 k of them as a rule, and each kept element's rank is counted.
-// (Bounds that k elements of one wavefront reach, the largest of them taken, keep some 5 k of them for
-// k = 20 and 1000 for k = 64.)  Rows with more ties than the list holds are searched once per token.
+// The likeliest tokens, by value and then by index: about the k / 4-th largest of a wavefront's
+// lane maxima is reached by k / 4 of its elements, so that k elements of the block's reach the
+// least of its 4 wavefronts' bounds.  The row's second reading (from the caches, or registers)
+// keeps only the elements at or above it, less than 2 k of them as a rule, and each kept element's
+// rank is counted. (Bounds that k elements of one wavefront reach, the largest of them taken, keep
+// some 5 k of them for k = 20 and 1000 for k = 64.)  Rows with more ties than the list holds are
+// searched once per token.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -422,8 +423,8 @@ __device__ __forceinline__ Sums block_join(const Sums& mine, float k2, Sums* par
     return t;
 }
 
-// The upper half of a key that at least k lanes of the wavefront reach: the k-th largest value's, cut to
-// its sign, exponent and 7 bits.
+// The upper half of a key that at least k lanes of the wavefront reach: the k-th largest value's,
+// cut to its sign, exponent and 7 bits.
 __device__ __forceinline__ uint32_t kth_of_lanes(float v, int k) {
     const uint32_t u = static_cast<uint32_t>(key_of(v, 0) >> 32);
     uint32_t t = 0;
@@ -442,14 +443,16 @@ struct TopList {
     int count;
 };
 
-// The `top` largest keys of columns [c0, c1), handed to put(rank, key); c1 - c0 >= top.  each: calls
-// its argument for this thread's vectors, as each_vector does.  mx: the largest value among them.
+// The `top` largest keys of columns [c0, c1), handed to put(rank, key); c1 - c0 >= top.  each:
+// calls its argument for this thread's vectors, as each_vector does.  mx: the largest value among
+// them.
 template <int VE, typename Each, typename Put>
 __device__ __forceinline__ void block_top(Each each, int c0, int c1, int top, float mx,
                                           TopList& list, Put put) {
     const int wave = threadIdx.x >> 6;
     constexpr int kWaves = kThreads / 64;
-    // for a few the largest bound that all of them reach in one wavefront is as good, with fewer kept
+    // for a few the largest bound that all of them reach in one wavefront is as good, with fewer
+    // kept
     const bool few = top <= kWaves;
     const uint32_t kth = kth_of_lanes(mx, few ? top : (top + kWaves - 1) / kWaves);
     if (lane_id() == 0) list.bound[wave] = kth;
@@ -603,9 +606,9 @@ __global__ __launch_bounds__(kThreads) void held_fwd_kernel(LogprobParams p) {
     }
 }
 
-// The slices of a row joined, a block per row.  Up to kCandidates keys, of which those count that reach
-// the least of the slices' (top / slices)-th keys, as top of them do (64 likeliest of 8 rows of 50257 in
-// fp32: 58 us with all of them ranked).
+// The slices of a row joined, a block per row.  Up to kCandidates keys, of which those count that
+// reach the least of the slices' (top / slices)-th keys, as top of them do (64 likeliest of 8 rows
+// of 50257 in fp32: 58 us with all of them ranked).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void join_kernel(LogprobParams p) {
     const float k2 = base2(p.scale);
@@ -696,7 +699,8 @@ __global__ __launch_bounds__(kThreads) void wide_bwd_kernel(LogprobParams p) {
     }
 }
 
-// ---- plans ---------------------------------------------------------------------------------------
+// ---- plans
+// ---------------------------------------------------------------------------------------
 
 // Lanes and vectors per lane of a narrow row (0 lanes: a wide one).
 struct Narrow {
@@ -710,11 +714,12 @@ Narrow narrow_of(int V, bool bf16) {
     return {0, 0};
 }
 
-// Whether a narrow row's many likeliest tokens are found by a block all the same: teams take a pass over
-// their registers per token, a block ranks what reaches its bound, or the whole of a short row.  A bound
-// needs lanes with columns in all 4 wavefronts.  256 rows, 64 tokens: of 250 columns 12 us, teams 47; of
-// 2000 in bf16 12, 79; but of 500, with two wavefronts empty, 22, 38 for 64 and 15 for 20 tokens.  Many
-// rows fill the chip with teams: 4096 of 250 take 58 us by blocks, 48 by teams.
+// Whether a narrow row's many likeliest tokens are found by a block all the same: teams take a pass
+// over their registers per token, a block ranks what reaches its bound, or the whole of a short
+// row.  A bound needs lanes with columns in all 4 wavefronts.  256 rows, 64 tokens: of 250 columns
+// 12 us, teams 47; of 2000 in bf16 12, 79; but of 500, with two wavefronts empty, 22, 38 for 64 and
+// 15 for 20 tokens.  Many rows fill the chip with teams: 4096 of 250 take 58 us by blocks, 48 by
+// teams.
 bool top_by_block(int64_t rows, int V, int top, bool bf16) {
     return top > 16 && rows <= 1024 && (V <= 256 || V >= 224 * (bf16 ? 8 : 4));
 }

@@ -38,9 +38,9 @@ struct Gates {
 };
 
 // lam2: lam log2 e, so that a = 2^l, l = lam2 r.  1 - a^2 = 1 - e^-q, q = -2 ln 2 l: near q = 0 the
-// difference would cancel, so up to q = 0.3 it is the series q - q^2 / 2! + ... - q^6 / 6! in powers
-// of l, whose first missing term is q^6 / 7! < 1.5e-7 of it; from there on the difference loses at
-// most 2 bits.
+// difference would cancel, so up to q = 0.3 it is the series q - q^2 / 2! + ... - q^6 / 6! in
+// powers of l, whose first missing term is q^6 / 7! < 1.5e-7 of it; from there on the difference
+// loses at most 2 bits.
 __device__ __forceinline__ Gates gates_of(float ga, float gx, float lam2) {
     Gates s;
     s.r = sigmoid_f(ga);
@@ -85,8 +85,8 @@ __device__ __forceinline__ void suffix16(float& P, float& S) {
                  : [P] "+v"(P), [S] "+v"(S));
 }
 
-// The same over 4 or 8 lanes of 16: a pair is composed with the one that lies a shift away, where the
-// team has a lane there.
+// The same over 4 or 8 lanes of 16: a pair is composed with the one that lies a shift away, where
+// the team has a lane there.
 template <int SHIFT>
 __device__ __forceinline__ void compose_from(float& P, float& S, bool has) {
     const float p = dpp<SHIFT, 0xf>(P, P), s = dpp<SHIFT, 0xf>(S, S);
@@ -587,14 +587,14 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void lru_bwd_kernel(LruPar
 
 }  // namespace
 
-// Teams: as few of 1, 4, 8, 16 and 64 lanes as hold a row, 8 steps each (41 x 3992 rows of 14 in bf16,
-// forward and backward: 13 and 26 us, 39 and 76 with 16 lanes).  Above 512 steps a wavefront a row
-// where there are rows enough; four, whose loads are one stretch of 4 KB, where many rows fill their
-// tiles of 2048 steps (12288 x 2048 bf16, forward and backward: 107 us, 110 with one) or where fewer
-// rows than that leave wavefronts wanting (1536 x 16384: 109, 130); sixteen (eight in the backward,
-// for its registers) for very long rows (5120 x 65536 forward: 481, 541 with one or four) and for few
-// (200 x 30011 fp32: 59, 63 with four, 78 in segments).  Below 128 rows those are cut into segments
-// that are composed first (64 x 65536: 44 us, 63 with sixteen).
+// Teams: as few of 1, 4, 8, 16 and 64 lanes as hold a row, 8 steps each (41 x 3992 rows of 14 in
+// bf16, forward and backward: 13 and 26 us, 39 and 76 with 16 lanes).  Above 512 steps a wavefront
+// a row where there are rows enough; four, whose loads are one stretch of 4 KB, where many rows
+// fill their tiles of 2048 steps (12288 x 2048 bf16, forward and backward: 107 us, 110 with one) or
+// where fewer rows than that leave wavefronts wanting (1536 x 16384: 109, 130); sixteen (eight in
+// the backward, for its registers) for very long rows (5120 x 65536 forward: 481, 541 with one or
+// four) and for few (200 x 30011 fp32: 59, 63 with four, 78 in segments).  Below 128 rows those are
+// cut into segments that are composed first (64 x 65536: 44 us, 63 with sixteen).
 LruPlan lru_plan(int64_t rows, int L, bool bwd) {
     LruPlan q{};
     q.tiles = (L + kTile - 1) / kTile;
