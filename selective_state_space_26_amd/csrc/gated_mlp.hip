@@ -36,7 +36,10 @@ constexpr int kRing = 2;          // stages in LDS
 constexpr int kSteps = kStageBytes / 32;
 // fp32: stages whose products are summed before their sum is added to another.  An MFMA adds 2
 // products and rounds, and a row of 2048 such steps was off by up to 2.4 times as much as parts of
-// 256 are (2 tokens of 1998: 1.1e-6 of the result).  They cost 0.5% of a product's time.
+// 256 are (2 tokens of 1998: 1.1e-6 of the result).  They cost 0.5% of a product's time.  Tiles of
+// 256 x 256 have no registers for a second sum: the plan takes them only where no block sums more
+// stages than these (2048 x 4096 -> 8192, forward: 10 u of the result with 128 x 128 and 2080 us,
+// 29 u and 2016 us with 256 x 256 before; 16384 x 512 -> 1024: 268 us with 256 x 256, 280).
 constexpr int kPartStages = 16;
 
 template <typename T>
@@ -448,8 +451,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    // fp32: the sums of the stages before the last kPartStages (the largest tiles have no registers
-    // for them)
+    // fp32: the sums of the stages before the last kPartStages (the largest tiles have no more)
     constexpr bool kParts = sizeof(T) == 4 && MI < 4;
     f32x16 sum[kParts ? MI : 1][2];
     const auto add_part = [&](bool first_one) {
@@ -1014,6 +1016,7 @@ ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf
         const double area = rows_of[t] * cols_of[t];
         const double stage = area * (bf16 ? 64 / 2048.0 / share16[t] : 32 / 128.0 / share32[t]);
         for (int s = 1; s <= 16 && (s == 1 || stages / s >= 4); ++s) {
+            if (!bf16 && t == 0 && over(stages, s) > kPartStages) continue;
             const int64_t turns = over(tiles * s, kCus), full = turns / held[t];
             const int rest = static_cast<int>(turns % held[t]);
             const double a_stage = full * std::max(held[t] * stage, kLoads) +

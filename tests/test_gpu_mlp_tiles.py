@@ -1,0 +1,47 @@
+"""The gated feed-forward block at sizes that take each of its product kernels' tiles, the widest among
+them, against its definition in fp64 on the GPU."""
+import pytest
+
+from helpers import log
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import selective_state_space_26_amd as msel  # noqa: E402
+
+from block_helpers import U32, normal  # noqa: E402
+from mlp_shapes import LONG_F32  # noqa: E402
+
+
+def _inputs(shape, dtype):
+    m, d, f = shape
+    return (normal((m, d), dtype, 1), normal((f, d), dtype, 2, d ** -0.5),
+            normal((f, d), dtype, 3, d ** -0.5), normal((m, f), dtype, 4))
+
+
+@pytest.mark.parametrize("shape", LONG_F32)
+def test_long_sums_in_fp32_at_every_size(shape):
+    """Sums in parts of 512 products whatever the tile.  A part's roundings are 6.5 u of it (256 steps,
+    each u / sqrt 3 of a sum that grows as a random walk), and so of the whole; its up to 32 parts add
+    sqrt(32 / 2) u / sqrt 3 = 2.3 u.  G and U are each off by 6.9 u, their product by 9.8 u, the
+    activation's roundings add 1 or 2; dx and the weights' gradients are sums of such terms (of which the
+    errors add in squares, as the terms) with roundings of their own: sqrt(9.8^2 + 6.9^2) = 12 u of the
+    result's norm.  (In one running sum of 4096 or 16384 products it is 23 to 29.)"""
+    log(f"mlp long fp32 sums {shape}")
+    x, wg, wu, dout = _inputs(shape, "f32")
+    X, G, W, D = (t.double() for t in (x, wg, wu, dout))
+    g, u = X @ G.T, X @ W.T
+    s = torch.sigmoid(g)
+
+    def check(name, got, ref):
+        off = float((got.double() - ref).norm() / ref.norm()) / U32
+        assert off <= 14, (name, off)
+    check("out", msel.msel_gated_mlp_fwd(x, wg, wu), g * s * u)
+    r = msel.msel_gated_mlp_bwd(x, wg, wu, dout)
+    dg, du = D * u * s * (1 + g * (1 - s)), D * g * s
+    check("dx", r["dx"], dg @ G + du @ W)
+    check("dw_gate", r["dw_gate"], dg.T @ X)
+    check("dw_up", r["dw_up"], du.T @ X)
