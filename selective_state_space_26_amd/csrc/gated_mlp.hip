@@ -74,10 +74,11 @@ __device__ __forceinline__ void act_grad(float z, float& v, float& slope) {
     // w is 0 long before the polynomial beside it leaves fp32's range
     slope = GELU ? fmaf(w, kTwoC * fminf(fmaf(0.134145f * z, z, 1.0f), 1e30f), s) : w + s;
 }
-// What a value's rounding to bf16 leaves (nothing of an infinity).
+// What a value's rounding to bf16 leaves: nothing where it became an infinity or a NaN, which stand
+// for the value alone.
 __device__ __forceinline__ float rest_of(float v) {
-    const float r = v - bf16lo(pack_bf16(v, 0.0f));
-    return r == r ? r : 0.0f;
+    const float rounded = bf16lo(pack_bf16(v, 0.0f));
+    return fabsf(rounded) < INFINITY ? v - rounded : 0.0f;
 }
 // f(GELU as a type): one branch around a whole epilogue, not two activations per element.
 template <typename Fn>

@@ -45,3 +45,25 @@ def test_long_sums_in_fp32_at_every_size(shape):
     check("dx", r["dx"], dg @ G + du @ W)
     check("dw_gate", r["dw_gate"], dg.T @ X)
     check("dw_up", r["dw_up"], du.T @ X)
+
+
+@pytest.mark.parametrize("tokens", [1, 20, 70, 4096, 4097])
+@pytest.mark.parametrize("split", [False, True])
+def test_gradients_that_round_to_infinity(tokens, split):
+    """dU = 181^2 2^113, finite in fp32 and above bf16's largest value by more than half a step: it
+    rounds to infinity, whether dG and dU are held in one bf16 number or in two, and so do the sums
+    that it is a term of.  dG = dout U act'(G) is 2^-12 of that: finite.  split: rows so long that both
+    projections' sums are split over blocks."""
+    log(f"mlp gradients beyond bf16 {tokens} {split}")
+    dim = 1032 if split else 1
+    x = torch.zeros((tokens, dim), device="cuda", dtype=torch.bfloat16)
+    wg, wu = (torch.zeros((1, dim), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    dout = torch.zeros((tokens, 1), device="cuda", dtype=torch.bfloat16)
+    x[-1, 0], wg[0, 0], wu[0, 0] = 0.5, 181.0, 2.0 ** -11
+    dout[-1, 0] = 181.0 * 2.0 ** 114
+    r = msel.msel_gated_mlp_bwd(x, wg, wu, dout)
+    # G = 90.5, so that act(G) = G and act'(G) = 1 in fp32; U = 2^-12, dG = 181 2^102
+    assert torch.equal(r["dw_gate"][0, :1], torch.tensor([181.0 * 2.0 ** 101], device="cuda").bfloat16())
+    assert r["dw_up"][0, 0].item() == float("inf")
+    assert r["dx"][-1, 0].item() == float("inf")
+    assert bool((r["dx"][:-1] == 0).all())
