@@ -1279,6 +1279,19 @@ size_t mlp_bwd_workspace_bytes(const MlpParams& p, bool bf16) {
     return MlpSpace(p, bf16, true).all;
 }
 
+void mlp_tiles(int64_t tokens, int dim, int hidden, bool bf16, int* tiles) {
+    MlpParams p{};
+    p.M = tokens;
+    p.D = dim;
+    p.F = hidden;
+    const MlpSpace fwd(p, bf16, false), bwd(p, bf16, true);
+    for (const ProductPlan& q : {is_skinny(p, bf16) ? ProductPlan{-1, 1} : fwd.gate, bwd.gate,
+                                 bwd.input, bwd.weights}) {
+        *tiles++ = q.tile;
+        *tiles++ = q.splits;
+    }
+}
+
 hipError_t launch_mlp_fwd(const MlpParams& p, bool bf16, hipStream_t stream) {
     return bf16 ? forward<bf16_t>(p, stream) : forward<float>(p, stream);
 }

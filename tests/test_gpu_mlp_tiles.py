@@ -12,8 +12,10 @@ if not torch.cuda.is_available():  # pragma: no cover
 
 import selective_state_space_26_amd as msel  # noqa: E402
 
-from block_helpers import U32, normal  # noqa: E402
-from mlp_shapes import LONG_F32  # noqa: E402
+from selective_state_space_26_amd import _lib  # noqa: E402
+
+from block_helpers import DTYPES, U32, U_OUT, normal  # noqa: E402
+from mlp_shapes import LONG_F32, TILES  # noqa: E402
 
 
 def _inputs(shape, dtype):
@@ -67,3 +69,77 @@ def test_gradients_that_round_to_infinity(tokens, split):
     assert r["dw_up"][0, 0].item() == float("inf")
     assert r["dx"][-1, 0].item() == float("inf")
     assert bool((r["dx"][:-1] == 0).all())
+
+
+def _act(g, gelu):
+    """The activation and its slope in fp64."""
+    if not gelu:
+        s = torch.sigmoid(g)
+        return g * s, s * (1 + g * (1 - s))
+    c = (2.0 / torch.pi) ** 0.5
+    s = torch.sigmoid(2 * c * (g + 0.044715 * g ** 3))
+    return g * s, s + g * s * (1 - s) * 2 * c * (1 + 0.134145 * g * g)
+
+
+def _sums(k):
+    return min(k, 8.0 * k ** 0.5) + 2.0
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", TILES)
+def test_every_tile_of_every_product(shape, dtype, act):
+    """Element by element.  A sum of k products in fp32 is off by at most k u of the sum of their
+    magnitudes, 8 sqrt(k) u with a wide margin where the errors are random; |act''| < 1.2; the
+    activation's exponent is off by a few roundings of its size, up to 4 (|g| + |g|^3); dG and dU are
+    rounded to the type of the operands.  Gradients of few elements have a second number each, so twice
+    the terms."""
+    log(f"mlp tiles {shape} {dtype} {act}")
+    x, wg, wu, dout = _inputs(shape, dtype)
+    X, G, W, D = (t.double() for t in (x, wg, wu, dout))
+    g, u = X @ G.T, X @ W.T
+    a, slope = _act(g, act == "gelu")
+    k = _sums(shape[1])
+    eg, eu = k * (X.abs() @ G.abs().T), k * (X.abs() @ W.abs().T)
+    near = 4 * g.abs() + 4 * g.abs() ** 3 + 16
+
+    def check(name, got, want, err):
+        room = U_OUT[got.dtype] * 1.001 * want.abs() + U32 * err
+        worst = float(((got.double() - want).abs() / room).max())
+        assert worst <= 1.0, (name, worst)
+    ea = 1.2 * eg + a.abs() * near
+    check("out", msel.msel_gated_mlp_fwd(x, wg, wu, act), a * u,
+          ea * u.abs() + a.abs() * eu + 4 * (a * u).abs())
+    r = msel.msel_gated_mlp_bwd(x, wg, wu, dout, act)
+    dg, du = D * u * slope, D * a
+    half = U_OUT[DTYPES[dtype]] / U32
+    edg = D.abs() * (u.abs() * (1.2 * eg + near * (slope.abs() + 1)) + slope.abs() * eu) \
+        + half * dg.abs()
+    edu = D.abs() * ea + half * du.abs()
+    k = _sums(4 * shape[2])
+    check("dx", r["dx"], dg @ G + du @ W, edg @ G.abs() + edu @ W.abs()
+          + k * (dg.abs() @ G.abs() + du.abs() @ W.abs()))
+    k = _sums(2 * shape[0])
+    check("dw_gate", r["dw_gate"], dg.T @ X, (edg + k * dg.abs()).T @ X.abs())
+    check("dw_up", r["dw_up"], du.T @ X, (edu + k * du.abs()).T @ X.abs())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", TILES)
+def test_in_range_and_twice_alike(shape, dtype):
+    """The checked build counts no index out of its buffer, and it and a second run give the same
+    bits."""
+    log(f"mlp tiles, checked build {shape} {dtype}")
+    x, wg, wu, dout = _inputs(shape, dtype)
+
+    def run():
+        return dict(out=msel.msel_gated_mlp_fwd(x, wg, wu, "gelu"),
+                    **msel.msel_gated_mlp_bwd(x, wg, wu, dout, "gelu"))
+    with _lib.using(_lib.LIB_CHECKED_PATH):
+        msel.bound_violations()
+        got = run()
+        count, f, line = msel.bound_violations()
+        assert count == 0, f"{count} out-of-range indexes, the first at {f}:{line}"
+    for _ in range(2):
+        for k, v in run().items():
+            assert torch.equal(v, got[k]), k
