@@ -90,8 +90,8 @@ struct MlpParams {
 size_t mlp_fwd_workspace_bytes(const MlpParams& p, bool bf16);
 size_t mlp_bwd_workspace_bytes(const MlpParams& p, bool bf16);
 // Which kernels a call takes, for the tests' choice of sizes: the tile (0: 256 x 256, 1: 128 x 128,
-// 2: 64 x 128, -1: none, the kernel for few tokens) and the splits of the forward's product, then of
-// the backward's three (dG and dU, dx, the weights' gradients).  8 ints.
+// 2: 64 x 128, -1: none, the kernel for few tokens) and the splits of the forward's product, then
+// of the backward's three (dG and dU, dx, the weights' gradients).  8 ints.
 void mlp_tiles(int64_t tokens, int dim, int hidden, bool bf16, int* tiles);
 hipError_t launch_mlp_fwd(const MlpParams& p, bool bf16, hipStream_t stream);
 hipError_t launch_mlp_bwd(const MlpParams& p, bool bf16, hipStream_t stream);

@@ -312,7 +312,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
         const T* a = static_cast<const T*>(p.a);
         if constexpr (kRowsA) {
             const int64_t c = min(m0 + chunk * OpA::kPerChunk, p.wa - OpA::kPerChunk);
-            src[i] = reinterpret_cast<const char*>(a + r * p.lda + MSEL_SPAN(c, OpA::kPerChunk, p.wa));
+            src[i] =
+                reinterpret_cast<const char*>(a + r * p.lda + MSEL_SPAN(c, OpA::kPerChunk, p.wa));
         } else {
             const int64_t m = min(m0 + r, p.M - 1);
             src[i] = reinterpret_cast<const char*>(a + MSEL_IDX(m, p.M) * p.lda) + chunk * 16;
@@ -346,7 +347,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     };
     const auto begin_part = [&](Stage& g) {
         if constexpr (KIND == Kind::kInput)  // A goes on, B is the other weight
-            g.b = (g.part & 1) != 0 ? static_cast<const char*>(p.b1) - static_cast<const char*>(p.b0) : 0;
+            g.b = (g.part & 1) != 0
+                      ? static_cast<const char*>(p.b1) - static_cast<const char*>(p.b0)
+                      : 0;
         if constexpr (KIND == Kind::kWeights) {  // A's low parts, B again
             g.a = g.part * p.low * static_cast<int64_t>(sizeof(T));
             g.b = 0;
@@ -408,20 +411,25 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void product_kernel(ProductParams p
     // loads [i0, i1) of a stage
     const auto load_part = [&](const Stage& stage, int buf, int i0, int i1) {
         if constexpr (kHeld) {
-            const char* const a = static_cast<const char*>(p.a) + stage.a + (kRowsA ? 0 : m0 * ld_a);
-            const auto from = buffer_of(a, kRowsA ? stage.left * ld_a : (p.M - m0) * ld_a - stage.a);
-            const auto other = buffer_of(static_cast<const char*>(p.b0) + stage.b, stage.left * ld_b);
+            const char* const a =
+                static_cast<const char*>(p.a) + stage.a + (kRowsA ? 0 : m0 * ld_a);
+            const char* const b = static_cast<const char*>(p.b0) + stage.b;
+            const auto from_of_a =
+                buffer_of(a, kRowsA ? stage.left * ld_a : (p.M - m0) * ld_a - stage.a);
+            const auto from_of_b = buffer_of(b, stage.left * ld_b);
+            const int to_a = static_cast<int>(round_a), to_b = static_cast<int>(round_b);
 #pragma unroll
             for (int i = i0; i < i1; ++i)
                 held[i] = __builtin_bit_cast(
                     u32x4, i < LA ? __builtin_amdgcn_raw_buffer_load_b128(
-                                        from, from_a + i * static_cast<int>(round_a), 0, 0)
+                                        from_of_a, from_a + i * to_a, 0, 0)
                                   : __builtin_amdgcn_raw_buffer_load_b128(
-                                        other, from_b + (i - LA) * static_cast<int>(round_b), 0, 0));
+                                        from_of_b, from_b + (i - LA) * to_b, 0, 0));
         } else {
             const int size = size_of(stage);
             // rows of this thread's first chunks behind the stage's end
-            [[maybe_unused]] const int past_a = tid / OpA::kChunks - size, past_b = tid / OpB::kChunks - size;
+            [[maybe_unused]] const int past_a = tid / OpA::kChunks - size;
+            [[maybe_unused]] const int past_b = tid / OpB::kChunks - size;
 #pragma unroll
             for (int i = 0; i < LA + LB; ++i) {
                 if (i < i0 || i >= i1) continue;
@@ -808,8 +816,8 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductParams p) {
     };
     const auto product = [&](const RawVec<T, VE>& a, const RawVec<T, VE>& b, f32x4_t& c) {
         if constexpr (sizeof(T) == 2) {
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.w),
-                                                        __builtin_bit_cast(bf16x8, b.w), c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, a.w), __builtin_bit_cast(bf16x8, b.w), c, 0, 0, 0);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -911,8 +919,9 @@ __global__ __launch_bounds__(256) void gate_join_kernel(ProductParams p) {
         for (int s = 0; s < p.splits; ++s) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
+                const float* const from = p.part + ((s * 2 + j) * p.M + m) * p.N + c;
                 float v[4];
-                to_f32<float, 4>(ld_part<float, 4>(p.part + ((s * 2 + j) * p.M + m) * p.N + c, valid), v);
+                to_f32<float, 4>(ld_part<float, 4>(from, valid), v);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sums[j][e] += v[e];
             }
@@ -1023,7 +1032,9 @@ ProductPlan plan_product(Kind kind, int64_t M, int64_t cols, int stages, bool bf
             const double a_stage = full * std::max(held[t] * stage, kLoads) +
                                    (rest > 0 ? std::max(rest * stage, kLoads) : 0.0);
             double cost = over(stages, s) * a_stage + turns * (1000.0 + area / 12.0);
-            if (s > 1) cost += (dual(kind) ? 18000.0 : 12000.0) + static_cast<double>(s) * M * cols * 8 / 6000.0;
+            if (s > 1)
+                cost += (dual(kind) ? 18000.0 : 12000.0) +
+                        static_cast<double>(s) * M * cols * 8 / 6000.0;
             if (least == 0.0 || cost < least) {
                 least = cost;
                 best = {t, s};
@@ -1090,14 +1101,18 @@ hipError_t launch_split(ProductParams p, const ProductPlan& q, float* part, hipS
     return hipGetLastError();
 }
 
-// Gradients of so few elements take dG and dU in two bf16 parts each, as good as unrounded: over
-// few elements the roundings do not average out (1 x 160 -> 4792: dx is off by 1.65 times what its
-// own rounding is, by 1.41 times in large ones).  4 x 768 -> 2048: 36 us, 29 with one part.
+// Up to so many tokens times the smaller width dG and dU are held in two bf16 numbers each, the
+// value rounded and what that left, beyond it in one, as the operands of the next products.  One
+// number leaves results off by 2.33e-3 of their norm at every size, two by 1.66e-3, which is the
+// rounding of the results themselves.  The second one doubles dx's and the weights' products: 4 x
+// 768 -> 2048 29 us, 26 with one, 8 x 2048 -> 5632 59, 50, 16384 x 768 -> 2048 593, 342.  So it is
+// there where launches are most of the call.
 constexpr int64_t kFew = 4096;
 
 // Parts of the workspace: offsets in bytes, absent parts take none.
 struct MlpSpace {
-    int64_t dp, hp;  // rows of the operands (whole chunks, at least a stage), the hidden width in stages
+    // rows of the operands (whole chunks, at least a stage), the hidden width in stages
+    int64_t dp, hp;
     size_t x = 0, wg = 0, wu = 0, dgu = 0, part = 0, all = 0;
     int parts_of = 1;  // bf16 numbers that dG and dU are held in, each
     ProductPlan gate, input, weights;

@@ -16,7 +16,9 @@
 // keeps only the elements at or above it, less than 2 k of them as a rule, and each kept element's
 // rank is counted. (Bounds that k elements of one wavefront reach, the largest of them taken, keep
 // some 5 k of them for k = 20 and 1000 for k = 64.)  Rows with more ties than the list holds are
-// searched once per token.
+// searched once per token, and so are rows whose mask leaves fewer lanes with a token than the
+// bound needs, since all masked columns tie (64 x 50257 fp32 with 40 tokens left, kernels: 20
+// likeliest 43 us, 15 without a mask; 64 likeliest 110).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -407,7 +409,8 @@ __device__ __forceinline__ void add_vector(Sums& t, const V& v, float k2) {
 template <typename T, bool ENTROPY>
 __device__ __forceinline__ Sums thread_sums(const T* row, int c0, int c1, float k2) {
     Sums t{-INFINITY, 0.0f, 0.0f};
-    each_vector<T>(row, c0, c1, [&](const auto& v, int, int, auto) { add_vector<ENTROPY>(t, v, k2); });
+    each_vector<T>(row, c0, c1,
+                   [&](const auto& v, int, int, auto) { add_vector<ENTROPY>(t, v, k2); });
     return t;
 }
 
@@ -563,7 +566,7 @@ __global__ __launch_bounds__(kThreads) void wide_fwd_kernel(LogprobParams p) {
 
 // Slices of up to kHeld columns stay in registers: loaded at once, and read once (64 rows of 50257
 // in fp32 with 20 likeliest tokens: 17 us in two readings).
-constexpr int kHeldCols = 8192, kHeld = kHeldCols - 64;  // 64: what may lie before a line of fp32, bf16
+constexpr int kHeldCols = 8192, kHeld = kHeldCols - 64;  // 64: what may lie before a line
 
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void held_fwd_kernel(LogprobParams p) {
@@ -587,7 +590,8 @@ __global__ __launch_bounds__(kThreads) void held_fwd_kernel(LogprobParams p) {
             for (int i = 0; i < N; ++i) {
                 float v[VE];
                 to_f32<T, VE>(raw[i], v);
-                if (c + i * kRound < c1) fn(v, c + i * kRound, kRound, std::integral_constant<int, 1>());
+                const int col = c + i * kRound;
+                if (col < c1) fn(v, col, kRound, std::integral_constant<int, 1>());
             }
         };
         Sums mine{-INFINITY, 0.0f, 0.0f};
@@ -601,7 +605,8 @@ __global__ __launch_bounds__(kThreads) void held_fwd_kernel(LogprobParams p) {
             for (int k = 0; k < VE; ++k) add_term(v[k], at, k2, mine.s, mine.w);
         });
         const Sums all = block_join(mine, k2, part);
-        finish<T, TOP>(p, row, u, r, c0, c1, mine.max, all, reinterpret_cast<TopList*>(&list), each);
+        finish<T, TOP>(p, row, u, r, c0, c1, mine.max, all, reinterpret_cast<TopList*>(&list),
+                       each);
         __syncthreads();
     }
 }
@@ -655,7 +660,8 @@ __global__ __launch_bounds__(kThreads) void join_kernel(LogprobParams p) {
 }
 
 // A block per (row, slice); slices > 1 only where the gradient goes to memory of its own, since a
-// row that is summed again is read whole before it is written.
+// row that is summed again is read whole before it is written (64 x 50257 fp32: 7.8 us, in place
+// 17; 512 x 50257 bf16: 21 and 22).
 template <typename T, bool PAST>
 __global__ __launch_bounds__(kThreads) void wide_bwd_kernel(LogprobParams p) {
     constexpr int VE = 16 / static_cast<int>(sizeof(T));
@@ -699,8 +705,7 @@ __global__ __launch_bounds__(kThreads) void wide_bwd_kernel(LogprobParams p) {
     }
 }
 
-// ---- plans
-// ---------------------------------------------------------------------------------------
+// ---- plans -------------------------------------------------------------------------------------
 
 // Lanes and vectors per lane of a narrow row (0 lanes: a wide one).
 struct Narrow {
@@ -717,9 +722,11 @@ Narrow narrow_of(int V, bool bf16) {
 // Whether a narrow row's many likeliest tokens are found by a block all the same: teams take a pass
 // over their registers per token, a block ranks what reaches its bound, or the whole of a short
 // row.  A bound needs lanes with columns in all 4 wavefronts.  256 rows, 64 tokens: of 250 columns
-// 12 us, teams 47; of 2000 in bf16 12, 79; but of 500, with two wavefronts empty, 22, 38 for 64 and
-// 15 for 20 tokens.  Many rows fill the chip with teams: 4096 of 250 take 58 us by blocks, 48 by
-// teams.
+// 12 us, teams 46; of 2000 in bf16 12, 78; but of 500, with two wavefronts empty, 21, 37 for 64 and
+// 12 for 17 tokens in fp32, and of 1000 in bf16 60, 51.  Many rows fill the chip with teams: 1024
+// of 250 take 20 us by blocks whatever is asked for, by teams 15, 25 and 46 for 17, 32 and 64
+// tokens; 4096 of 250 60, 15, 25 and 47.  (Wide ones would gain beyond: 4096 of 2000 in bf16 41 us,
+// teams 154, for 64 tokens.)
 bool top_by_block(int64_t rows, int V, int top, bool bf16) {
     return top > 16 && rows <= 1024 && (V <= 256 || V >= 224 * (bf16 ? 8 : 4));
 }

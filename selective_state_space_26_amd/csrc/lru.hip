@@ -588,16 +588,16 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void lru_bwd_kernel(LruPar
 }  // namespace
 
 // Teams: as few of 1, 4, 8, 16 and 64 lanes as hold a row, 8 steps each (41 x 3992 rows of 14 in
-// bf16, forward and backward: 13 and 26 us, 39 and 76 with 16 lanes).  Above 512 steps a wavefront
+// bf16, forward and backward: 14 and 24 us, 39 and 76 with 16 lanes).  Above 512 steps a wavefront
 // a row where there are rows enough; four, whose loads are one stretch of 4 KB, where many rows
 // fill their tiles of 2048 steps (8192 x 4096, forward and backward: bf16 54 and 88 us, 61 and 107
 // with one, fp32 106 and 190, 119 and 222; 12288 x 2048 bf16: 107 us together, 110) or where fewer
-// rows than that leave wavefronts wanting (1536 x 16384 bf16: 41 and 75, 52 and 78); sixteen (eight
-// in the backward, for its registers) for very long rows (5120 x 65536 forward: 481, 541 with one or
-// four) and for up to a row per CU (200 x 30011 bf16: 17 and 25 us, 22 and 31 with four, fp32 22 and
-// 36, 24 and 39; but of 511 x 12000, whose blocks take two turns, fp32 27 and 38, 20 and 34 with
-// four).  Below 128 rows those are cut into segments that are composed first (64 x 65536: 44 us, 63
-// with sixteen).
+// rows than that leave wavefronts wanting (1536 x 16384 bf16: 41 and 75, 52 and 78); sixteen
+// (eight in the backward, for its registers) for very long rows (5120 x 65536 forward: 481, 541
+// with one or four) and for up to a row per CU (200 x 30011 bf16: 17 and 25 us, 22 and 31 with
+// four, fp32 22 and 36, 24 and 39; but of 511 x 12000, whose blocks take two turns, fp32 27 and 38,
+// 20 and 34 with four).  Below 128 rows those are cut into segments that are composed first (64 x
+// 65536: 44 us, 63 with sixteen).
 LruPlan lru_plan(int64_t rows, int L, bool bwd) {
     LruPlan q{};
     q.tiles = (L + kTile - 1) / kTile;

@@ -64,7 +64,9 @@ def msel_gated_mlp_fwd(x, w_gate, w_up, activation="silu", out=None, workspace=N
 def msel_gated_mlp_bwd(x, w_gate, w_up, dout, activation="silu", want_dx=True,
                        want_dweights=True, workspace=None):
     """Gradients of sum(dout * out) for msel_gated_mlp_fwd, forming both projections again.
-    Returns {"dx", "dw_gate", "dw_up"}, in x's dtype (absent ones are None)."""
+    Returns {"dx", "dw_gate", "dw_up"}, in x's dtype (absent ones are None).  In bfloat16 the
+    gradients of the projections are rounded once between the products, to one bfloat16 number or,
+    up to tokens * min(dim, hidden) = 4096, to two."""
     a, shape = _args(x, w_gate, w_up, activation)
     dev = x.device
     if dout is None:
